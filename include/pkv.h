@@ -75,8 +75,10 @@ extern "C" {
 #define PKV_ERR_DECODE_QLEN (1 << 4) /* a sequence below num_decode_seqs whose   */
                                      /* query length is not 1                    */
 #define PKV_ERR_TIMEOUT (1 << 5)     /* an on-chip wait gave up (bounded spin)   */
+#define PKV_ERR_NONFINITE (1 << 6)   /* pkv_write_int8: an infinity or NaN in k  */
+                                     /* or v                                     */
 
-typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype;
+typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2, PKV_INT8 = 3 } pkv_dtype;
 
 /* Shape of the paged KV cache ([book] ch. 6 "Transformation de la disposition
  * mémoire du KV cache": separate K and V caches, each
@@ -85,7 +87,9 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2 } pkv_dtype;
  * ([gpuhub] note under "KV cache manager").
  * Supported: block_size 16, head_size 64 or 128, dtype PKV_BF16, PKV_F32 or
  * PKV_FP8_E4M3 (e4m3 codes; [book] ch. 6 "Matrice de capacités": fp8 cache
- * dtypes), the last through pkv_write_fp8 / pkv_attention_fp8 only. */
+ * dtypes) through pkv_write_fp8 / pkv_attention_fp8 only, PKV_INT8 (codes
+ * with a scale for each block and kv head) through pkv_write_int8 /
+ * pkv_attention_int8 only. */
 typedef struct {
   int32_t num_blocks;
   int32_t block_size;
@@ -290,6 +294,75 @@ int pkv_attention_cascade_fp8(void *out, const void *q, const void *k_cache,
  * batches with chunked-prefill rows (num_decode_seqs given), at most 512
  * chunk rows and a prefix >= 4096 tokens; else 0. */
 int pkv_use_cascade(const pkv_attn_meta *meta, int32_t common_prefix_blocks);
+
+/* INT8 KV cache with a scale for each block of 16 tokens and kv head; no
+ * counterpart in the pages.  K = code * k_scales[block][h] (likewise V), codes
+ * in [-127, 127].  Unlike the e4m3 cache it needs no calibrated scale: the
+ * write makes the scales.
+ *   k_cache, v_cache    int8 [num_blocks, block_size, num_kv_heads, head_size]
+ *   k_scales, v_scales  fp32 [num_blocks, num_kv_heads] (device)
+ * cache->dtype must be PKV_INT8.
+ *
+ * Write: the rows of sequence s (rows query_start_loc[s] ..
+ * query_start_loc[s + 1] - 1 of k and v) are its last tokens, positions
+ * L - q_s .. L - 1 with L = context_lens[s]; position p goes to block
+ * block_tables[s][p / 16], offset p % 16.  The batch is described as for
+ * pkv_attention_int8, by the same arrays and the same meta (num_seqs,
+ * num_tokens, block_table_stride and max_query_len are read).  For each
+ * touched block and kv head, with a = max |x| over the finite elements of the
+ * rows put there by this call:
+ *   want  = max(a / 127, 2^-60)
+ *   scale = want if the call writes the block's offset 0 (the block begins
+ *           anew, whatever it held), else max(scale so far, want)
+ *   code  = x * (1 / scale), rounded to nearest even;
+ * where the scale grew, the codes of the block's earlier tokens become
+ * code * (scale so far / scale), rounded to nearest even (fp32 arithmetic,
+ * divisions rounded to nearest).  So a block's tokens are written in order,
+ * offset 0 first; a scale so far that is not a finite number of at least
+ * 2^-60 counts as 2^-60.  An infinity is stored as the largest code of its
+ * sign and a NaN as zero, and PKV_ERR_NONFINITE is set.  Two sequences that
+ * write into the same block in one call: that block's contents are
+ * unspecified.  Sequences with bad lengths (the conditions and bits of
+ * pkv_attention) and blocks with a bad id are skipped. */
+int pkv_write_int8(const void *k, const void *v, const int32_t *block_tables,
+                   const int32_t *context_lens, const int32_t *query_start_loc,
+                   void *k_cache, void *v_cache, float *k_scales, float *v_scales,
+                   const pkv_cache_desc *cache, const pkv_attn_meta *meta, void *stream);
+
+/* PagedAttention over an INT8 cache: as pkv_attention (lengths, masks, window,
+ * errors, rows left alone) with q and out in bf16.  A scale below 2^-60 (zero
+ * included) counts as 2^-60; scales of blocks that no query sees are not read.
+ * The workspace's size comes from pkv_attention_int8_workspace_size (not from
+ * pkv_attention_workspace_size); it is scratch of one call, so calls that may
+ * overlap, captured graphs included, need one each. */
+size_t pkv_attention_int8_workspace_size(const pkv_cache_desc *cache, const pkv_attn_meta *meta);
+int pkv_attention_int8(void *out, const void *q, const void *k_cache, const void *v_cache,
+                       const int32_t *block_tables, const int32_t *context_lens,
+                       const int32_t *query_start_loc, float scale, const float *k_scales,
+                       const float *v_scales, const pkv_cache_desc *cache,
+                       const pkv_attn_meta *meta, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/* Copies pages between blocks of the same buffers: the device side of
+ * copy-on-write forks and of a pool made smaller (pkv_pool.h:
+ * pkv_pool_fork_request, pkv_pool_resize, pkv_pool_take_copies).  Buffer i is
+ * num_blocks pages of page_bytes[i] bytes, one after the other: a layer's K or
+ * V cache of any dtype, or the scales of an int8 cache; every buffer of every
+ * layer goes in one call.
+ *   buffers, page_bytes  HOST arrays [num_buffers]; each buffer 4-byte aligned
+ *                        and its page a multiple of 4 bytes, at most 2^30
+ *                        (16-byte alignment of both is the fast case).  The
+ *                        buffers do not overlap
+ *   pairs                HOST int32 [num_pairs][2]: (from, to) block ids in
+ *                        [0, num_blocks), else PKV_E_SHAPE and nothing is
+ *                        enqueued
+ * The result is that of copying the pairs one after the other in the order
+ * given: a block may be copied on, or overwritten after it was read (each
+ * such dependence costs a launch of its own).  The host arrays are read
+ * during the call only; a call captured into a CUDA graph replays the pairs it
+ * was captured with. */
+int pkv_copy_blocks(void *const *buffers, const int64_t *page_bytes, int32_t num_buffers,
+                    int32_t num_blocks, const int32_t *pairs, int32_t num_pairs, void *stream);
 
 /* Reads (and, if clear != 0, resets) the current device's error word: the OR
  * of PKV_ERR_* bits raised by kernels since the last clear.  SYNCHRONISES the

@@ -175,7 +175,7 @@ int encode_fn(PFN_cuTensorMapEncodeTiled_v12000* fn) {
 int encode_cache_map(CUtensorMap* map, const void* base, const pkv_cache_desc& c) {
   PFN_cuTensorMapEncodeTiled_v12000 fn;
   if (int st = encode_fn(&fn)) return st;
-  const bool fp8 = c.dtype == PKV_FP8_E4M3;
+  const bool fp8 = c.dtype == PKV_FP8_E4M3 || c.dtype == PKV_INT8;   // one-byte codes
   const cuuint64_t eb = fp8 ? 1 : 2;
   const cuuint64_t row_bytes = static_cast<cuuint64_t>(c.head_size) * eb;
   const CUtensorMapL2promotion promo =
@@ -221,6 +221,7 @@ int encode_query_map(CUtensorMap* map, const void* q, int num_tokens, int num_q_
   return r == CUDA_SUCCESS ? PKV_OK : PKV_E_CUDA;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_cache(const pkv_cache_desc* c) {
@@ -937,6 +938,216 @@ extern "C" int pkv_debug_wait_test(int enable) {
   return PKV_OK;
 }
 
+// ------------------------------------------------------------- int8 caches
+
+namespace pkv {
+namespace {
+
+int check_cache_int8(const pkv_cache_desc* c) {
+  if (c == nullptr) return PKV_E_NULL;
+  if (c->dtype != PKV_INT8) return PKV_E_DTYPE;
+  pkv_cache_desc as_bytes = *c;
+  as_bytes.dtype = PKV_FP8_E4M3;   // the same limits as the other one-byte cache
+  return check_cache(&as_bytes);
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" int pkv_write_int8(const void* k, const void* v, const int32_t* block_tables,
+                              const int32_t* context_lens, const int32_t* query_start_loc,
+                              void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                              const pkv_cache_desc* cache, const pkv_attn_meta* meta,
+                              void* stream) {
+  if (int st = check_cache_int8(cache)) return st;
+  if (int st = check_meta(cache, meta)) return st;
+  if (meta->num_seqs == 0 || meta->num_tokens == 0) return PKV_OK;
+  if (!k || !v || !block_tables || !context_lens || !query_start_loc || !k_cache || !v_cache ||
+      !k_scales || !v_scales)
+    return PKV_E_NULL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(query_start_loc) ||
+      !aligned4(k_scales) || !aligned4(v_scales))
+    return PKV_E_ALIGN;
+  WriteInt8Args a{};
+  a.k = k;
+  a.v = v;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start_loc = query_start_loc;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.bt_stride = meta->block_table_stride;
+  a.num_seqs = meta->num_seqs;
+  a.num_tokens = meta->num_tokens;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.head_size = cache->head_size;
+  a.num_blocks = cache->num_blocks;
+  a.max_query_len = meta->max_query_len;
+  // one row a sequence: its one block; else rows / 16 + 2 a sequence
+  a.num_units = meta->max_query_len == 1
+                    ? meta->num_seqs
+                    : meta->num_tokens / kBlock + 2 * static_cast<int64_t>(meta->num_seqs) + 1;
+  if (a.num_units * cache->num_kv_heads > INT32_MAX) return PKV_E_SHAPE;   // (the grid)
+  int sms;
+  if (int st = device_state(&a.err, &sms)) return st;
+  PKV_TRY(launch_write_int8(a, as_stream(stream)));
+  return PKV_OK;
+}
+
+extern "C" size_t pkv_attention_int8_workspace_size(const pkv_cache_desc* cache,
+                                                    const pkv_attn_meta* meta) {
+  if (check_cache_int8(cache) != PKV_OK || check_meta(cache, meta) != PKV_OK)
+    return static_cast<size_t>(-1);
+  return 0;
+}
+
+extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
+                                  const void* v_cache, const int32_t* block_tables,
+                                  const int32_t* context_lens, const int32_t* query_start_loc,
+                                  float scale, const float* k_scales, const float* v_scales,
+                                  const pkv_cache_desc* cache, const pkv_attn_meta* meta,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  if (int st = check_cache_int8(cache)) return st;
+  if (int st = check_meta(cache, meta)) return st;
+  if (meta->num_seqs == 0 || meta->num_tokens == 0) return PKV_OK;
+  if (cache->num_blocks == 0) return PKV_E_SHAPE;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start_loc ||
+      !k_scales || !v_scales)
+    return PKV_E_NULL;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(query_start_loc) ||
+      !aligned4(k_scales) || !aligned4(v_scales))
+    return PKV_E_ALIGN;
+  (void)workspace;
+  (void)workspace_bytes;
+  int32_t* err;
+  int sms, dev;
+  if (int st = device_state(&err, &sms, &dev)) return st;
+  const cudaStream_t st = as_stream(stream);
+  AttnInt8Args a{};
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start_loc = query_start_loc;
+  a.err = err;
+  a.bt_stride = meta->block_table_stride;
+  a.num_seqs = meta->num_seqs;
+  a.num_tokens = meta->num_tokens;
+  a.num_q_heads = meta->num_q_heads;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.num_blocks = cache->num_blocks;
+  a.max_query_len = meta->max_query_len;
+  a.window = meta->sliding_window;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  PKV_TRY(launch_attention_int8(a, cache->head_size, st));
+  return PKV_OK;
+}
+
+// -------------------------------------------------------------- page copies
+
+namespace pkv {
+namespace {
+
+// The blocks that the pairs of one launch read and write: open addressing
+// over a table four times the pairs a launch holds.
+class PairSet {
+ public:
+  // Whether (from, to) may join the launch: `from` is not written in it, `to`
+  // neither read nor written.
+  bool independent(int from, int to) const {
+    return (flags(from) & kWritten) == 0 && flags(to) == 0;
+  }
+  void add(int from, int to) {
+    mark(from, kRead);
+    mark(to, kWritten);
+  }
+  void clear() { std::fill(flag_, flag_ + kSlots, uint8_t{0}); }
+
+ private:
+  static constexpr int kSlots = 4 * kCopyPairs;   // at most half full
+  static constexpr uint8_t kRead = 1, kWritten = 2;
+  int find(int block) const {
+    unsigned i = (static_cast<uint32_t>(block) * 2654435769u) >> 22;
+    while (flag_[i] != 0 && key_[i] != block) i = (i + 1) % kSlots;
+    return static_cast<int>(i);
+  }
+  uint8_t flags(int block) const { return flag_[find(block)]; }
+  void mark(int block, uint8_t f) {
+    const int i = find(block);
+    key_[i] = block;
+    flag_[i] |= f;
+  }
+  int32_t key_[kSlots];
+  uint8_t flag_[kSlots] = {};
+  static_assert(kSlots == 1 << 10, "the hash keeps the top 10 bits");
+};
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" int pkv_copy_blocks(void* const* buffers, const int64_t* page_bytes,
+                               int32_t num_buffers, int32_t num_blocks, const int32_t* pairs,
+                               int32_t num_pairs, void* stream) {
+  if (num_buffers < 0 || num_blocks < 0 || num_pairs < 0) return PKV_E_SHAPE;
+  if (num_buffers == 0 || num_pairs == 0) return PKV_OK;
+  if (!buffers || !page_bytes || !pairs) return PKV_E_NULL;
+  for (int i = 0; i < num_buffers; ++i) {
+    if (!buffers[i]) return PKV_E_NULL;
+    if (page_bytes[i] < 1 || page_bytes[i] > (int64_t{1} << 30)) return PKV_E_SHAPE;
+    if (!aligned4(buffers[i]) || page_bytes[i] % 4 != 0) return PKV_E_ALIGN;
+  }
+  for (int64_t i = 0; i < 2 * static_cast<int64_t>(num_pairs); ++i)
+    if (pairs[i] < 0 || pairs[i] >= num_blocks) return PKV_E_SHAPE;
+  int32_t* err;
+  int sms;
+  if (int st = device_state(&err, &sms)) return st;
+  const cudaStream_t st = as_stream(stream);
+  CopyArgs a;
+  PairSet set;
+  a.num_pairs = 0;
+  auto flush = [&]() -> int {
+    for (int b0 = 0; b0 < num_buffers; b0 += kCopyBuffers) {
+      a.num_buffers = std::min(kCopyBuffers, num_buffers - b0);
+      uint32_t units = 0;
+      for (int i = 0; i < a.num_buffers; ++i) {
+        CopyBuffer& b = a.buffers[i];
+        b.base = buffers[b0 + i];
+        b.page_bytes = page_bytes[b0 + i];
+        b.unit_begin = units;
+        if (b.page_bytes > kCopyUnit / 2) {
+          b.split = static_cast<int32_t>((b.page_bytes + kCopyUnit - 1) / kCopyUnit);
+          units += static_cast<uint32_t>(a.num_pairs) * b.split;
+        } else {
+          const int per = static_cast<int>(kCopyUnit / b.page_bytes);
+          b.split = -per;
+          units += (a.num_pairs + per - 1) / per;
+        }
+      }
+      PKV_TRY(launch_copy_blocks(a, units, st));
+    }
+    a.num_pairs = 0;
+    set.clear();
+    return PKV_OK;
+  };
+  for (int i = 0; i < num_pairs; ++i) {
+    const int from = pairs[2 * i], to = pairs[2 * i + 1];
+    if (from == to) continue;
+    if (a.num_pairs == kCopyPairs || !set.independent(from, to))
+      if (int e = flush()) return e;
+    a.pairs[a.num_pairs++] = make_int2(from, to);
+    set.add(from, to);
+  }
+  return a.num_pairs > 0 ? flush() : PKV_OK;
+}
+
 extern "C" int pkv_get_error(int32_t* error_bits, int clear) {
   if (error_bits == nullptr) return PKV_E_NULL;
   int32_t* err;
@@ -963,7 +1174,8 @@ extern "C" const char* pkv_status_string(int status) {
     case PKV_E_NULL: return "a required pointer is NULL";
     case PKV_E_DTYPE:
       return "dtype not supported by this call (PKV_F32/PKV_BF16: pkv_write, pkv_attention; "
-             "PKV_FP8_E4M3: pkv_write_fp8, pkv_attention_fp8)";
+             "PKV_FP8_E4M3: pkv_write_fp8, pkv_attention_fp8; "
+             "PKV_INT8: pkv_write_int8, pkv_attention_int8)";
     case PKV_E_SHAPE: return "unsupported or out-of-range shape (block_size 16, head_size 64/128)";
     case PKV_E_GQA: return "num_q_heads is not a multiple of num_kv_heads";
     case PKV_E_WORKSPACE: return "workspace missing or smaller than pkv_attention_workspace_size";

@@ -116,6 +116,14 @@ __device__ __forceinline__ int seq_of_row(const int32_t* qsl, int num_seqs, int 
   return (num_seqs > 0 && __ldg(qsl + lo) <= tok && tok < __ldg(qsl + lo + 1)) ? lo : -1;
 }
 
+// int8 caches: block scales below this (zero included) count as this, so that
+// a block of zeros keeps a scale whose reciprocal and logarithm are finite;
+// NaN stays NaN.
+constexpr float kInt8ScaleFloor = 0x1p-60f;
+__device__ __forceinline__ float int8_scale(float s) {
+  return s < kInt8ScaleFloor ? kInt8ScaleFloor : s;
+}
+
 // Named barrier over `nthreads` threads (a multiple of 32).
 __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

@@ -151,7 +151,73 @@ struct F32Args {
   float scale;
 };
 
+// ---- int8 caches (one fp32 scale per block and kv head)
+
+struct WriteInt8Args {
+  const void* k;                 // bf16 [T, Hkv, D]
+  const void* v;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start_loc;
+  void* k_cache;
+  void* v_cache;
+  float* k_scales;               // [num_blocks, Hkv]
+  float* v_scales;
+  int32_t* err;
+  int64_t bt_stride;
+  int64_t num_units;             // touched blocks at most (one unit each)
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t num_kv_heads;
+  int32_t head_size;
+  int32_t num_blocks;
+  int32_t max_query_len;
+};
+
+struct AttnInt8Args {
+  void* out;                     // bf16 [T, Hq, D]
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scales;
+  const float* v_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start_loc;
+  int32_t* err;
+  int64_t bt_stride;
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t num_blocks;
+  int32_t max_query_len;
+  int32_t window;
+  float scale_log2;
+};
+
+// ---- page copies
+constexpr int kCopyPairs = 256;
+constexpr int kCopyBuffers = 64;
+constexpr int kCopyUnit = 16384;   // bytes a CTA copies
+
+struct CopyBuffer {
+  void* base;
+  int64_t page_bytes;
+  uint32_t unit_begin;       // first CTA of this buffer
+  int32_t split;             // > 0: units a page is cut into; < 0: -(small pages in a unit)
+};
+struct CopyArgs {
+  CopyBuffer buffers[kCopyBuffers];
+  int2 pairs[kCopyPairs];    // (from, to): no block is read and written, or written twice
+  int32_t num_buffers;
+  int32_t num_pairs;
+};
+
 cudaError_t launch_write(const WriteArgs& a, cudaStream_t stream, int num_sms);
+cudaError_t launch_write_int8(const WriteInt8Args& a, cudaStream_t stream);
+cudaError_t launch_attention_int8(const AttnInt8Args& a, int head_size, cudaStream_t stream);
+cudaError_t launch_copy_blocks(const CopyArgs& a, unsigned units, cudaStream_t stream);
 cudaError_t launch_write_fp8(const WriteArgs& a, cudaStream_t stream, int num_sms);
 // fp8 = true: the caches hold e4m3 codes (the maps are uint8, unswizzled).
 cudaError_t launch_decode_bf16(const CUtensorMap& kmap, const CUtensorMap& vmap,

@@ -11,12 +11,13 @@ import ctypes
 import os
 import threading
 
+import numpy as np
 import torch
 
 _lock = threading.Lock()
 _lib = None
 
-PKV_F32, PKV_BF16, PKV_FP8_E4M3 = 0, 1, 2
+PKV_F32, PKV_BF16, PKV_FP8_E4M3, PKV_INT8 = 0, 1, 2, 3
 # FP8 caches hold e4m3 codes; either dtype may carry them.
 FP8_DTYPES = (torch.uint8, torch.float8_e4m3fn)
 ERR_SLOT = 1 << 0
@@ -25,10 +26,13 @@ ERR_CONTEXT_LEN = 1 << 2
 ERR_QUERY_LEN = 1 << 3
 ERR_DECODE_QLEN = 1 << 4
 ERR_TIMEOUT = 1 << 5
+ERR_NONFINITE = 1 << 6
 EXPORTED = ("pkv_write", "pkv_write_fp8", "pkv_attention_workspace_size", "pkv_attention",
             "pkv_attention_fp8", "pkv_attention_static_scratch",
             "pkv_attention_cascade_workspace_size", "pkv_attention_cascade",
             "pkv_attention_cascade_fp8", "pkv_use_cascade",
+            "pkv_write_int8", "pkv_attention_int8_workspace_size", "pkv_attention_int8",
+            "pkv_copy_blocks",
             "pkv_get_error", "pkv_status_string", "pkv_last_cuda_error",
             "pkv_last_cuda_error_string", "pkv_debug_wait_test")
 STATIC_SCRATCH_BYTES = 64 << 20
@@ -102,6 +106,18 @@ def load(path: str | None = None):
         lib.pkv_attention_static_scratch.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float,
                                                      ctypes.POINTER(CacheDesc),
                                                      ctypes.POINTER(AttnMeta), vp]
+        lib.pkv_write_int8.restype = ctypes.c_int
+        lib.pkv_write_int8.argtypes = [vp] * 9 + [ctypes.POINTER(CacheDesc),
+                                                  ctypes.POINTER(AttnMeta), vp]
+        lib.pkv_attention_int8_workspace_size.restype = ctypes.c_size_t
+        lib.pkv_attention_int8_workspace_size.argtypes = [ctypes.POINTER(CacheDesc),
+                                                          ctypes.POINTER(AttnMeta)]
+        lib.pkv_attention_int8.restype = ctypes.c_int
+        lib.pkv_attention_int8.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp,
+                                           ctypes.POINTER(CacheDesc), ctypes.POINTER(AttnMeta),
+                                           vp, ctypes.c_size_t, vp]
+        lib.pkv_copy_blocks.restype = ctypes.c_int
+        lib.pkv_copy_blocks.argtypes = [vp, vp, i32, i32, vp, i32, vp]
         lib.pkv_get_error.restype = ctypes.c_int
         lib.pkv_get_error.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.c_int]
         lib.pkv_status_string.restype = ctypes.c_char_p
@@ -132,6 +148,8 @@ def _dtype_code(t: torch.Tensor) -> int:
         return PKV_F32
     if t.dtype in FP8_DTYPES:
         return PKV_FP8_E4M3
+    if t.dtype == torch.int8:
+        return PKV_INT8
     raise PkvError(f"unsupported dtype {t.dtype}")
 
 
@@ -382,6 +400,134 @@ def attention_static_scratch(out, q, k_cache, v_cache, block_tables, context_len
         out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         block_tables.data_ptr(), context_lens.data_ptr(), query_start_loc.data_ptr(),
         float(scale), ctypes.byref(desc), ctypes.byref(meta), _stream(stream)))
+
+
+def _int8_cache(k_cache, v_cache, k_scales, v_scales) -> CacheDesc:
+    """Checks the caches and scales of an int8 cache against each other."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _require(t, n, dtype=torch.int8, ndim=4)
+    if k_cache.shape != v_cache.shape:
+        raise PkvError("k_cache and v_cache must have the same shape")
+    want = (k_cache.shape[0], k_cache.shape[2])
+    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        _require(t, n, dtype=torch.float32, ndim=2)
+        if t.shape != want:
+            raise PkvError(f"{n} must be [num_blocks, num_kv_heads]")
+    return cache_desc(k_cache)
+
+
+def _batch(block_tables, context_lens, query_start_loc) -> None:
+    """Checks the batch's metadata arrays against each other."""
+    _require(block_tables, "block_tables", dtype=torch.int32, ndim=2)
+    _require(context_lens, "context_lens", dtype=torch.int32, ndim=1)
+    _require(query_start_loc, "query_start_loc", dtype=torch.int32, ndim=1)
+    S = context_lens.shape[0]
+    if block_tables.shape[0] < S or query_start_loc.shape[0] < S + 1:
+        raise PkvError("block_tables needs num_seqs rows, query_start_loc num_seqs + 1 entries")
+
+
+def _same_device(*tensors) -> None:
+    """Every tensor on the current device: the kernels run there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t.device.index != dev:
+            raise PkvError(f"tensors must be on the current CUDA device ({dev})")
+
+
+def write_int8(k, v, block_tables, context_lens, query_start_loc, k_cache, v_cache, k_scales,
+               v_scales, *, max_query_len, stream=None) -> None:
+    """pkv_write_int8: the batch's bf16 rows k/v [T, Hkv, D] into the int8
+    caches at the sequences' last positions, making the scales fp32
+    [num_blocks, Hkv] of the blocks they touch."""
+    lib = load()
+    desc = _int8_cache(k_cache, v_cache, k_scales, v_scales)
+    for t, n in ((k, "k"), (v, "v")):
+        _require(t, n, dtype=torch.bfloat16, ndim=3)
+        if t.shape != (k.shape[0], desc.num_kv_heads, desc.head_size):
+            raise PkvError("k and v must be [num_tokens, num_kv_heads, head_size]")
+    _batch(block_tables, context_lens, query_start_loc)
+    _same_device(k, v, block_tables, context_lens, query_start_loc, k_cache, v_cache, k_scales,
+                 v_scales)
+    meta = AttnMeta(context_lens.shape[0], k.shape[0], desc.num_kv_heads, block_tables.shape[1],
+                    int(max_query_len), 0, -1, 0, 0)
+    _check(lib.pkv_write_int8(k.data_ptr(), v.data_ptr(), block_tables.data_ptr(),
+                              context_lens.data_ptr(), query_start_loc.data_ptr(),
+                              k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+                              v_scales.data_ptr(), ctypes.byref(desc), ctypes.byref(meta),
+                              _stream(stream)))
+
+
+def workspace_size_int8(k_cache, meta: AttnMeta) -> int:
+    desc = cache_desc(k_cache)
+    n = load().pkv_attention_int8_workspace_size(ctypes.byref(desc), ctypes.byref(meta))
+    if n == ctypes.c_size_t(-1).value:
+        raise PkvError("invalid attention description")
+    return int(n)
+
+
+def attention_int8(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                   k_scales, v_scales, *, max_query_len, max_context_len, num_decode_seqs=-1,
+                   kv_split_tokens=0, sliding_window=0, workspace=None, stream=None) -> None:
+    """pkv_attention_int8 into ``out`` [T, Hq, D] (bf16) over int8 caches with
+    the scales write_int8 made.  ``workspace`` (uint8 CUDA tensor of
+    workspace_size_int8 bytes) is allocated here when not given and needed."""
+    lib = load()
+    desc = _int8_cache(k_cache, v_cache, k_scales, v_scales)
+    for t, n in ((out, "out"), (q, "q")):
+        _require(t, n, dtype=torch.bfloat16, ndim=3)
+    if out.shape != q.shape or q.shape[2] != desc.head_size:
+        raise PkvError("out and q must be [num_tokens, num_q_heads, head_size]")
+    _batch(block_tables, context_lens, query_start_loc)
+    _same_device(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, k_scales,
+                 v_scales)
+    meta = attn_meta(q, block_tables, context_lens, max_query_len=max_query_len,
+                     max_context_len=max_context_len, num_decode_seqs=num_decode_seqs,
+                     kv_split_tokens=kv_split_tokens, sliding_window=sliding_window)
+    if workspace is None:
+        need = lib.pkv_attention_int8_workspace_size(ctypes.byref(desc), ctypes.byref(meta))
+        if need == ctypes.c_size_t(-1).value:
+            need = 0   # (the call itself says what is wrong)
+        if need:
+            if stream is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            else:      # scratch of the stream that uses it
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_ptr, ws_bytes = 0, 0
+    if workspace is not None:
+        _require(workspace, "workspace")
+        _same_device(workspace)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.pkv_attention_int8(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+                                  v_cache.data_ptr(), block_tables.data_ptr(),
+                                  context_lens.data_ptr(), query_start_loc.data_ptr(),
+                                  float(scale), k_scales.data_ptr(), v_scales.data_ptr(),
+                                  ctypes.byref(desc), ctypes.byref(meta), ws_ptr, ws_bytes,
+                                  _stream(stream)))
+
+
+def copy_blocks(buffers, pairs, stream=None) -> None:
+    """pkv_copy_blocks: copies whole blocks of every buffer (CUDA tensors
+    [num_blocks, ...]: the K and V caches and scales of all layers) along
+    ``pairs`` (host ints [n, 2]: from, to), in order."""
+    lib = load()
+    pairs = np.ascontiguousarray(pairs, dtype=np.int32)
+    if pairs.size == 0:
+        return
+    if pairs.ndim != 2 or pairs.shape[1] != 2:
+        raise PkvError("pairs must be [n, 2] (from, to)")
+    n = len(buffers)
+    if n == 0:
+        return
+    nb = buffers[0].shape[0]
+    for t in buffers:
+        if not (t.is_cuda and t.is_contiguous() and t.dim() >= 1 and t.shape[0] == nb):
+            raise PkvError("buffers must be contiguous CUDA tensors of the same number of blocks")
+    _same_device(*buffers)
+    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in buffers])
+    page = (ctypes.c_int64 * n)(*[t.nbytes // max(nb, 1) for t in buffers])
+    _check(lib.pkv_copy_blocks(ptrs, page, n, nb, pairs.ctypes.data, pairs.shape[0],
+                               _stream(stream)))
 
 
 def get_error(clear: bool = True) -> int:
