@@ -951,6 +951,48 @@ int check_cache_int8(const pkv_cache_desc* c) {
   return check_cache(&as_bytes);
 }
 
+// How the decode sequences of an int8 batch are cut: their blocks on one line,
+// in equal ranges (pkv_decode_int8.cu).
+struct Int8Plan {
+  int num_decode = 0;
+  int col_groups = 1;
+  int num_ranges = 1;     // ranges that give every resident warp one (range, head)
+  int max_ranges = 1;     // that there can be: the workspace has two slots for each
+  size_t ws_o_bytes = 0, ws_lse_bytes = 0, ws_bytes = 0;
+};
+
+// Blocks of a range at least: below this a warp's start and its partial cost
+// more than the keys it reads.
+constexpr int kMinRangeBlocks = 8;
+
+int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms, Int8Plan* p) {
+  *p = Int8Plan{};
+  p->num_decode = m->max_query_len <= 1 ? m->num_seqs : std::max(m->num_decode_seqs, 0);
+  if (p->num_decode == 0) return PKV_OK;
+  p->col_groups = (m->num_q_heads / c->num_kv_heads + 7) / 8;
+  const int64_t heads = static_cast<int64_t>(c->num_kv_heads) * p->col_groups;
+  const int64_t warps = static_cast<int64_t>(num_sms) * kDecInt8CtasPerSm * 4;
+  p->num_ranges = static_cast<int>(std::max<int64_t>(warps / heads, 1));
+  int64_t longest = (static_cast<int64_t>(m->max_context_len) + kBlock - 1) / kBlock;
+  if (m->sliding_window > 0)   // W keys span at most (W + 14) / 16 + 1 blocks
+    longest = std::min(longest, (static_cast<int64_t>(m->sliding_window) + 14) / kBlock + 1);
+  const int64_t blocks = longest * p->num_decode;
+  const int64_t ranges =
+      m->kv_split_tokens > 0
+          ? (blocks + m->kv_split_tokens / kBlock - 1) / (m->kv_split_tokens / kBlock)
+          : std::min<int64_t>(p->num_ranges, (blocks + kMinRangeBlocks - 1) / kMinRangeBlocks);
+  if (ranges * heads > INT32_MAX / 2 || blocks / p->num_ranges > INT32_MAX / 2) return PKV_E_SHAPE;
+  p->max_ranges = static_cast<int>(std::max<int64_t>(ranges, 1));
+  if (p->max_ranges > 1) {
+    const size_t rows = 2 * static_cast<size_t>(p->max_ranges) * m->num_q_heads;
+    p->ws_o_bytes = round_up(rows * c->head_size * sizeof(float), 256);
+    p->ws_lse_bytes = round_up(rows * sizeof(float), 256);
+    p->ws_bytes = p->ws_o_bytes + p->ws_lse_bytes +
+                  round_up(static_cast<size_t>(p->num_decode) * sizeof(int2), 256);
+  }
+  return PKV_OK;
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -1001,7 +1043,12 @@ extern "C" size_t pkv_attention_int8_workspace_size(const pkv_cache_desc* cache,
                                                     const pkv_attn_meta* meta) {
   if (check_cache_int8(cache) != PKV_OK || check_meta(cache, meta) != PKV_OK)
     return static_cast<size_t>(-1);
-  return 0;
+  int32_t* err;
+  int sms;
+  Int8Plan p;
+  if (device_state(&err, &sms) != PKV_OK || make_int8_plan(cache, meta, sms, &p) != PKV_OK)
+    return static_cast<size_t>(-1);
+  return p.ws_bytes;
 }
 
 extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
@@ -1021,33 +1068,82 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
       !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(query_start_loc) ||
       !aligned4(k_scales) || !aligned4(v_scales))
     return PKV_E_ALIGN;
-  (void)workspace;
-  (void)workspace_bytes;
   int32_t* err;
   int sms, dev;
   if (int st = device_state(&err, &sms, &dev)) return st;
+  Int8Plan p;
+  if (int st = make_int8_plan(cache, meta, sms, &p)) return st;
+  if (p.ws_bytes > 0) {
+    if (workspace == nullptr || workspace_bytes < p.ws_bytes) return PKV_E_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PKV_E_ALIGN;
+  }
   const cudaStream_t st = as_stream(stream);
-  AttnInt8Args a{};
-  a.out = out;
-  a.q = q;
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
-  a.k_scales = k_scales;
-  a.v_scales = v_scales;
-  a.block_tables = block_tables;
-  a.context_lens = context_lens;
-  a.query_start_loc = query_start_loc;
-  a.err = err;
-  a.bt_stride = meta->block_table_stride;
-  a.num_seqs = meta->num_seqs;
-  a.num_tokens = meta->num_tokens;
-  a.num_q_heads = meta->num_q_heads;
-  a.num_kv_heads = cache->num_kv_heads;
-  a.num_blocks = cache->num_blocks;
-  a.max_query_len = meta->max_query_len;
-  a.window = meta->sliding_window;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  PKV_TRY(launch_attention_int8(a, cache->head_size, st));
+  const float scale_log2 = scale * 1.4426950408889634f;
+  const int G = meta->num_q_heads / cache->num_kv_heads;
+  if (p.num_decode > 0) {
+    CUtensorMap kmap, vmap;
+    if (int e = encode_cache_map(&kmap, k_cache, *cache)) return e;
+    if (int e = encode_cache_map(&vmap, v_cache, *cache)) return e;
+    DecodeInt8Args d{};
+    d.out = out;
+    d.q = q;
+    d.k_scales = k_scales;
+    d.v_scales = v_scales;
+    d.block_tables = block_tables;
+    d.context_lens = context_lens;
+    d.query_start_loc = query_start_loc;
+    if (p.ws_bytes > 0) {
+      char* ws = static_cast<char*>(workspace);
+      d.ws_o = reinterpret_cast<float*>(ws);
+      d.ws_lse = reinterpret_cast<float*>(ws + p.ws_o_bytes);
+      d.span = reinterpret_cast<int2*>(ws + p.ws_o_bytes + p.ws_lse_bytes);
+    }
+    d.err = err;
+    d.bt_stride = meta->block_table_stride;
+    d.num_seqs = p.num_decode;
+    d.num_tokens = meta->num_tokens;
+    d.num_q_heads = meta->num_q_heads;
+    d.num_kv_heads = cache->num_kv_heads;
+    d.group = G;
+    d.col_groups = p.col_groups;
+    d.num_blocks = cache->num_blocks;
+    d.max_context_len = meta->max_context_len;
+    d.window = meta->sliding_window;
+    d.range_blocks = meta->kv_split_tokens / kBlock;
+    d.min_range_blocks = kMinRangeBlocks;
+    d.num_ranges = p.num_ranges;
+    d.max_ranges = p.max_ranges;
+    const int64_t items =
+        static_cast<int64_t>(p.max_ranges) * cache->num_kv_heads * p.col_groups;
+    d.grid = static_cast<uint32_t>(
+        std::min<int64_t>((items + 3) / 4, static_cast<int64_t>(sms) * kDecInt8CtasPerSm));
+    d.scale_log2 = scale_log2;
+    PKV_TRY(launch_decode_int8(kmap, vmap, d, cache->head_size, p.max_ranges > 1, st));
+  }
+  if (p.num_decode < meta->num_seqs) {
+    AttnInt8Args a{};
+    a.out = out;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_start_loc = query_start_loc;
+    a.err = err;
+    a.bt_stride = meta->block_table_stride;
+    a.seq_begin = p.num_decode;
+    a.num_seqs = meta->num_seqs;
+    a.num_tokens = meta->num_tokens;
+    a.num_q_heads = meta->num_q_heads;
+    a.num_kv_heads = cache->num_kv_heads;
+    a.num_blocks = cache->num_blocks;
+    a.max_query_len = meta->max_query_len;
+    a.window = meta->sliding_window;
+    a.scale_log2 = scale_log2;
+    PKV_TRY(launch_attention_int8(a, cache->head_size, st));
+  }
   return PKV_OK;
 }
 

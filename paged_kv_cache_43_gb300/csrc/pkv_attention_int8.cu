@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(kWarps * 32) pkv_attention_int8_kernel(const A
   const int hq = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = seq_of_row(a.query_start_loc, a.num_seqs, t);
-  if (s < 0) return;   // a row of no sequence
+  if (s < a.seq_begin) return;   // a row of no sequence, or of a decode sequence
   const int q0 = __ldg(a.query_start_loc + s);
   const int qn = __ldg(a.query_start_loc + s + 1) - q0;
   const int L = __ldg(a.context_lens + s);

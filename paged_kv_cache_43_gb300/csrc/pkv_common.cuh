@@ -317,6 +317,13 @@ __device__ __forceinline__ int f16_row_exponent(float amax) {
   if (!(amax > 16384.f) || !(amax <= 3.402823466e38f)) return 0;
   return ((__float_as_int(amax) >> 23) & 0xFF) - 127 + 1 - 14;  // amax * 2^-e < 2^14
 }
+// As above for rows of any size: e with amax * 2^-e in [2^13, 2^14), small
+// rows scaled up (0 for an all-zero or non-finite row; e >= -112 keeps 2^-e
+// finite).
+__device__ __forceinline__ int f16_fit_exponent(float amax) {
+  if (!(amax > 0.f) || !(amax <= 3.402823466e38f)) return 0;
+  return max(((__float_as_int(amax) >> 23) & 0xFF) - 127 + 1 - 14, -112);
+}
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((127 + e) << 23); }
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, float mul) {
   return pack_f16(bf16_lo(w) * mul, bf16_hi(w) * mul);

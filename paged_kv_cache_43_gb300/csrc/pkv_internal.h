@@ -186,6 +186,7 @@ struct AttnInt8Args {
   const int32_t* query_start_loc;
   int32_t* err;
   int64_t bt_stride;
+  int32_t seq_begin;             // sequences [seq_begin, num_seqs)
   int32_t num_seqs;
   int32_t num_tokens;
   int32_t num_q_heads;
@@ -194,6 +195,40 @@ struct AttnInt8Args {
   int32_t max_query_len;
   int32_t window;
   float scale_log2;
+};
+
+// Decode over sequences [0, num_seqs) of an int8 cache.
+constexpr int kDecInt8CtasPerSm = 4;   // resident CTAs (of 4 warps) per SM
+struct DecodeInt8Args {
+  void* out;                     // bf16 [T, Hq, D]
+  const void* q;
+  const float* k_scales;
+  const float* v_scales;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start_loc;
+  float* ws_o;                   // [2 max_ranges, Hq, D] partial outputs
+  float* ws_lse;                 // [2 max_ranges, Hq], log2 domain
+  int2* span;                    // [num_seqs]: first range, ranges (null: one range)
+  int32_t* err;
+  int64_t bt_stride;
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t group;
+  int32_t col_groups;            // groups of 8 q heads per kv head
+  int32_t num_blocks;
+  int32_t max_context_len;
+  int32_t window;
+  int32_t range_blocks;          // blocks of a range (0: an equal share)
+  int32_t min_range_blocks;
+  int32_t num_ranges;            // ranges that fill the GPU (equal shares)
+  int32_t max_ranges;            // ranges the workspace holds
+  uint32_t grid;
+  float scale_log2;
+  uint64_t wait_limit_ns;        // test hook, as DecodeArgs
+  int32_t debug_stall;
 };
 
 // ---- page copies
@@ -217,6 +252,9 @@ struct CopyArgs {
 cudaError_t launch_write(const WriteArgs& a, cudaStream_t stream, int num_sms);
 cudaError_t launch_write_int8(const WriteInt8Args& a, cudaStream_t stream);
 cudaError_t launch_attention_int8(const AttnInt8Args& a, int head_size, cudaStream_t stream);
+cudaError_t launch_decode_int8(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const DecodeInt8Args& a, int head_size, bool merge,
+                               cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyArgs& a, unsigned units, cudaStream_t stream);
 cudaError_t launch_write_fp8(const WriteArgs& a, cudaStream_t stream, int num_sms);
 // fp8 = true: the caches hold e4m3 codes (the maps are uint8, unswizzled).
