@@ -1080,10 +1080,10 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
   const cudaStream_t st = as_stream(stream);
   const float scale_log2 = scale * 1.4426950408889634f;
   const int G = meta->num_q_heads / cache->num_kv_heads;
-  if (p.num_decode > 0) {
-    CUtensorMap kmap, vmap;
-    if (int e = encode_cache_map(&kmap, k_cache, *cache)) return e;
-    if (int e = encode_cache_map(&vmap, v_cache, *cache)) return e;
+  CUtensorMap kmap, vmap;
+  if (int e = encode_cache_map(&kmap, k_cache, *cache)) return e;
+  if (int e = encode_cache_map(&vmap, v_cache, *cache)) return e;
+  auto decode_part = [&](cudaStream_t st) -> int {
     DecodeInt8Args d{};
     d.out = out;
     d.q = q;
@@ -1119,32 +1119,76 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
         std::min<int64_t>((items + 3) / 4, static_cast<int64_t>(sms) * kDecInt8CtasPerSm));
     d.scale_log2 = scale_log2;
     PKV_TRY(launch_decode_int8(kmap, vmap, d, cache->head_size, p.max_ranges > 1, st));
-  }
-  if (p.num_decode < meta->num_seqs) {
-    AttnInt8Args a{};
-    a.out = out;
-    a.q = q;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.k_scales = k_scales;
-    a.v_scales = v_scales;
-    a.block_tables = block_tables;
-    a.context_lens = context_lens;
-    a.query_start_loc = query_start_loc;
-    a.err = err;
-    a.bt_stride = meta->block_table_stride;
-    a.seq_begin = p.num_decode;
-    a.num_seqs = meta->num_seqs;
-    a.num_tokens = meta->num_tokens;
-    a.num_q_heads = meta->num_q_heads;
-    a.num_kv_heads = cache->num_kv_heads;
-    a.num_blocks = cache->num_blocks;
-    a.max_query_len = meta->max_query_len;
-    a.window = meta->sliding_window;
-    a.scale_log2 = scale_log2;
-    PKV_TRY(launch_attention_int8(a, cache->head_size, st));
-  }
-  return PKV_OK;
+    return PKV_OK;
+  };
+  const int npf = meta->num_seqs - p.num_decode;
+  auto prefill_part = [&](cudaStream_t st) -> int {
+    if (G > 128) {   // more q heads on a kv head than a query tile has rows
+      AttnInt8Args a{};
+      a.out = out;
+      a.q = q;
+      a.k_cache = k_cache;
+      a.v_cache = v_cache;
+      a.k_scales = k_scales;
+      a.v_scales = v_scales;
+      a.block_tables = block_tables;
+      a.context_lens = context_lens;
+      a.query_start_loc = query_start_loc;
+      a.err = err;
+      a.bt_stride = meta->block_table_stride;
+      a.seq_begin = p.num_decode;
+      a.num_seqs = meta->num_seqs;
+      a.num_tokens = meta->num_tokens;
+      a.num_q_heads = meta->num_q_heads;
+      a.num_kv_heads = cache->num_kv_heads;
+      a.num_blocks = cache->num_blocks;
+      a.max_query_len = meta->max_query_len;
+      a.window = meta->sliding_window;
+      a.scale_log2 = scale_log2;
+      PKV_TRY(launch_attention_int8(a, cache->head_size, st));
+      return PKV_OK;
+    }
+    PrefillArgs f{};
+    f.out = out;
+    f.q = q;
+    f.block_tables = block_tables;
+    f.context_lens = context_lens;
+    f.query_start_loc = query_start_loc;
+    f.err = err;
+    f.bt_stride = meta->block_table_stride;
+    f.seq_begin = p.num_decode;
+    f.num_seqs = npf;
+    f.num_q_heads = meta->num_q_heads;
+    f.num_kv_heads = cache->num_kv_heads;
+    f.group = G;
+    f.num_blocks = cache->num_blocks;
+    f.num_tokens = meta->num_tokens;
+    f.max_query_len = meta->max_query_len;
+    f.window = meta->sliding_window;
+    f.k_scales = k_scales;
+    f.v_scales = v_scales;
+    f.scale_log2 = scale_log2;
+    f.longest_first = p.num_decode == 0 ? 1 : 0;   // alone on the GPU, or beside decode
+    const int toks = prefill_tc_tokens_per_cta(G);
+    f.num_mtiles = (meta->max_query_len + toks - 1) / toks;
+    CUtensorMap qmap, omap;
+    if (int e = encode_query_map(&qmap, q, meta->num_tokens, meta->num_q_heads, cache->head_size, G))
+      return e;
+    if (int e =
+            encode_query_map(&omap, out, meta->num_tokens, meta->num_q_heads, cache->head_size, G))
+      return e;
+    PKV_TRY(launch_prefill_tc_int8(qmap, kmap, vmap, omap, f, cache->head_size, st));
+    return PKV_OK;
+  };
+  if (p.num_decode == 0) return prefill_part(st);
+  if (npf == 0) return decode_part(st);
+  // decode and prefill rows in one batch: as pkv_attention
+  SideFork fork(dev, st);
+  if (int e = fork.begin()) return e;
+  int rc = prefill_part(fork.stream());
+  if (rc == PKV_OK) rc = decode_part(st);
+  const int jr = fork.join();
+  return rc != PKV_OK ? rc : jr;
 }
 
 // -------------------------------------------------------------- page copies

@@ -285,6 +285,18 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   return d;
 }
 
+// Four int8 codes (byte i = code i) -> four fp16 values, exactly: the code +
+// 128 becomes the low bits of 1024 + (code + 128), less 1152.
+__device__ __forceinline__ uint32_t sub_1152(uint32_t x) {
+  uint32_t y;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x64806480u));
+  return y;
+}
+__device__ __forceinline__ uint2 i8x4_to_f16x4(uint32_t codes) {
+  const uint32_t u = codes ^ 0x80808080u;
+  return make_uint2(sub_1152(prmt(u, 0x64646464u, 0x4140u)), sub_1152(prmt(u, 0x64646464u, 0x4342u)));
+}
+
 // Operand-type switch of the mma.sync kernels: bf16 (bf16 caches) or fp16
 // (FP8 caches).
 template <bool F16>

@@ -45,18 +45,6 @@ constexpr int dec8_smem_bytes() {
          (kThreads + 1) * 8;
 }
 
-// Four int8 codes (byte i = code i) -> four fp16 values, exactly: the code +
-// 128 becomes the low bits of 1024 + (code + 128), less 1152.
-__device__ __forceinline__ uint32_t sub_1152(uint32_t x) {
-  uint32_t y;
-  asm("sub.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x64806480u));
-  return y;
-}
-__device__ __forceinline__ uint2 i8x4_to_f16x4(uint32_t codes) {
-  const uint32_t u = codes ^ 0x80808080u;
-  return make_uint2(sub_1152(prmt(u, 0x64646464u, 0x4140u)), sub_1152(prmt(u, 0x64646464u, 0x4342u)));
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

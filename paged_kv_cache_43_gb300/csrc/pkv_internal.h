@@ -124,6 +124,9 @@ struct PrefillArgs {
   // tile so that the waits for it run out.
   uint64_t wait_limit_ns;
   int32_t debug_stall;
+  // Int8 cache: block scales [num_blocks, Hkv] (null otherwise)
+  const float* k_scales;
+  const float* v_scales;
 };
 
 // Settings of the test hook, applied to the decode and tcgen05 prefill
@@ -287,6 +290,12 @@ cudaError_t launch_prefill_tc(const CUtensorMap& qmap, const CUtensorMap& kmap,
                               const CUtensorMap& vmap, const CUtensorMap& omap,
                               const PrefillArgs& a, int head_size, bool fp8,
                               cudaStream_t stream);
+
+// The same kernel over int8 caches with block scales (a.k_scales, a.v_scales);
+// any group of at most 128.
+cudaError_t launch_prefill_tc_int8(const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                   const CUtensorMap& vmap, const CUtensorMap& omap,
+                                   const PrefillArgs& a, int head_size, cudaStream_t stream);
 
 // Rows of the prefill kernel's query tile (grid.x covers ceil(q_len*G / this)).
 constexpr int kPrefillRows = 64;

@@ -57,6 +57,16 @@
 //    scaled by 2^-e, its scores by 2^e) and the MMAs run on fp16 operands with
 //    P in fp16.  The K descale folds into the score scale, the V descale into
 //    the output.
+//  * int8 cache with a scale per (cache block, kv head): the codes travel and
+//    widen like e4m3 codes (an int8 code is exact in fp16).  A score's scale is
+//    its key block's; the block's V scale rides in the softmax exponent, P =
+//    2^(x + log2 sv - m) with m following the largest x + log2 sv, so P in fp16
+//    is at most 2^8 whatever the scales are, and the row sum divides it out
+//    again (per block, in fp32).  Both cost nothing per element: they are the
+//    factor and the addend of the exponent's one FMA, per block of 16 keys
+//    instead of per tile.  Each softmax warp fetches its tiles' 8 + 8 scales
+//    itself, ids two tiles and scales one tile ahead, and hands them round by
+//    shuffles.  Every code is finite, so rows no key may see need no zeroing.
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 #include "pkv_tc.cuh"
@@ -64,6 +74,9 @@
 namespace pkv {
 
 namespace {
+
+// What the caches hold (the kernel's template switch).
+constexpr int kBf16 = 0, kE4m3 = 1, kInt8 = 2;
 
 constexpr int kTcRows = 128;      // UMMA M (rows of one query tile)
 constexpr int kTcTiles = 2;       // query tiles per CTA
@@ -189,13 +202,20 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Widens one 128-key x 128 e4m3 tile (128-byte swizzled rows at `tile`) in
+template <bool I8>
+__device__ __forceinline__ uint2 codes_to_f16x4(uint32_t codes) {
+  if constexpr (I8) return i8x4_to_f16x4(codes);
+  else return e4m3x4_to_f16x4(codes);
+}
+
+// Widens one 128-key x 128 tile of e4m3 or int8 codes (128-byte swizzled rows at `tile`) in
 // place into the fp16 tile layout (two 64-column halves, 16 KB apart,
 // 128-byte swizzled); all 32 lanes of the calling warp.  A batch covers 16
 // rows: a lane reads its 16-code chunk of 4 rows (4 loads in flight), and
 // only after the warp has read the whole batch does it write the batch's fp16
 // chunks (those of half 0 overwrite the same rows' codes); batches touch
 // disjoint rows, so two warps may widen batches [b0, b1) of the same tile.
+template <bool I8>
 __device__ __forceinline__ void widen_tile_fp8(uint8_t* tile, int lane, int b0, int b1) {
   const int c = lane & 7;           // chunk: columns 16c .. 16c + 15
   const int j = 2 * (c & 3);        // its first 8-column chunk within the half
@@ -211,8 +231,8 @@ __device__ __forceinline__ void widen_tile_fp8(uint8_t* tile, int lane, int b0, 
     uint4 lo[4], hi[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint2 x = e4m3x4_to_f16x4(codes[i].x), y = e4m3x4_to_f16x4(codes[i].y);
-      const uint2 z = e4m3x4_to_f16x4(codes[i].z), w = e4m3x4_to_f16x4(codes[i].w);
+      const uint2 x = codes_to_f16x4<I8>(codes[i].x), y = codes_to_f16x4<I8>(codes[i].y);
+      const uint2 z = codes_to_f16x4<I8>(codes[i].z), w = codes_to_f16x4<I8>(codes[i].w);
       lo[i] = make_uint4(x.x, x.y, y.x, y.y);
       hi[i] = make_uint4(z.x, z.y, w.x, w.y);
     }
@@ -256,6 +276,7 @@ __device__ __forceinline__ void zero_v_rows(uint8_t* vt, int lead, int tail, int
 // 2b + 1; going from the last batch to the first, those were read earlier
 // (or, for b = 0, by this batch before its writes).  A lane reads two 16-code
 // chunks per batch.
+template <bool I8>
 __device__ __forceinline__ void widen_tile_fp8_d64(uint8_t* tile, int lane) {
   const int c = lane & 3;           // code chunk: columns 16c .. 16c + 15
 #pragma unroll 1
@@ -269,8 +290,8 @@ __device__ __forceinline__ void widen_tile_fp8_d64(uint8_t* tile, int lane) {
     uint4 lo[2], hi[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint2 x = e4m3x4_to_f16x4(codes[i].x), y = e4m3x4_to_f16x4(codes[i].y);
-      const uint2 z = e4m3x4_to_f16x4(codes[i].z), w = e4m3x4_to_f16x4(codes[i].w);
+      const uint2 x = codes_to_f16x4<I8>(codes[i].x), y = codes_to_f16x4<I8>(codes[i].y);
+      const uint2 z = codes_to_f16x4<I8>(codes[i].z), w = codes_to_f16x4<I8>(codes[i].w);
       lo[i] = make_uint4(x.x, x.y, y.x, y.y);
       hi[i] = make_uint4(z.x, z.y, w.x, w.y);
     }
@@ -352,13 +373,15 @@ __device__ __forceinline__ TcWork pick_work(const PrefillArgs& a, int toks, int3
 
 // LPT: the longest-first instantiation (a separate kernel, so that the plain
 // one keeps its work indices as launch coordinates and its register budget).
-template <int D, bool FP8, bool LPT>
+template <int D, int FMT, bool LPT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     pkv_prefill_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap,
                           const __grid_constant__ CUtensorMap omap, const PrefillArgs a) {
   using Lt = TcLayout<D>;
+  constexpr bool FP8 = FMT != kBf16;   // one-byte codes, widened to fp16
+  constexpr bool I8 = FMT == kInt8;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -371,10 +394,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // Cascade prefix launch: one "sequence" whose rows are the batch's decode
   // rows (sequence t at row t), non-causal over the shared keys, one key split
   // per grid.z; otherwise grid.z is the sequence.
-  const bool casc = a.cascade_prefix != 0;
+  const bool casc = !I8 && a.cascade_prefix != 0;
   const int G = a.group;
   const int Hq = a.num_q_heads;
-  const int tile_toks = kTcRows / G;                // tokens per query tile
+  const int tile_toks = kTcRows / G;                // tokens per query tile (int8: G any
+                                                    // size, the tile's last rows idle)
   const int toks = kTcTiles * tile_toks;            // tokens per CTA
   int s, kvh, mtile;
   if constexpr (LPT) {
@@ -551,7 +575,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint64_t keep = policy_evict_normal();   // K/V tiles are re-read by the
     const int32_t* bt = a.block_tables + static_cast<int64_t>(s) * a.bt_stride;  // other row tiles
     if (warp == 8 && lane == 0) {
-      mbar_arrive_expect_tx(q_full, ntq * Lt::kQTile);
+      mbar_arrive_expect_tx(q_full, I8 ? ntq * Lt::kHalves * tile_toks * G * 128
+                                       : ntq * Lt::kQTile);
       for (int t = 0; t < ntq; ++t)
 #pragma unroll
         for (int h = 0; h < Lt::kHalves; ++h)
@@ -708,11 +733,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!warp_wait(smem_u32(&sh->kv_land[st]), ring_phase(e), abort, a.err, wlim)) break;
       uint8_t* tile = sKV + st * Lt::kTileBytes;
       if constexpr (D == 128)
-        widen_tile_fp8(tile, lane, r0 / 16, r1 / 16);
+        widen_tile_fp8<I8>(tile, lane, r0 / 16, r1 / 16);
       else
-        widen_tile_fp8_d64(tile, lane);
+        widen_tile_fp8_d64<I8>(tile, lane);
       int lead, tail;
-      if ((e & 1) && v_edges(e >> 1, lead, tail)) {
+      if (!I8 && (e & 1) && v_edges(e >> 1, lead, tail)) {
         __syncwarp();
         zero_v_rows<D>(tile, lead, tail, r0, r1, lane);
       }
@@ -730,7 +755,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const int tok = tok0 + t * tile_toks + row / G;
     const int g = row % G;
-    const bool valid = tok <= tok_last;
+    const bool valid = tok <= tok_last && (!I8 || row < tile_toks * G);
     const int pos = casc ? L - 1 : L - qn + (valid ? tok : tok_last);
     const uint32_t b_sfull = smem_u32(&sh->s_full[t]);
     const uint32_t b_pfull = smem_u32(&sh->p_full[t]), b_pvdone = smem_u32(&sh->pv_done[t]);
@@ -742,10 +767,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // descales of this (sequence, kv head) -- a cascade prefix row's own
       // sequence (rows are the batch's query tokens); this thread's Q row to
       // fp16
-      const int ds =
-          casc ? max(seq_of_row(a.query_start_loc, a.casc_seqs, valid ? tok : tok_last), 0) : s;
-      sl2 *= __ldg(a.k_descale + static_cast<int64_t>(ds) * a.num_kv_heads + kvh);
-      out_scale = __ldg(a.v_descale + static_cast<int64_t>(ds) * a.num_kv_heads + kvh);
+      if constexpr (!I8) {
+        const int ds =
+            casc ? max(seq_of_row(a.query_start_loc, a.casc_seqs, valid ? tok : tok_last), 0) : s;
+        sl2 *= __ldg(a.k_descale + static_cast<int64_t>(ds) * a.num_kv_heads + kvh);
+        out_scale = __ldg(a.v_descale + static_cast<int64_t>(ds) * a.num_kv_heads + kvh);
+      }
       bool qok = warp_wait(q_full, 0, abort, a.err, wlim);
       if (qok) {
         uint8_t* qrow = sQ + t * Lt::kQTile + row * 128;
@@ -761,9 +788,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int e = 0; e < 4; ++e)
               amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
           }
-        const int ex = f16_row_exponent(amax);
-        const float down = pow2f(-ex);
+        const int ex = I8 ? f16_fit_exponent(amax) : f16_row_exponent(amax);
+        float down = pow2f(-ex);
         sl2 *= pow2f(ex);
+        if (I8 && sl2 < 0.f) {   // a negative scale: its sign goes to the query
+          sl2 = -sl2;
+          down = -down;
+        }
 #pragma unroll
         for (int h = 0; h < Lt::kHalves; ++h)
 #pragma unroll
@@ -780,6 +811,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     float m_used = -INFINITY, l = 0.f;
     bool done = t < ntq;
+    // Int8: block scales of key tile j in lanes 0-7 (K) and 8-15 (V).
+    const int32_t* i8_bt = a.block_tables + static_cast<int64_t>(s) * a.bt_stride;
+    const float* i8_scales = (lane & 8) ? a.v_scales : a.k_scales;
+    auto i8_id = [&](int j) {
+      const int b = (j0 + j) * (kTcKeys / kBlock) + (lane & 7);
+      return lane < 16 && b >= b_lo && b < nblk ? __ldg(i8_bt + b) : -1;
+    };
+    auto i8_scale = [&](int id) {   // (a block that is not read: any finite scale)
+      return id >= 0 && id < a.num_blocks
+                 ? __ldg(i8_scales + static_cast<int64_t>(id) * a.num_kv_heads + kvh) : 1.f;
+    };
+    float i8_next = 1.f;
+    int i8_id_next = -1;
+    if constexpr (I8) {
+      i8_next = i8_scale(i8_id(0));
+      i8_id_next = i8_id(1);
+    }
     // first key this row sees (its window; after the shared prefix in a
     // cascade suffix launch)
     const int lo = max(a.window > 0 ? pos - a.window + 1 : 0, a.key_begin);
@@ -849,25 +897,55 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int c = 0; c < kTcKeys; ++c) x[c] = c < nvis ? x[c] : -INFINITY;
         }
       }
-      // row max: four independent chains of three-input maxima
-      float m4[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-      for (int c = 4; c < kTcKeys - 4; c += 8) {
-        m4[0] = tc::max3(m4[0], x[c], x[c + 1]);
-        m4[1] = tc::max3(m4[1], x[c + 2], x[c + 3]);
-        m4[2] = tc::max3(m4[2], x[c + 4], x[c + 5]);
-        m4[3] = tc::max3(m4[3], x[c + 6], x[c + 7]);
+      [[maybe_unused]] float i8_now = 1.f;   // K scale, or log2 of the V scale, of block lane % 8
+      if constexpr (I8) {
+        i8_now = int8_scale(i8_next);
+        i8_now = (lane & 8) ? log2f(i8_now) : i8_now;
+        i8_next = i8_scale(i8_id_next);
+        i8_id_next = i8_id(j + 2);
       }
-      m4[0] = tc::max3(m4[0], x[kTcKeys - 4], x[kTcKeys - 3]);
-      m4[1] = tc::max3(m4[1], x[kTcKeys - 2], x[kTcKeys - 1]);
-      const float mt = tc::max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
+      // a block's score factor; kept above zero for the masked -inf
+      auto i8_factor = [&](int b) {
+        const float f = __shfl_sync(0xffffffffu, i8_now, b) * sl2;
+        return f < 1e-37f ? 1e-37f : f;
+      };
+      auto i8_log2v = [&](int b) { return __shfl_sync(0xffffffffu, i8_now, 8 + b); };
+      // row max: four independent chains of three-input maxima
+      float mt;
+      if constexpr (I8) {   // by blocks, each with its scales
+        mt = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < kTcKeys / kBlock; ++b) {
+          const float* xb = x + b * kBlock;
+          float u = tc::max3(xb[0], xb[1], xb[2]), w = tc::max3(xb[3], xb[4], xb[5]);
+          u = tc::max3(u, xb[6], xb[7]);
+          w = tc::max3(w, xb[8], xb[9]);
+          u = tc::max3(u, xb[10], xb[11]);
+          w = tc::max3(w, xb[12], xb[13]);
+          u = tc::max3(u, xb[14], xb[15]);
+          mt = fmaxf(mt, fmaf(fmaxf(u, w), i8_factor(b), i8_log2v(b)));
+        }
+      } else {
+        float m4[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < kTcKeys - 4; c += 8) {
+          m4[0] = tc::max3(m4[0], x[c], x[c + 1]);
+          m4[1] = tc::max3(m4[1], x[c + 2], x[c + 3]);
+          m4[2] = tc::max3(m4[2], x[c + 4], x[c + 5]);
+          m4[3] = tc::max3(m4[3], x[c + 6], x[c + 7]);
+        }
+        m4[0] = tc::max3(m4[0], x[kTcKeys - 4], x[kTcKeys - 3]);
+        m4[1] = tc::max3(m4[1], x[kTcKeys - 2], x[kTcKeys - 1]);
+        mt = tc::max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
+      }
       float alpha = 1.f;
       if (mt > m_used + kLazyRescale) {
         alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - mt);
         m_used = mt;
       }
       const float neg_mu = (m_used == -INFINITY) ? 0.f : -m_used;
-      const uint64_t m2 = tc::pack_f32x2(sl2, sl2), b2 = tc::pack_f32x2(neg_mu, neg_mu);
+      [[maybe_unused]] const uint64_t m2 = tc::pack_f32x2(sl2, sl2),
+                                      b2 = tc::pack_f32x2(neg_mu, neg_mu);
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // rescale O in TMEM
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -881,24 +959,53 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       // P = 2^(s * scale*log2(e) - max): packed FMA, MUFU ex2, bf16 pairs
       // written over S's first 64 columns; the row sum adds the fp32 weights
-      uint64_t acc[4] = {0, 0, 0, 0};
+      float ls;
+      if constexpr (I8) {
+        float part[2] = {0.f, 0.f};
 #pragma unroll
-      for (int c0 = 0; c0 < kTcKeys / 2; c0 += 32) {
-        uint32_t pk[32];
+        for (int c0 = 0; c0 < kTcKeys / 2; c0 += 32) {
+          uint32_t pk[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const int k = 2 * (c0 + c);
-          float y0, y1;
-          tc::fma_f32x2(x[k], x[k + 1], m2, b2, y0, y1);
-          y0 = ex2(y0);
-          y1 = ex2(y1);
-          pk[c] = pack2<FP8>(y0, y1);
-          tc::add_f32x2(acc[c & 3], y0, y1);
+          for (int b = 0; b < 4; ++b) {   // 8 pairs of keys a block
+            const int blk = c0 / 8 + b;
+            const float f = i8_factor(blk), lv = i8_log2v(blk), add = lv + neg_mu;
+            const uint64_t f2 = tc::pack_f32x2(f, f), a2 = tc::pack_f32x2(add, add);
+            uint64_t acc = 0;
+#pragma unroll
+            for (int c = 8 * b; c < 8 * b + 8; ++c) {
+              const int k = 2 * (c0 + c);
+              float y0, y1;
+              tc::fma_f32x2(x[k], x[k + 1], f2, a2, y0, y1);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              pk[c] = pack_f16(y0, y1);
+              tc::add_f32x2(acc, y0, y1);
+            }
+            part[b & 1] = fmaf(tc::sum_f32x2(acc), ex2(-lv), part[b & 1]);
+          }
+          tc::st32(tP + c0, pk);
         }
-        tc::st32(tP + c0, pk);
+        ls = part[0] + part[1];
+      } else {
+        uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int c0 = 0; c0 < kTcKeys / 2; c0 += 32) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int k = 2 * (c0 + c);
+            float y0, y1;
+            tc::fma_f32x2(x[k], x[k + 1], m2, b2, y0, y1);
+            y0 = ex2(y0);
+            y1 = ex2(y1);
+            pk[c] = pack2<FP8>(y0, y1);
+            tc::add_f32x2(acc[c & 3], y0, y1);
+          }
+          tc::st32(tP + c0, pk);
+        }
+        ls = (tc::sum_f32x2(acc[0]) + tc::sum_f32x2(acc[1])) +
+                         (tc::sum_f32x2(acc[2]) + tc::sum_f32x2(acc[3]));
       }
-      const float ls = (tc::sum_f32x2(acc[0]) + tc::sum_f32x2(acc[1])) +
-                       (tc::sum_f32x2(acc[2]) + tc::sum_f32x2(acc[3]));
       l = l * alpha + ls;
       tc::wait_st();
       tc::fence_before_sync();
@@ -1048,13 +1155,13 @@ extern "C" int pkv_tc_timeline_clear() {
 namespace {
 #endif
 
-template <int D, bool FP8>
+template <int D, int FMT>
 cudaError_t launch_tc_t(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                         const CUtensorMap& omap, const PrefillArgs& a, cudaStream_t stream) {
   constexpr int smem = tc_smem_bytes<D>();
   const bool lpt = a.longest_first && !a.cascade_prefix &&
                    static_cast<int64_t>(a.num_seqs) * a.num_mtiles <= kLptUnits;
-  auto kfn = lpt ? pkv_prefill_tc_kernel<D, FP8, true> : pkv_prefill_tc_kernel<D, FP8, false>;
+  auto kfn = lpt ? pkv_prefill_tc_kernel<D, FMT, true> : pkv_prefill_tc_kernel<D, FMT, false>;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // cascade prefix: grid.z = prefix key splits
@@ -1083,10 +1190,18 @@ cudaError_t launch_prefill_tc(const CUtensorMap& qmap, const CUtensorMap& kmap,
                               const PrefillArgs& a, int head_size, bool fp8, cudaStream_t stream) {
   if (a.num_seqs == 0 || a.num_mtiles == 0) return cudaSuccess;
   if (fp8)
-    return head_size == 128 ? launch_tc_t<128, true>(qmap, kmap, vmap, omap, a, stream)
-                            : launch_tc_t<64, true>(qmap, kmap, vmap, omap, a, stream);
-  if (head_size == 128) return launch_tc_t<128, false>(qmap, kmap, vmap, omap, a, stream);
-  return launch_tc_t<64, false>(qmap, kmap, vmap, omap, a, stream);
+    return head_size == 128 ? launch_tc_t<128, kE4m3>(qmap, kmap, vmap, omap, a, stream)
+                            : launch_tc_t<64, kE4m3>(qmap, kmap, vmap, omap, a, stream);
+  if (head_size == 128) return launch_tc_t<128, kBf16>(qmap, kmap, vmap, omap, a, stream);
+  return launch_tc_t<64, kBf16>(qmap, kmap, vmap, omap, a, stream);
+}
+
+cudaError_t launch_prefill_tc_int8(const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                   const CUtensorMap& vmap, const CUtensorMap& omap,
+                                   const PrefillArgs& a, int head_size, cudaStream_t stream) {
+  if (a.num_seqs == 0 || a.num_mtiles == 0) return cudaSuccess;
+  if (head_size == 128) return launch_tc_t<128, kInt8>(qmap, kmap, vmap, omap, a, stream);
+  return launch_tc_t<64, kInt8>(qmap, kmap, vmap, omap, a, stream);
 }
 
 }  // namespace pkv
