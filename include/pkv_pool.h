@@ -42,6 +42,8 @@ extern "C" {
 #define PKV_POOL_NO_SPACE 1    /* not enough free blocks; nothing changed        */
 #define PKV_E_REQUEST (-10)    /* unknown request id, duplicate id, or a call out */
                                /* of order (admit after allocation)               */
+#define PKV_E_MEMORY (-11)     /* host memory ran out (fork, resize, a copy to    */
+                               /* note down); nothing changed                     */
 
 typedef struct pkv_pool pkv_pool; /* opaque; owned by the caller of create/destroy */
 
@@ -90,6 +92,29 @@ int pkv_pool_allocate_slots_batch(pkv_pool *pool, const int64_t *req_ids,
                                   const int32_t *num_new_tokens, int32_t num_reqs,
                                   int32_t sliding_window, int64_t *slot_mapping,
                                   int32_t *num_done);
+/* Forks request parent_id into the new request child_id: the same token ids,
+ * the same computed count and the same blocks, shared (counted).  Afterwards
+ * the two go on apart.  Full blocks stay shared; when pkv_pool_allocate_slots
+ * is to put a position into a partly filled block that another request holds
+ * too, the request first gets a block of its own and the pair (shared block,
+ * own block) is noted for pkv_pool_take_copies (copy on write; the last holder
+ * keeps the block).  No counterpart in the pages. */
+int pkv_pool_fork_request(pkv_pool *pool, int64_t parent_id, int64_t child_id);
+/* Makes the pool num_blocks blocks large (>= 1).  Smaller: blocks in use with
+ * ids >= num_blocks move to free ones below (the free queue's first, so cached
+ * blocks go last), with their cached hashes, and their pairs (old, new) are
+ * noted for pkv_pool_take_copies; free blocks past the end leave the pool and
+ * the prefix cache.  PKV_POOL_NO_SPACE if the blocks in use do not fit; nothing
+ * changed.  Larger: the new blocks go to the head of the free queue, lowest id
+ * first.  No counterpart in the pages. */
+int pkv_pool_resize(pkv_pool *pool, int32_t num_blocks);
+/* Hands over the oldest noted block copies, at most `capacity` of them, as
+ * (from, to) pairs in the order in which pkv_copy_blocks has to make them, and
+ * forgets them; *num_pairs = how many (less than capacity: none are left).
+ * After each scheduling step, make them before the step's KV write, on the
+ * stream of the KV work; after a resize to fewer blocks, before the caches
+ * give up their last blocks. */
+int pkv_pool_take_copies(pkv_pool *pool, int32_t *pairs, int32_t capacity, int32_t *num_pairs);
 /* Releases every block of the request (last to first) and forgets it. */
 int pkv_pool_free_request(pkv_pool *pool, int64_t req_id);
 

@@ -38,6 +38,9 @@ Readings where the pages are silent (stated once here, relied on by the tests):
 * A request releases its blocks last to first, so that under LRU the deepest
   blocks of a cached prefix leave before its root.
 * A hit, like any block the request holds, is released with the request.
+
+Forks (copy on write) and resizing have no counterpart in the pages; they
+follow the descriptions in the library's pool header.
 """
 from __future__ import annotations
 
@@ -84,6 +87,7 @@ class Pool:
         self.null_block = self.free.pop(0)
         self.map = {}                   # hash -> [block ids], oldest first
         self.reqs = {}
+        self.copies = []                # noted (from, to) block copies, oldest first
 
     # ---------------------------------------------------------------- blocks
     def num_free(self) -> int:
@@ -188,13 +192,23 @@ class Pool:
                 if r.blocks[i] != self.null_block:
                     drop.append(i)
         need = -(-end // bs) - len(r.blocks)
-        if need > len(self.free) + sum(1 for i in drop if self.ref[r.blocks[i]] == 1):
+        # a partly filled block that another request holds too is not written:
+        # the request gets a block of its own first, and a copy is noted
+        at = first // bs
+        cow = (num_new_tokens > 0 and first % bs != 0 and r.blocks[at] != self.null_block
+               and self.ref[r.blocks[at]] > 1)
+        if need + cow > len(self.free) + sum(1 for i in drop if self.ref[r.blocks[i]] == 1):
             return None
         if drop:
             freed = [r.blocks[i] for i in drop]
             for i in drop:
                 r.blocks[i] = self.null_block
             self._free_blocks(list(reversed(freed)))
+        if cow:
+            shared, own = r.blocks[at], self._get_new_blocks(1)[0]
+            r.blocks[at] = own
+            self.ref[shared] -= 1
+            self.copies.append((shared, own))
         # phase 3: new blocks for the new tokens
         if need > 0:
             r.blocks.extend(self._get_new_blocks(need))
@@ -207,6 +221,52 @@ class Pool:
                 if r.blocks[i] != self.null_block:
                     self._cache_block(r.blocks[i], h)
         return slots
+
+    def fork_request(self, parent_id, child_id):
+        """the child shares everything the parent has; counts go up."""
+        p = self.reqs[parent_id]
+        assert child_id not in self.reqs
+        c = self.reqs[child_id] = Request(p.tokens)
+        c.blocks = list(p.blocks)
+        c.num_computed = p.num_computed
+        for b in c.blocks:
+            if b != self.null_block:
+                self.ref[b] += 1
+
+    def resize(self, num_blocks) -> bool:
+        """the pool made num_blocks large: blocks in use past the end move, in id
+        order, to the free queue's first blocks below it."""
+        nb = len(self.ref)
+        if num_blocks >= nb:
+            self.free[:0] = list(range(nb, num_blocks))
+            self.ref += [0] * (num_blocks - nb)
+            self.hash += [None] * (num_blocks - nb)
+            return True
+        high = [b for b in range(num_blocks, nb) if self.ref[b] > 0]
+        low = [b for b in self.free if b < num_blocks]
+        if len(high) > len(low):
+            return False
+        to = dict(zip(high, low))
+        for b in self.free:
+            if b >= num_blocks:
+                self._evict_hash(b)
+        for b, c in to.items():
+            self._evict_hash(c)
+            self.ref[c] = self.ref[b]
+            self.hash[c] = self.hash[b]
+            if self.hash[b] is not None:
+                chain = self.map[self.hash[b]]
+                chain[chain.index(b)] = c
+            self.copies.append((b, c))
+        for r in self.reqs.values():
+            r.blocks = [to.get(b, b) for b in r.blocks]
+        self.free = low[len(high):]
+        del self.ref[num_blocks:], self.hash[num_blocks:]
+        return True
+
+    def take_copies(self):
+        out, self.copies = self.copies, []
+        return out
 
     def append_token(self, req_id, token):
         self.reqs[req_id].tokens.append(int(token))

@@ -15,9 +15,11 @@
 //    per-block arrays, so filing and evicting a block allocate nothing;
 //  * a request keeps its token ids, its block ids and the hashes of its full
 //    blocks, extended incrementally as tokens become computed.
+#include <algorithm>
 #include <cstdint>
 #include <new>
 #include <unordered_map>
+#include <utility>
 #include <vector>
 
 #include "pkv_pool.h"
@@ -69,6 +71,10 @@ struct pkv_pool {
   int64_t entries = 0;
   std::vector<int32_t> hnext, hprev;
   std::unordered_map<int64_t, Request> reqs;
+  // noted block copies (from, to), oldest first; those before copies_taken
+  // have been handed over
+  std::vector<std::pair<int32_t, int32_t>> copies;
+  size_t copies_taken = 0;
 
   size_t home(uint64_t key) const {
     return static_cast<size_t>((key * 0x9E3779B97F4A7C15ull) >> shift);
@@ -106,6 +112,22 @@ struct pkv_pool {
     }
     table[i].head = -1;
     --entries;
+  }
+  // Block `to` takes the place of block `from` in the prefix cache (`to` has
+  // no hash).
+  void move_hash(int32_t from, int32_t to) {
+    if (!has_hash[from]) return;
+    Entry& e = table[probe(hash[from])];
+    const int32_t p = hprev[from], n = hnext[from];
+    hprev[to] = p;
+    hnext[to] = n;
+    if (p >= 0) hnext[p] = to;
+    else e.head = to;
+    if (n >= 0) hprev[n] = to;
+    else e.tail = to;
+    hash[to] = hash[from];
+    has_hash[to] = 1;
+    has_hash[from] = 0;
   }
   // First block filed under key, or -1.
   int32_t lookup(uint64_t key) const {
@@ -190,6 +212,21 @@ struct pkv_pool {
     if (--ref[b] == 0) {
       if (has_hash[b]) push_tail(b);
       else push_head(b);
+    }
+  }
+
+  // Whether n more copies can be noted without allocating.
+  bool room_for_copies(size_t n) {
+    try {
+      if (copies_taken == copies.size()) {   // all handed over: start again
+        copies.clear();
+        copies_taken = 0;
+      }
+      if (copies.capacity() - copies.size() < n)
+        copies.reserve(std::max(2 * copies.size(), copies.size() + n));
+      return true;
+    } catch (...) {
+      return false;
     }
   }
 
@@ -318,12 +355,23 @@ int pkv_pool_allocate_slots(pkv_pool* pool, int64_t req_id, int32_t num_new_toke
       }
   }
   const int64_t need = (end + bs - 1) / bs - static_cast<int64_t>(r.blocks.size());
-  if (need > pool->num_free + freeable) return PKV_POOL_NO_SPACE;
+  // a partly filled block that a fork shares: a block of its own, and a copy
+  const size_t open = static_cast<size_t>(first / bs);
+  const bool cow = num_new_tokens > 0 && first % bs != 0 && open < r.blocks.size() &&
+                   r.blocks[open] != pool->null_block && pool->ref[r.blocks[open]] > 1;
+  if (need + (cow ? 1 : 0) > pool->num_free + freeable) return PKV_POOL_NO_SPACE;
+  if (cow && !pool->room_for_copies(1)) return PKV_E_MEMORY;
   // released last to first, replaced by the null block
   for (size_t k = drop.size(); k-- > 0;) {
     const int32_t b = r.blocks[drop[k]];
     r.blocks[drop[k]] = pool->null_block;
     pool->release(b);
+  }
+  if (cow) {
+    const int32_t shared = r.blocks[open];
+    r.blocks[open] = pool->get_new_block();
+    pool->copies.emplace_back(shared, r.blocks[open]);
+    pool->release(shared);
   }
   // phase 3: new blocks for the new tokens
   for (int64_t i = 0; i < need; ++i) r.blocks.push_back(pool->get_new_block());
@@ -361,6 +409,105 @@ int pkv_pool_allocate_slots_batch(pkv_pool* pool, const int64_t* req_ids,
     off += num_new_tokens[i];
     *num_done = i + 1;
   }
+  return PKV_OK;
+}
+
+int pkv_pool_fork_request(pkv_pool* pool, int64_t parent_id, int64_t child_id) {
+  if (!pool) return PKV_E_NULL;
+  auto it = pool->reqs.find(parent_id);
+  if (it == pool->reqs.end() || pool->reqs.count(child_id)) return PKV_E_REQUEST;
+  try {
+    Request child = it->second;
+    it = pool->reqs.emplace(child_id, std::move(child)).first;
+  } catch (...) {
+    return PKV_E_MEMORY;
+  }
+  for (int32_t b : it->second.blocks)
+    if (b != pool->null_block) pool->touch(b);
+  return PKV_OK;
+}
+
+int pkv_pool_resize(pkv_pool* pool, int32_t num_blocks) {
+  if (!pool) return PKV_E_NULL;
+  if (num_blocks < 1) return PKV_E_SHAPE;
+  const int32_t nb = pool->nb;
+  if (num_blocks == nb) return PKV_OK;
+  const int32_t keep = std::min(nb, num_blocks);
+  // what may fail comes first: the moves (old id -> new id), the free queue of
+  // the new pool and the arrays' room
+  std::vector<int32_t> moved, queue;
+  try {
+    moved.assign(nb, -1);
+    queue.reserve(num_blocks);
+    for (int32_t b = num_blocks - 1; b >= nb; --b) queue.push_back(b);   // (head last)
+    std::reverse(queue.begin(), queue.end());
+    int32_t src = keep, moves = 0;
+    auto next_high = [&]() {   // the next block in use past the new end
+      while (src < nb && pool->ref[src] == 0) ++src;
+      return src < nb ? src++ : -1;
+    };
+    int32_t high = next_high();
+    for (int32_t b = pool->next[nb]; b != nb; b = pool->next[b]) {
+      if (b >= keep) continue;
+      if (high >= 0) {
+        moved[high] = b;
+        ++moves;
+        high = next_high();
+      } else {
+        queue.push_back(b);
+      }
+    }
+    if (high >= 0) return PKV_POOL_NO_SPACE;
+    if (!pool->room_for_copies(moves)) return PKV_E_MEMORY;
+    pool->ref.reserve(num_blocks);
+    pool->prev.reserve(static_cast<size_t>(num_blocks) + 1);
+    pool->next.reserve(static_cast<size_t>(num_blocks) + 1);
+    pool->in_free.reserve(num_blocks);
+    pool->has_hash.reserve(num_blocks);
+    pool->hash.reserve(num_blocks);
+    pool->hnext.reserve(num_blocks);
+    pool->hprev.reserve(num_blocks);
+  } catch (...) {
+    return PKV_E_MEMORY;
+  }
+  for (int32_t b = keep; b < nb; ++b) {
+    const int32_t to = moved[b];
+    if (to < 0) {   // free: out of the cache
+      pool->evict_hash(b);
+      continue;
+    }
+    pool->evict_hash(to);
+    pool->ref[to] = pool->ref[b];
+    pool->move_hash(b, to);
+    pool->copies.emplace_back(b, to);
+  }
+  for (auto& kv : pool->reqs)
+    for (int32_t& b : kv.second.blocks)
+      if (b >= keep) b = moved[b];
+  pool->ref.resize(num_blocks, 0);
+  pool->in_free.assign(num_blocks, 0);
+  pool->has_hash.resize(num_blocks, 0);
+  pool->hash.resize(num_blocks, 0);
+  pool->hnext.resize(num_blocks, -1);
+  pool->hprev.resize(num_blocks, -1);
+  pool->nb = num_blocks;
+  pool->prev.assign(static_cast<size_t>(num_blocks) + 1, num_blocks);
+  pool->next.assign(static_cast<size_t>(num_blocks) + 1, num_blocks);
+  pool->num_free = 0;
+  for (int32_t b : queue) pool->push_tail(b);
+  return PKV_OK;
+}
+
+int pkv_pool_take_copies(pkv_pool* pool, int32_t* pairs, int32_t capacity, int32_t* num_pairs) {
+  if (!pool || !num_pairs || (capacity > 0 && !pairs)) return PKV_E_NULL;
+  if (capacity < 0) return PKV_E_SHAPE;
+  const size_t n = std::min(pool->copies.size() - pool->copies_taken, static_cast<size_t>(capacity));
+  for (size_t i = 0; i < n; ++i) {
+    pairs[2 * i] = pool->copies[pool->copies_taken + i].first;
+    pairs[2 * i + 1] = pool->copies[pool->copies_taken + i].second;
+  }
+  pool->copies_taken += n;
+  *num_pairs = static_cast<int32_t>(n);
   return PKV_OK;
 }
 

@@ -7,6 +7,7 @@ calls raise: there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -402,36 +403,54 @@ def attention_static_scratch(out, q, k_cache, v_cache, block_tables, context_len
         float(scale), ctypes.byref(desc), ctypes.byref(meta), _stream(stream)))
 
 
-def _int8_cache(k_cache, v_cache, k_scales, v_scales) -> CacheDesc:
-    """Checks the caches and scales of an int8 cache against each other."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _require(t, n, dtype=torch.int8, ndim=4)
-    if k_cache.shape != v_cache.shape:
-        raise PkvError("k_cache and v_cache must have the same shape")
-    want = (k_cache.shape[0], k_cache.shape[2])
-    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-        _require(t, n, dtype=torch.float32, ndim=2)
-        if t.shape != want:
-            raise PkvError(f"{n} must be [num_blocks, num_kv_heads]")
-    return cache_desc(k_cache)
-
-
-def _batch(block_tables, context_lens, query_start_loc) -> None:
-    """Checks the batch's metadata arrays against each other."""
-    _require(block_tables, "block_tables", dtype=torch.int32, ndim=2)
-    _require(context_lens, "context_lens", dtype=torch.int32, ndim=1)
-    _require(query_start_loc, "query_start_loc", dtype=torch.int32, ndim=1)
-    S = context_lens.shape[0]
-    if block_tables.shape[0] < S or query_start_loc.shape[0] < S + 1:
-        raise PkvError("block_tables needs num_seqs rows, query_start_loc num_seqs + 1 entries")
-
-
-def _same_device(*tensors) -> None:
-    """Every tensor on the current device: the kernels run there."""
-    dev = torch.cuda.current_device()
+def _all_on(dev: int, dtype, *tensors) -> bool:
+    """Whether every tensor is a contiguous one of `dtype` on CUDA device `dev`."""
     for t in tensors:
-        if t.device.index != dev:
-            raise PkvError(f"tensors must be on the current CUDA device ({dev})")
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
+
+
+def _refuse(dev: int, **tensors) -> None:
+    """Says what is wrong with the first tensor (name=(tensor, dtype)) that
+    _all_on did not take."""
+    for name, (t, dtype) in tensors.items():
+        _require(t, name, dtype=dtype)
+        if t.get_device() != dev:
+            raise PkvError(f"{name} must be on the current CUDA device ({dev})")
+
+
+def _current_device() -> int:
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):   # no driver, or a torch without CUDA
+        return -2                            # (no tensor is there)
+
+
+def _int8_batch(dev, k_cache, v_cache, block_tables, context_lens, query_start_loc, k_scales,
+                v_scales, **rows) -> None:
+    """Checks the tensors of an int8 call one by one against each other (the
+    rows bf16, by name); the calls make the same checks in one go first, since a
+    decode step's kernel is over in microseconds."""
+    bf16, i32, i8, f32 = torch.bfloat16, torch.int32, torch.int8, torch.float32
+    _refuse(dev, **{n: (t, bf16) for n, t in rows.items()}, k_cache=(k_cache, i8),
+            v_cache=(v_cache, i8), block_tables=(block_tables, i32),
+            context_lens=(context_lens, i32), query_start_loc=(query_start_loc, i32),
+            k_scales=(k_scales, f32), v_scales=(v_scales, f32))
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise PkvError("k_cache and v_cache must both be [num_blocks, 16, num_kv_heads, head_size]")
+    for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t.shape != (k_cache.shape[0], k_cache.shape[2]):
+            raise PkvError(f"{n} must be [num_blocks, num_kv_heads]")
+    if block_tables.dim() != 2 or context_lens.dim() != 1 or query_start_loc.dim() != 1 or \
+            block_tables.shape[0] < context_lens.shape[0] or \
+            query_start_loc.shape[0] < context_lens.shape[0] + 1:
+        raise PkvError("block_tables [num_seqs, stride], context_lens [num_seqs] and "
+                       "query_start_loc [num_seqs + 1] must fit together")
+    one, two = rows.values()
+    if one.dim() != 3 or one.shape != two.shape or one.shape[2] != k_cache.shape[3] or \
+            ("k" in rows and one.shape[1] != k_cache.shape[2]):
+        raise PkvError(" and ".join(rows) + " must both be [num_tokens, heads, head_size]")
 
 
 def write_int8(k, v, block_tables, context_lens, query_start_loc, k_cache, v_cache, k_scales,
@@ -439,27 +458,44 @@ def write_int8(k, v, block_tables, context_lens, query_start_loc, k_cache, v_cac
     """pkv_write_int8: the batch's bf16 rows k/v [T, Hkv, D] into the int8
     caches at the sequences' last positions, making the scales fp32
     [num_blocks, Hkv] of the blocks they touch."""
-    lib = load()
-    desc = _int8_cache(k_cache, v_cache, k_scales, v_scales)
-    for t, n in ((k, "k"), (v, "v")):
-        _require(t, n, dtype=torch.bfloat16, ndim=3)
-        if t.shape != (k.shape[0], desc.num_kv_heads, desc.head_size):
-            raise PkvError("k and v must be [num_tokens, num_kv_heads, head_size]")
-    _batch(block_tables, context_lens, query_start_loc)
-    _same_device(k, v, block_tables, context_lens, query_start_loc, k_cache, v_cache, k_scales,
-                 v_scales)
-    meta = AttnMeta(context_lens.shape[0], k.shape[0], desc.num_kv_heads, block_tables.shape[1],
-                    int(max_query_len), 0, -1, 0, 0)
-    _check(lib.pkv_write_int8(k.data_ptr(), v.data_ptr(), block_tables.data_ptr(),
-                              context_lens.data_ptr(), query_start_loc.data_ptr(),
-                              k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
-                              v_scales.data_ptr(), ctypes.byref(desc), ctypes.byref(meta),
-                              _stream(stream)))
+    lib = _lib or load()
+    dev = _current_device()
+    if not (_all_on(dev, torch.bfloat16, k, v) and _all_on(dev, torch.int8, k_cache, v_cache)
+            and _all_on(dev, torch.int32, block_tables, context_lens, query_start_loc)
+            and _all_on(dev, torch.float32, k_scales, v_scales)
+            and _int8_shapes(k, v, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                             k_scales, v_scales) and k.shape[1] == k_cache.shape[2]):
+        _int8_batch(dev, k_cache, v_cache, block_tables, context_lens, query_start_loc, k_scales,
+                    v_scales, k=k, v=v)
+    nb, bs, hkv, d = k_cache.shape
+    desc = CacheDesc(nb, bs, hkv, d, PKV_INT8)
+    meta = AttnMeta(context_lens.shape[0], k.shape[0], hkv, block_tables.shape[1], max_query_len,
+                    0, -1, 0, 0)
+    st = lib.pkv_write_int8(k.data_ptr(), v.data_ptr(), block_tables.data_ptr(),
+                            context_lens.data_ptr(), query_start_loc.data_ptr(),
+                            k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(),
+                            v_scales.data_ptr(), desc, meta, _stream_on(dev, stream))
+    if st != 0:
+        _check(st)
+
+
+def _int8_shapes(x, y, k_cache, v_cache, block_tables, context_lens, query_start_loc, k_scales,
+                 v_scales) -> bool:
+    """Whether the shapes of an int8 call's tensors fit (see _int8_batch)."""
+    c, t, S = k_cache.shape, block_tables.shape, context_lens.shape
+    return (len(c) == 4 and v_cache.shape == c and k_scales.shape == v_scales.shape
+            == (c[0], c[2]) and len(x.shape) == 3 and x.shape == y.shape and x.shape[2] == c[3]
+            and len(S) == 1 and len(t) == 2 and t[0] >= S[0] and query_start_loc.dim() == 1
+            and query_start_loc.shape[0] > S[0])
+
+
+def _stream_on(dev: int, stream) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
 
 
 def workspace_size_int8(k_cache, meta: AttnMeta) -> int:
     desc = cache_desc(k_cache)
-    n = load().pkv_attention_int8_workspace_size(ctypes.byref(desc), ctypes.byref(meta))
+    n = load().pkv_attention_int8_workspace_size(desc, meta)
     if n == ctypes.c_size_t(-1).value:
         raise PkvError("invalid attention description")
     return int(n)
@@ -471,63 +507,67 @@ def attention_int8(out, q, k_cache, v_cache, block_tables, context_lens, query_s
     """pkv_attention_int8 into ``out`` [T, Hq, D] (bf16) over int8 caches with
     the scales write_int8 made.  ``workspace`` (uint8 CUDA tensor of
     workspace_size_int8 bytes) is allocated here when not given and needed."""
-    lib = load()
-    desc = _int8_cache(k_cache, v_cache, k_scales, v_scales)
-    for t, n in ((out, "out"), (q, "q")):
-        _require(t, n, dtype=torch.bfloat16, ndim=3)
-    if out.shape != q.shape or q.shape[2] != desc.head_size:
-        raise PkvError("out and q must be [num_tokens, num_q_heads, head_size]")
-    _batch(block_tables, context_lens, query_start_loc)
-    _same_device(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, k_scales,
-                 v_scales)
-    meta = attn_meta(q, block_tables, context_lens, max_query_len=max_query_len,
-                     max_context_len=max_context_len, num_decode_seqs=num_decode_seqs,
-                     kv_split_tokens=kv_split_tokens, sliding_window=sliding_window)
-    if workspace is None:
-        need = lib.pkv_attention_int8_workspace_size(ctypes.byref(desc), ctypes.byref(meta))
-        if need == ctypes.c_size_t(-1).value:
-            need = 0   # (the call itself says what is wrong)
-        if need:
-            if stream is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            else:      # scratch of the stream that uses it
-                with torch.cuda.stream(stream):
-                    workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    lib = _lib or load()
+    dev = _current_device()
+    if not (_all_on(dev, torch.bfloat16, out, q) and _all_on(dev, torch.int8, k_cache, v_cache)
+            and _all_on(dev, torch.int32, block_tables, context_lens, query_start_loc)
+            and _all_on(dev, torch.float32, k_scales, v_scales)
+            and _int8_shapes(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                             k_scales, v_scales)):
+        _int8_batch(dev, k_cache, v_cache, block_tables, context_lens, query_start_loc, k_scales,
+                    v_scales, out=out, q=q)
+    nb, bs, hkv, d = k_cache.shape
+    T, hq, _ = q.shape
+    desc = CacheDesc(nb, bs, hkv, d, PKV_INT8)
+    meta = AttnMeta(context_lens.shape[0], T, hq, block_tables.shape[1], max_query_len,
+                    max_context_len, num_decode_seqs, sliding_window, kv_split_tokens)
     ws_ptr, ws_bytes = 0, 0
-    if workspace is not None:
-        _require(workspace, "workspace")
-        _same_device(workspace)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib.pkv_attention_int8(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
-                                  v_cache.data_ptr(), block_tables.data_ptr(),
-                                  context_lens.data_ptr(), query_start_loc.data_ptr(),
-                                  float(scale), k_scales.data_ptr(), v_scales.data_ptr(),
-                                  ctypes.byref(desc), ctypes.byref(meta), ws_ptr, ws_bytes,
-                                  _stream(stream)))
+    if workspace is None:
+        ws_bytes = lib.pkv_attention_int8_workspace_size(desc, meta)
+        if ws_bytes == ctypes.c_size_t(-1).value:
+            ws_bytes = 0   # (the call itself says what is wrong)
+        elif ws_bytes:
+            if stream is None:
+                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            else:          # scratch of the stream that uses it
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+            ws_ptr = workspace.data_ptr()
+    else:
+        _refuse(dev, workspace=(workspace, None))
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    st = lib.pkv_attention_int8(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+                                v_cache.data_ptr(), block_tables.data_ptr(),
+                                context_lens.data_ptr(), query_start_loc.data_ptr(), scale,
+                                k_scales.data_ptr(), v_scales.data_ptr(), desc, meta, ws_ptr,
+                                ws_bytes, _stream_on(dev, stream))
+    if st != 0:
+        _check(st)
 
 
 def copy_blocks(buffers, pairs, stream=None) -> None:
     """pkv_copy_blocks: copies whole blocks of every buffer (CUDA tensors
     [num_blocks, ...]: the K and V caches and scales of all layers) along
     ``pairs`` (host ints [n, 2]: from, to), in order."""
-    lib = load()
+    lib = _lib or load()
     pairs = np.ascontiguousarray(pairs, dtype=np.int32)
-    if pairs.size == 0:
+    if pairs.size == 0 or len(buffers) == 0:
         return
     if pairs.ndim != 2 or pairs.shape[1] != 2:
         raise PkvError("pairs must be [n, 2] (from, to)")
-    n = len(buffers)
-    if n == 0:
-        return
-    nb = buffers[0].shape[0]
+    dev = _current_device()
+    nb = buffers[0].shape[0] if buffers[0].dim() else 0
     for t in buffers:
-        if not (t.is_cuda and t.is_contiguous() and t.dim() >= 1 and t.shape[0] == nb):
-            raise PkvError("buffers must be contiguous CUDA tensors of the same number of blocks")
-    _same_device(*buffers)
-    ptrs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in buffers])
-    page = (ctypes.c_int64 * n)(*[t.nbytes // max(nb, 1) for t in buffers])
-    _check(lib.pkv_copy_blocks(ptrs, page, n, nb, pairs.ctypes.data, pairs.shape[0],
-                               _stream(stream)))
+        if t.get_device() != dev or not t.is_contiguous() or t.dim() == 0 or t.shape[0] != nb:
+            _refuse(dev, buffers=(t, None))
+            raise PkvError("buffers must all be [num_blocks, ...] of the same number of blocks")
+    # (arrays of the C call: pointers and bytes of a page)
+    ptrs = array.array("Q", [t.data_ptr() for t in buffers])
+    page = array.array("q", [t.nbytes // nb for t in buffers] if nb else [0] * len(buffers))
+    st = lib.pkv_copy_blocks(ptrs.buffer_info()[0], page.buffer_info()[0], len(buffers), nb,
+                             pairs.ctypes.data, pairs.shape[0], _stream_on(dev, stream))
+    if st != 0:
+        _check(st)
 
 
 def get_error(clear: bool = True) -> int:

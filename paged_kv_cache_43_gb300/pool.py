@@ -15,7 +15,8 @@ EXPORTED = ("pkv_pool_create", "pkv_pool_destroy", "pkv_pool_num_free", "pkv_poo
             "pkv_pool_num_cached", "pkv_pool_add_request", "pkv_pool_append_tokens",
             "pkv_pool_append_token_batch",
             "pkv_pool_admit", "pkv_pool_allocate_slots", "pkv_pool_allocate_slots_batch",
-            "pkv_pool_free_request",
+            "pkv_pool_free_request", "pkv_pool_fork_request", "pkv_pool_resize",
+            "pkv_pool_take_copies",
             "pkv_pool_block_table", "pkv_pool_build_block_tables", "pkv_pool_num_computed",
             "pkv_pool_block_state", "pkv_pool_free_queue")
 
@@ -41,6 +42,9 @@ def _lib():
             "pkv_pool_allocate_slots": (ctypes.c_int, [vp, i64, i32, i32, P64]),
             "pkv_pool_allocate_slots_batch": (ctypes.c_int, [vp, P64, P32, i32, i32, P64, P32]),
             "pkv_pool_free_request": (ctypes.c_int, [vp, i64]),
+            "pkv_pool_fork_request": (ctypes.c_int, [vp, i64, i64]),
+            "pkv_pool_resize": (ctypes.c_int, [vp, i32]),
+            "pkv_pool_take_copies": (ctypes.c_int, [vp, P32, i32, P32]),
             "pkv_pool_block_table": (ctypes.c_int, [vp, i64, P32, i32, P32]),
             "pkv_pool_build_block_tables": (ctypes.c_int, [vp, P64, i32, P32, i32]),
             "pkv_pool_num_computed": (ctypes.c_int, [vp, i64, P32]),
@@ -137,6 +141,27 @@ class BlockPool:
 
     def free_request(self, req_id: int):
         self._check(self._lib.pkv_pool_free_request(self._p, int(req_id)))
+
+    def fork_request(self, parent_id: int, child_id: int):
+        """child_id: a new request that shares the parent's tokens and blocks."""
+        self._check(self._lib.pkv_pool_fork_request(self._p, int(parent_id), int(child_id)))
+
+    def resize(self, num_blocks: int) -> bool:
+        """Makes the pool larger or smaller; False (and no change) when the
+        blocks in use do not fit.  The moves are among take_copies()."""
+        return self._check(self._lib.pkv_pool_resize(self._p, int(num_blocks))) != NO_SPACE
+
+    def take_copies(self) -> np.ndarray:
+        """int32 [n, 2] (from, to): the block copies noted since the last call,
+        for pkv.copy_blocks before the next KV write."""
+        parts, n = [], ctypes.c_int32(256)
+        while n.value == 256:
+            part = np.empty((256, 2), dtype=np.int32)
+            self._check(self._lib.pkv_pool_take_copies(
+                self._p, part.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), 256,
+                ctypes.byref(n)))
+            parts.append(part[:n.value])
+        return parts[0] if len(parts) == 1 else np.concatenate(parts)
 
     def block_table(self, req_id: int):
         n = ctypes.c_int32(0)
