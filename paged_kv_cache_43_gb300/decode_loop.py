@@ -16,6 +16,12 @@ tables — or, for a decode-only step whose requests share leading blocks and
 when pkv_use_cascade says it pays ("Implémentation du cœur ... vLLM", ch. 6:
 the scheduler's common_prefix_len feeding use_cascade), cascade attention.
 
+The loop also runs over an int8 cache (dtype=torch.int8: pkv_write_int8 and
+pkv_attention_int8, a scale for each block and kv head, q and out in bf16),
+forks running requests (fork_request: parallel sampling from one prefix, the
+pool's copy on write carried out by pkv_copy_blocks before the step's write)
+and changes the caches' size between steps (resize).
+
 There is no model: a token's q, k and v rows are a fixed function of (token
 id, position) — rows of seeded N(0, 1) tables summed in fp32 and rounded to
 the cache dtype — which is the one property of real K/V that prefix caching
@@ -61,6 +67,7 @@ class Step:
     preempted: list = field(default_factory=list)
     finished: list = field(default_factory=list)
     cascade_blocks: int = 0                         # > 0: cascade over this prefix
+    copies: np.ndarray | None = None                # block copies made before the write
 
 
 class DecodeLoop:
@@ -71,6 +78,10 @@ class DecodeLoop:
         self.pool = BlockPool(num_blocks, 16, caching)
         self.hq, self.hkv, self.d = num_q_heads, num_kv_heads, head_size
         self.dtype, self.device, self.window = dtype, torch.device(device), window
+        self.int8 = dtype == torch.int8
+        if self.int8 and use_cascade:
+            raise ValueError("cascade attention does not take int8 caches")
+        self.row_dtype = torch.bfloat16 if self.int8 else dtype
         self.max_batch_tokens = max_batch_tokens
         self.scale = scale if scale is not None else 1.0 / float(np.sqrt(head_size))
         g = torch.Generator().manual_seed(seed)
@@ -79,22 +90,56 @@ class DecodeLoop:
         self.pq, self.pk, self.pv = tab(max_pos, num_q_heads), tab(max_pos, num_kv_heads), tab(max_pos, num_kv_heads)
         self.vocab, self.seed = vocab, seed
         self.use_cascade = use_cascade
-        shape = (num_blocks, 16, num_kv_heads, head_size)
-        self.k_cache = torch.full(shape, float("nan"), dtype=dtype, device=self.device)
-        self.v_cache = torch.full(shape, float("nan"), dtype=dtype, device=self.device)
+        self.k_cache, self.v_cache, *self.scales = self._new_caches(num_blocks)
         self.waiting: deque = deque()
         self.running: list = []
         self._next_id = 0
         self._order = 0
 
+    # ---------------------------------------------------------------- caches
+    def _new_caches(self, num_blocks):
+        """K and V caches (and, int8, their scales) with nothing valid in them."""
+        shape = (num_blocks, 16, self.hkv, self.d)
+        if not self.int8:
+            return [torch.full(shape, float("nan"), dtype=self.dtype, device=self.device)
+                    for _ in range(2)]
+        return ([torch.zeros(shape, dtype=torch.int8, device=self.device) for _ in range(2)]
+                + [torch.full((num_blocks, self.hkv), float("nan"), device=self.device)
+                   for _ in range(2)])
+
+    def buffers(self):
+        """Everything a block holds, for pkv.copy_blocks."""
+        return [self.k_cache, self.v_cache, *self.scales]
+
+    def _make_copies(self):
+        """Carries out the block copies the pool has noted (before the write)."""
+        pairs = self.pool.take_copies()
+        if len(pairs):
+            pkv.copy_blocks(self.buffers(), pairs)
+        return pairs
+
+    def resize(self, num_blocks: int) -> bool:
+        """Changes the caches' size between steps: blocks in use move below the
+        new end, then the caches are reallocated.  False when they do not fit."""
+        if not self.pool.resize(num_blocks):
+            return False
+        self._make_copies()
+        old, new = self.buffers(), self._new_caches(num_blocks)
+        n = min(num_blocks, old[0].shape[0])
+        for a, b in zip(old, new):
+            b[:n].copy_(a[:n])
+        self.k_cache, self.v_cache, *self.scales = new
+        return True
+
     # ------------------------------------------------------------------ rows
     def rows(self, token_ids, positions):
-        """q, k, v rows of (token, position) pairs, in the cache dtype (host)."""
+        """q, k, v rows of (token, position) pairs, in the cache dtype (bf16 for
+        an int8 cache; host)."""
         t = torch.as_tensor(token_ids, dtype=torch.long)
         p = torch.as_tensor(positions, dtype=torch.long)
-        q = (self.tq[t] + self.pq[p]).to(self.dtype)
-        k = (self.tk[t] + self.pk[p]).to(self.dtype)
-        v = (self.tv[t] + self.pv[p]).to(self.dtype)
+        q = (self.tq[t] + self.pq[p]).to(self.row_dtype)
+        k = (self.tk[t] + self.pk[p]).to(self.row_dtype)
+        v = (self.tv[t] + self.pv[p]).to(self.row_dtype)
         return q, k, v
 
     # -------------------------------------------------------------- requests
@@ -103,6 +148,24 @@ class DecodeLoop:
         self._next_id += 1
         self.waiting.append(Req(rid, [int(x) for x in prompt], int(max_new_tokens)))
         return rid
+
+    def fork_request(self, rid: int) -> int:
+        """A new request that goes on from where `rid` stands (its prompt, what
+        it has generated, its blocks), sampling on its own."""
+        new = self._next_id
+        for r in self.running:
+            if r.rid == rid:
+                self.pool.fork_request(rid, new)
+                self._order += 1
+                self.running.append(Req(new, list(r.tokens), r.max_new, r.generated, self._order))
+                break
+        else:
+            r = next((r for r in self.waiting if r.rid == rid), None)
+            if r is None:
+                raise KeyError(f"no request {rid}")
+            self.waiting.append(Req(new, list(r.tokens), r.max_new, r.generated))
+        self._next_id += 1
+        return new
 
     def _preempt(self, r: Req):
         """recompute preemption: blocks back to the pool, request back in front."""
@@ -189,7 +252,12 @@ class DecodeLoop:
         nd = 0
         while nd < len(q_lens) and q_lens[nd] == 1:
             nd += 1
-        pkv.write(k, v, sm, self.k_cache, self.v_cache)
+        copies = self._make_copies()
+        if self.int8:
+            pkv.write_int8(k, v, bt, cl, qsl, self.k_cache, self.v_cache, *self.scales,
+                           max_query_len=max(q_lens))
+        else:
+            pkv.write(k, v, sm, self.k_cache, self.v_cache)
         casc = 0
         if self.use_cascade and nd == len(q_lens) and self.window == 0:
             # leading blocks every row of the step shares (the common prefix)
@@ -203,6 +271,10 @@ class DecodeLoop:
         if casc:
             pkv.attention_cascade(out, q, self.k_cache, self.v_cache, bt, cl, qsl, self.scale,
                                   casc, max_context_len=max(ctx))
+        elif self.int8:
+            pkv.attention_int8(out, q, self.k_cache, self.v_cache, bt, cl, qsl, self.scale,
+                               *self.scales, max_query_len=max(q_lens), max_context_len=max(ctx),
+                               num_decode_seqs=nd, sliding_window=self.window)
         else:
             pkv.attention(out, q, self.k_cache, self.v_cache, bt, cl, qsl, self.scale,
                           max_query_len=max(q_lens), max_context_len=max(ctx),
@@ -221,4 +293,4 @@ class DecodeLoop:
                 self.pool.free_request(r.rid)
                 self.running.remove(r)
         return Step(ids, q_lens, sm, bt, cl, qsl, q, k, v, out, [s[1] for s in sched],
-                    preempted, finished, casc)
+                    preempted, finished, casc, copies)
