@@ -64,9 +64,10 @@
 //    is at most 2^8 whatever the scales are, and the row sum divides it out
 //    again (per block, in fp32).  Both cost nothing per element: they are the
 //    factor and the addend of the exponent's one FMA, per block of 16 keys
-//    instead of per tile.  Each softmax warp fetches its tiles' 8 + 8 scales
-//    itself, ids two tiles and scales one tile ahead, and hands them round by
-//    shuffles.  Every code is finite, so rows no key may see need no zeroing.
+//    instead of per tile.  Warp 9 fetches each tile's 8 + 8 scales (ids two
+//    tiles and scales one tile ahead) into a ring in shared memory that the
+//    softmax warps read by broadcast loads.  Every code is finite, so rows no
+//    key may see need no zeroing.
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 #include "pkv_tc.cuh"
@@ -83,8 +84,8 @@ constexpr int kTcTiles = 2;       // query tiles per CTA
 constexpr int kTcKeys = 128;      // keys per K/V tile
 // Warps: 0-3 softmax of query tile 0, 4-7 of query tile 1 (warpgroups 0 and
 // 1: warp w reads TMEM lanes 32 (w % 4) ..), 8 the K producer (and the V
-// producer with an FP8 cache), 9 TMEM allocation, 10 the V producer (bf16) or
-// a widener (FP8), 11 a widener (FP8, D = 128; idle otherwise).  The launch
+// producer with an FP8 cache), 9 TMEM allocation (and the block scales of an
+// int8 cache), 10 the V producer (bf16) or a widener (FP8), 11 a widener (FP8, D = 128; idle otherwise).  The launch
 // gives each thread 168 registers; warpgroup 2 then hands registers back so
 // that the softmax warpgroups run at 208 (2 x 128 x 208 + 128 x 80 =
 // 384 x 168).
@@ -119,6 +120,8 @@ struct TcLayout {
   static constexpr int kTileBytes = kHalves * kKvHalf;  // one K (or V) tile
 };
 
+constexpr int kScaleRing = 4;   // int8: key tiles whose block scales are held
+
 struct TcShared {
   uint64_t q_full, q_conv;
   uint64_t drain[kTcTiles];   // each tile's issuer: all its products complete
@@ -129,6 +132,10 @@ struct TcShared {
   uint32_t tmem_base;
   int32_t abort;
   int32_t n_issued[2];   // bf16 producers: K / V tiles issued, for the drain
+  // Int8: block b of key tile j has (K scale, log2 of the V scale, 1 / V scale)
+  // in sc[j % kScaleRing][b].
+  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
+  alignas(16) float4 sc[kScaleRing][kTcKeys / kBlock];
 };
 
 template <int D>
@@ -504,6 +511,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(smem_u32(&sh->kv_empty[i]), issuers);
       mbar_init(smem_u32(&sh->kv_land[i]), 1);
     }
+    if constexpr (I8)
+      for (int i = 0; i < kScaleRing; ++i) {
+        mbar_init(smem_u32(&sh->sc_full[i]), 1);
+        mbar_init(smem_u32(&sh->sc_empty[i]), 4 * issuers);   // the softmax warps
+      }
     sh->abort = 0;
     fence_barrier_init();
   }
@@ -719,6 +731,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (warp == 8 && lane == 0) (void)mbar_wait(q_full, 0);   // the query tiles too
     __syncwarp();
+   } else if (I8 && warp == 9) {
+    // -------------------------------------------------- block scales (int8)
+    const int32_t* bt = a.block_tables + static_cast<int64_t>(s) * a.bt_stride;
+    const float* scales = (lane & 8) ? a.v_scales : a.k_scales;
+    auto id_of = [&](int j) {
+      const int b = (j0 + j) * (kTcKeys / kBlock) + (lane & 7);
+      return lane < 16 && b >= b_lo && b < nblk ? __ldg(bt + b) : -1;
+    };
+    auto scale_of = [&](int id) {   // (a block that is not read: any finite scale)
+      return id >= 0 && id < a.num_blocks
+                 ? __ldg(scales + static_cast<int64_t>(id) * a.num_kv_heads + kvh) : 1.f;
+    };
+    float next = scale_of(id_of(0));
+    int id_next = id_of(1);
+    for (int j = 0; j < n_rel; ++j) {
+      const int st = j % kScaleRing;
+      const float now = int8_scale(next);
+      next = scale_of(id_next);
+      id_next = id_of(j + 2);
+      const float lv = log2f(__shfl_sync(0xffffffffu, now, 8 + (lane & 7)));
+      if (j >= kScaleRing && !warp_wait(smem_u32(&sh->sc_empty[st]), (j / kScaleRing - 1) & 1, abort,
+                                        a.err, wlim))
+        break;
+      if (lane < 8) sh->sc[st][lane] = make_float4(now, lv, ex2(-lv), 0.f);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh->sc_full[st]));
+    }
    } else if (FP8 && (warp == 10 || (D == 128 && warp == 11))) {
     // ------------------------------------------------- widen e4m3 tiles (FP8)
     // Ring elements in order, so that each wait on a slot's kv_land is for
@@ -791,9 +830,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int ex = I8 ? f16_fit_exponent(amax) : f16_row_exponent(amax);
         float down = pow2f(-ex);
         sl2 *= pow2f(ex);
-        if (I8 && sl2 < 0.f) {   // a negative scale: its sign goes to the query
-          sl2 = -sl2;
-          down = -down;
+        if (I8) {
+          if (sl2 < 0.f) {   // a negative scale: its sign goes to the query
+            sl2 = -sl2;
+            down = -down;
+          }
+          // scores this small are zero; a factor sl2 * K scale (>= 2^-60) that
+          // is itself above zero keeps a masked -inf what it is
+          sl2 = fmaxf(sl2, 0x1p-66f);
         }
 #pragma unroll
         for (int h = 0; h < Lt::kHalves; ++h)
@@ -811,23 +855,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     float m_used = -INFINITY, l = 0.f;
     bool done = t < ntq;
-    // Int8: block scales of key tile j in lanes 0-7 (K) and 8-15 (V).
-    const int32_t* i8_bt = a.block_tables + static_cast<int64_t>(s) * a.bt_stride;
-    const float* i8_scales = (lane & 8) ? a.v_scales : a.k_scales;
-    auto i8_id = [&](int j) {
-      const int b = (j0 + j) * (kTcKeys / kBlock) + (lane & 7);
-      return lane < 16 && b >= b_lo && b < nblk ? __ldg(i8_bt + b) : -1;
-    };
-    auto i8_scale = [&](int id) {   // (a block that is not read: any finite scale)
-      return id >= 0 && id < a.num_blocks
-                 ? __ldg(i8_scales + static_cast<int64_t>(id) * a.num_kv_heads + kvh) : 1.f;
-    };
-    float i8_next = 1.f;
-    int i8_id_next = -1;
-    if constexpr (I8) {
-      i8_next = i8_scale(i8_id(0));
-      i8_id_next = i8_id(1);
-    }
     // first key this row sees (its window; after the shared prefix in a
     // cascade suffix launch)
     const int lo = max(a.window > 0 ? pos - a.window + 1 : 0, a.key_begin);
@@ -897,19 +924,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int c = 0; c < kTcKeys; ++c) x[c] = c < nvis ? x[c] : -INFINITY;
         }
       }
-      [[maybe_unused]] float i8_now = 1.f;   // K scale, or log2 of the V scale, of block lane % 8
+      [[maybe_unused]] const float4* i8_sc = sh->sc[j % kScaleRing];
       if constexpr (I8) {
-        i8_now = int8_scale(i8_next);
-        i8_now = (lane & 8) ? log2f(i8_now) : i8_now;
-        i8_next = i8_scale(i8_id_next);
-        i8_id_next = i8_id(j + 2);
+        if (!warp_wait(smem_u32(&sh->sc_full[j % kScaleRing]), (j / kScaleRing) & 1, abort, a.err,
+                       wlim)) {
+          done = false;
+          break;
+        }
       }
-      // a block's score factor; kept above zero for the masked -inf
-      auto i8_factor = [&](int b) {
-        const float f = __shfl_sync(0xffffffffu, i8_now, b) * sl2;
-        return f < 1e-37f ? 1e-37f : f;
-      };
-      auto i8_log2v = [&](int b) { return __shfl_sync(0xffffffffu, i8_now, 8 + b); };
       // row max: four independent chains of three-input maxima
       float mt;
       if constexpr (I8) {   // by blocks, each with its scales
@@ -923,7 +945,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           u = tc::max3(u, xb[10], xb[11]);
           w = tc::max3(w, xb[12], xb[13]);
           u = tc::max3(u, xb[14], xb[15]);
-          mt = fmaxf(mt, fmaf(fmaxf(u, w), i8_factor(b), i8_log2v(b)));
+          const float2 c = *reinterpret_cast<const float2*>(i8_sc + b);
+          mt = fmaxf(mt, fmaf(fmaxf(u, w), c.x * sl2, c.y));
         }
       } else {
         float m4[4] = {x[0], x[1], x[2], x[3]};
@@ -968,7 +991,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int b = 0; b < 4; ++b) {   // 8 pairs of keys a block
             const int blk = c0 / 8 + b;
-            const float f = i8_factor(blk), lv = i8_log2v(blk), add = lv + neg_mu;
+            const float4 sc = i8_sc[blk];
+            const float f = sc.x * sl2, add = sc.y + neg_mu;
             const uint64_t f2 = tc::pack_f32x2(f, f), a2 = tc::pack_f32x2(add, add);
             uint64_t acc = 0;
 #pragma unroll
@@ -981,7 +1005,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               pk[c] = pack_f16(y0, y1);
               tc::add_f32x2(acc, y0, y1);
             }
-            part[b & 1] = fmaf(tc::sum_f32x2(acc), ex2(-lv), part[b & 1]);
+            part[b & 1] = fmaf(tc::sum_f32x2(acc), sc.z, part[b & 1]);
           }
           tc::st32(tP + c0, pk);
         }
@@ -1011,6 +1035,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_pfull);
+      if (I8 && lane == 0) mbar_arrive(smem_u32(&sh->sc_empty[j % kScaleRing]));
       if (quarter == 0 && lane == 0) TC_MARK(900 + 64 * t + (j & 63));
       if (t == 0 && lane == 0) TC_MARK(1700 + 64 * quarter + (j & 63));
       if (issuer) {
