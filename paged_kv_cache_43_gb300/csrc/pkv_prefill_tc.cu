@@ -64,10 +64,12 @@
 //    is at most 2^8 whatever the scales are, and the row sum divides it out
 //    again (per block, in fp32).  Both cost nothing per element: they are the
 //    factor and the addend of the exponent's one FMA, per block of 16 keys
-//    instead of per tile.  Warp 9 fetches each tile's 8 + 8 scales (ids two
-//    tiles and scales one tile ahead) into a ring in shared memory that the
-//    softmax warps read by broadcast loads.  Every code is finite, so rows no
-//    key may see need no zeroing.
+//    instead of per tile.  Each softmax warp fetches its tiles' 8 + 8 scales
+//    itself (ids two tiles and scales one tile ahead) and lays them out in
+//    shared memory of its own, read by broadcast loads, while it has S to wait
+//    for: a warp that fetched them for all (handing them over by mbarriers)
+//    put 0.2-0.5 us a tile into the chain.  Every code is finite, so rows no key may
+//    see need no zeroing.
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 #include "pkv_tc.cuh"
@@ -84,8 +86,8 @@ constexpr int kTcTiles = 2;       // query tiles per CTA
 constexpr int kTcKeys = 128;      // keys per K/V tile
 // Warps: 0-3 softmax of query tile 0, 4-7 of query tile 1 (warpgroups 0 and
 // 1: warp w reads TMEM lanes 32 (w % 4) ..), 8 the K producer (and the V
-// producer with an FP8 cache), 9 TMEM allocation (and the block scales of an
-// int8 cache), 10 the V producer (bf16) or a widener (FP8), 11 a widener (FP8, D = 128; idle otherwise).  The launch
+// producer with an FP8 cache), 9 TMEM allocation, 10 the V producer (bf16) or
+// a widener (FP8), 11 a widener (FP8, D = 128; idle otherwise).  The launch
 // gives each thread 168 registers; warpgroup 2 then hands registers back so
 // that the softmax warpgroups run at 208 (2 x 128 x 208 + 128 x 80 =
 // 384 x 168).
@@ -120,8 +122,6 @@ struct TcLayout {
   static constexpr int kTileBytes = kHalves * kKvHalf;  // one K (or V) tile
 };
 
-constexpr int kScaleRing = 4;   // int8: key tiles whose block scales are held
-
 struct TcShared {
   uint64_t q_full, q_conv;
   uint64_t drain[kTcTiles];   // each tile's issuer: all its products complete
@@ -132,10 +132,9 @@ struct TcShared {
   uint32_t tmem_base;
   int32_t abort;
   int32_t n_issued[2];   // bf16 producers: K / V tiles issued, for the drain
-  // Int8: block b of key tile j has (K scale, log2 of the V scale, 1 / V scale)
-  // in sc[j % kScaleRing][b].
-  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
-  alignas(16) float4 sc[kScaleRing][kTcKeys / kBlock];
+  // Int8: (K scale, log2 of the V scale, 1 / V scale, the tile's largest V
+  // scale) of a key tile's blocks, a copy for each softmax warp.
+  alignas(16) float4 sc[8][kTcKeys / kBlock];
 };
 
 template <int D>
@@ -209,6 +208,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// (K widened to code + 128 as fp16 subnormals, the 128 taken off the scores,
+// would save two of the five operations for four codes, but ran slower: 819
+// against 737 us for four 2048-token chunks over 2K to 8K keys.)
 template <bool I8>
 __device__ __forceinline__ uint2 codes_to_f16x4(uint32_t codes) {
   if constexpr (I8) return i8x4_to_f16x4(codes);
@@ -511,11 +513,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(smem_u32(&sh->kv_empty[i]), issuers);
       mbar_init(smem_u32(&sh->kv_land[i]), 1);
     }
-    if constexpr (I8)
-      for (int i = 0; i < kScaleRing; ++i) {
-        mbar_init(smem_u32(&sh->sc_full[i]), 1);
-        mbar_init(smem_u32(&sh->sc_empty[i]), 4 * issuers);   // the softmax warps
-      }
     sh->abort = 0;
     fence_barrier_init();
   }
@@ -731,33 +728,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (warp == 8 && lane == 0) (void)mbar_wait(q_full, 0);   // the query tiles too
     __syncwarp();
-   } else if (I8 && warp == 9) {
-    // -------------------------------------------------- block scales (int8)
-    const int32_t* bt = a.block_tables + static_cast<int64_t>(s) * a.bt_stride;
-    const float* scales = (lane & 8) ? a.v_scales : a.k_scales;
-    auto id_of = [&](int j) {
-      const int b = (j0 + j) * (kTcKeys / kBlock) + (lane & 7);
-      return lane < 16 && b >= b_lo && b < nblk ? __ldg(bt + b) : -1;
-    };
-    auto scale_of = [&](int id) {   // (a block that is not read: any finite scale)
-      return id >= 0 && id < a.num_blocks
-                 ? __ldg(scales + static_cast<int64_t>(id) * a.num_kv_heads + kvh) : 1.f;
-    };
-    float next = scale_of(id_of(0));
-    int id_next = id_of(1);
-    for (int j = 0; j < n_rel; ++j) {
-      const int st = j % kScaleRing;
-      const float now = int8_scale(next);
-      next = scale_of(id_next);
-      id_next = id_of(j + 2);
-      const float lv = log2f(__shfl_sync(0xffffffffu, now, 8 + (lane & 7)));
-      if (j >= kScaleRing && !warp_wait(smem_u32(&sh->sc_empty[st]), (j / kScaleRing - 1) & 1, abort,
-                                        a.err, wlim))
-        break;
-      if (lane < 8) sh->sc[st][lane] = make_float4(now, lv, ex2(-lv), 0.f);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh->sc_full[st]));
-    }
    } else if (FP8 && (warp == 10 || (D == 128 && warp == 11))) {
     // ------------------------------------------------- widen e4m3 tiles (FP8)
     // Ring elements in order, so that each wait on a slot's kv_land is for
@@ -855,6 +825,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     float m_used = -INFINITY, l = 0.f;
     bool done = t < ntq;
+    // Int8: block scales of a key tile, lanes 0-7 the K, 8-15 the V scales.
+    [[maybe_unused]] const float4* sc = sh->sc[warp];
+    auto i8_id = [&](int j) {
+      const int b = (j0 + j) * (kTcKeys / kBlock) + (lane & 7);
+      return lane < 16 && b >= b_lo && b < nblk
+                 ? __ldg(a.block_tables + static_cast<int64_t>(s) * a.bt_stride + b) : -1;
+    };
+    auto i8_scale = [&](int id) {   // (a block that is not read: any finite scale)
+      return id >= 0 && id < a.num_blocks
+                 ? __ldg(((lane & 8) ? a.v_scales : a.k_scales) +
+                         static_cast<int64_t>(id) * a.num_kv_heads + kvh) : 1.f;
+    };
+    float i8_next = 1.f;
+    int i8_id_next = -1;
+    if constexpr (I8) {
+      i8_next = i8_scale(i8_id(0));
+      i8_id_next = i8_id(1);
+    }
     // first key this row sees (its window; after the shared prefix in a
     // cascade suffix launch)
     const int lo = max(a.window > 0 ? pos - a.window + 1 : 0, a.key_begin);
@@ -891,64 +879,151 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     __syncwarp();
     for (int j = 0; done && j < n_rel; ++j) {
+      if constexpr (I8) {   // this tile's scales to shared memory, the next tile's on their way
+        float now = int8_scale(i8_next);
+        i8_next = i8_scale(i8_id_next);
+        i8_id_next = i8_id(j + 2);
+        const float lv = log2f(__shfl_sync(0xffffffffu, now, 8 + (lane & 7)));
+        float top = now;   // lanes 8-15: the largest V scale
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        top = __shfl_sync(0xffffffffu, top, 8);
+        if (lane < 8) sh->sc[warp][lane] = make_float4(now, lv, ex2(-lv), top);
+        __syncwarp();
+      }
       // S_t(j) complete (its commit also covers P_t(j - 1) V, so O_t is stable)
       if (!warp_wait(b_sfull, j & 1, abort, a.err, wlim)) { done = false; break; }
       tc::fence_after_sync();
       if (quarter == 0 && lane == 0) TC_MARK(700 + 64 * t + (j & 63));
       if (t == 0 && quarter > 0 && lane == 0 && j < 32) TC_MARK(1030 + 32 * (quarter - 1) + j);
-      float x[kTcKeys];
-#pragma unroll
-      for (int c0 = 0; c0 < kTcKeys; c0 += 32) {
-        uint32_t r[32];
-        tc::ld32(tS + c0, r);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) x[c0 + c] = __uint_as_float(r[c]);
-      }
-      tc::wait_ld();
-      // causal mask on raw scores (also hides keys >= L); scale > 0, so the
-      // row max of the raw scores gives the max of the scaled ones
-      const int key0 = (j0 + j) * kTcKeys;
-      // (warp-uniform branches: the votes below need every lane)
-      if (__any_sync(0xffffffffu, key0 + kTcKeys - 1 > pos || key0 < lo)) {
-        // visible columns [nlo, nvis) of this row (rows that see the whole
-        // tile keep every column); one compare per element where no row of
-        // the warp has a lower bound in this tile
-        const int nvis = pos - key0 + 1;
-        const int nlo = lo - key0;
-        if (__any_sync(0xffffffffu, nlo > 0)) {
-#pragma unroll
-          for (int c = 0; c < kTcKeys; ++c)
-            x[c] = (c < nvis && c >= nlo) ? x[c] : -INFINITY;
-        } else {
-#pragma unroll
-          for (int c = 0; c < kTcKeys; ++c) x[c] = c < nvis ? x[c] : -INFINITY;
-        }
-      }
-      [[maybe_unused]] const float4* i8_sc = sh->sc[j % kScaleRing];
       if constexpr (I8) {
-        if (!warp_wait(smem_u32(&sh->sc_full[j % kScaleRing]), (j / kScaleRing) & 1, abort, a.err,
-                       wlim)) {
-          done = false;
-          break;
-        }
-      }
-      // row max: four independent chains of three-input maxima
-      float mt;
-      if constexpr (I8) {   // by blocks, each with its scales
-        mt = -INFINITY;
+        // The weights are first formed against the reference m of the tiles
+        // before: no pass over the row for its maximum.  Only if one may have
+        // grown past 2^15 (fp16 holds it until then; none is above the row sum
+        // times the largest V scale), or there is no reference yet, the row is
+        // loaded again, the maximum found and the weights formed anew.  P is
+        // stored after that is settled, since it lies over S.
+        float alpha = 1.f, ls;
+        uint32_t pk[kTcKeys / 2];
+        bool find_max = __any_sync(0xffffffffu, valid && m_used == -INFINITY);
+#pragma unroll 1
+        while (true) {
+          float x[kTcKeys];
 #pragma unroll
-        for (int b = 0; b < kTcKeys / kBlock; ++b) {
-          const float* xb = x + b * kBlock;
-          float u = tc::max3(xb[0], xb[1], xb[2]), w = tc::max3(xb[3], xb[4], xb[5]);
-          u = tc::max3(u, xb[6], xb[7]);
-          w = tc::max3(w, xb[8], xb[9]);
-          u = tc::max3(u, xb[10], xb[11]);
-          w = tc::max3(w, xb[12], xb[13]);
-          u = tc::max3(u, xb[14], xb[15]);
-          const float2 c = *reinterpret_cast<const float2*>(i8_sc + b);
-          mt = fmaxf(mt, fmaf(fmaxf(u, w), c.x * sl2, c.y));
+          for (int c0 = 0; c0 < kTcKeys; c0 += 32) {
+            uint32_t r[32];
+            tc::ld32(tS + c0, r);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c0 + c] = __uint_as_float(r[c]);
+          }
+          tc::wait_ld();
+          // causal mask on raw scores (also hides keys >= L); scale > 0, so the
+          // row max of the raw scores gives the max of the scaled ones
+          const int key0 = (j0 + j) * kTcKeys;
+          // (warp-uniform branches: the votes below need every lane)
+          if (__any_sync(0xffffffffu, key0 + kTcKeys - 1 > pos || key0 < lo)) {
+            // visible columns [nlo, nvis) of this row (rows that see the whole
+            // tile keep every column); one compare per element where no row of
+            // the warp has a lower bound in this tile
+            const int nvis = pos - key0 + 1;
+            const int nlo = lo - key0;
+            if (__any_sync(0xffffffffu, nlo > 0)) {
+#pragma unroll
+              for (int c = 0; c < kTcKeys; ++c)
+                x[c] = (c < nvis && c >= nlo) ? x[c] : -INFINITY;
+            } else {
+#pragma unroll
+              for (int c = 0; c < kTcKeys; ++c) x[c] = c < nvis ? x[c] : -INFINITY;
+            }
+          }
+          if (find_max) {
+            float mt = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < kTcKeys / kBlock; ++b) {
+              const float* xb = x + b * kBlock;
+              float u = tc::max3(xb[0], xb[1], xb[2]), w = tc::max3(xb[3], xb[4], xb[5]);
+              u = tc::max3(u, xb[6], xb[7]);
+              w = tc::max3(w, xb[8], xb[9]);
+              u = tc::max3(u, xb[10], xb[11]);
+              w = tc::max3(w, xb[12], xb[13]);
+              u = tc::max3(u, xb[14], xb[15]);
+              mt = fmaxf(mt, fmaf(fmaxf(u, w), sc[b].x * sl2, sc[b].y));
+            }
+            if (mt > m_used + kLazyRescale) {
+              alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - mt);
+              m_used = mt;
+            }
+          }
+          const float neg_mu = (m_used == -INFINITY) ? 0.f : -m_used;
+          float part[2] = {0.f, 0.f}, top = 0.f;
+#pragma unroll
+          for (int b = 0; b < kTcKeys / kBlock; ++b) {
+            const float4 c = sc[b];
+            const float f = c.x * sl2, add = c.y + neg_mu;
+            const uint64_t f2 = tc::pack_f32x2(f, f), a2 = tc::pack_f32x2(add, add);
+            uint64_t acc = 0;
+#pragma unroll
+            for (int k = b * kBlock; k < (b + 1) * kBlock; k += 2) {
+              float y0, y1;
+              tc::fma_f32x2(x[k], x[k + 1], f2, a2, y0, y1);
+              y0 = ex2(y0);
+              y1 = ex2(y1);
+              pk[k / 2] = pack_f16(y0, y1);
+              tc::add_f32x2(acc, y0, y1);
+            }
+            part[b & 1] = fmaf(tc::sum_f32x2(acc), c.z, part[b & 1]);
+            if (b == 0) top = c.w;
+          }
+          ls = part[0] + part[1];
+          if (find_max || !__any_sync(0xffffffffu, valid && !(ls * top <= 32768.f))) break;
+          find_max = true;
         }
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // rescale O in TMEM
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tc::ld32(tO + c0, o);
+            tc::wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tc::st32(tO + c0, o);
+          }
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < kTcKeys / 2; c0 += 32)
+          tc::st32(tP + c0, *reinterpret_cast<uint32_t(*)[32]>(pk + c0));
+        l = l * alpha + ls;
       } else {
+        float x[kTcKeys];
+#pragma unroll
+        for (int c0 = 0; c0 < kTcKeys; c0 += 32) {
+          uint32_t r[32];
+          tc::ld32(tS + c0, r);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c0 + c] = __uint_as_float(r[c]);
+        }
+        tc::wait_ld();
+        // causal mask on raw scores (also hides keys >= L); scale > 0, so the
+        // row max of the raw scores gives the max of the scaled ones
+        const int key0 = (j0 + j) * kTcKeys;
+        // (warp-uniform branches: the votes below need every lane)
+        if (__any_sync(0xffffffffu, key0 + kTcKeys - 1 > pos || key0 < lo)) {
+          // visible columns [nlo, nvis) of this row (rows that see the whole
+          // tile keep every column); one compare per element where no row of
+          // the warp has a lower bound in this tile
+          const int nvis = pos - key0 + 1;
+          const int nlo = lo - key0;
+          if (__any_sync(0xffffffffu, nlo > 0)) {
+#pragma unroll
+            for (int c = 0; c < kTcKeys; ++c)
+              x[c] = (c < nvis && c >= nlo) ? x[c] : -INFINITY;
+          } else {
+#pragma unroll
+            for (int c = 0; c < kTcKeys; ++c) x[c] = c < nvis ? x[c] : -INFINITY;
+          }
+        }
+        // row max: four independent chains of three-input maxima
         float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int c = 4; c < kTcKeys - 4; c += 8) {
@@ -959,58 +1034,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         m4[0] = tc::max3(m4[0], x[kTcKeys - 4], x[kTcKeys - 3]);
         m4[1] = tc::max3(m4[1], x[kTcKeys - 2], x[kTcKeys - 1]);
-        mt = tc::max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
-      }
-      float alpha = 1.f;
-      if (mt > m_used + kLazyRescale) {
-        alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - mt);
-        m_used = mt;
-      }
-      const float neg_mu = (m_used == -INFINITY) ? 0.f : -m_used;
-      [[maybe_unused]] const uint64_t m2 = tc::pack_f32x2(sl2, sl2),
-                                      b2 = tc::pack_f32x2(neg_mu, neg_mu);
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // rescale O in TMEM
+        const float mt = tc::max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * sl2;
+        float alpha = 1.f;
+        if (mt > m_used + kLazyRescale) {
+          alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - mt);
+          m_used = mt;
+        }
+        const float neg_mu = (m_used == -INFINITY) ? 0.f : -m_used;
+        const uint64_t m2 = tc::pack_f32x2(sl2, sl2), b2 = tc::pack_f32x2(neg_mu, neg_mu);
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // rescale O in TMEM
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t o[32];
-          tc::ld32(tO + c0, o);
-          tc::wait_ld();
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[32];
+            tc::ld32(tO + c0, o);
+            tc::wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-          tc::st32(tO + c0, o);
-        }
-      }
-      // P = 2^(s * scale*log2(e) - max): packed FMA, MUFU ex2, bf16 pairs
-      // written over S's first 64 columns; the row sum adds the fp32 weights
-      float ls;
-      if constexpr (I8) {
-        float part[2] = {0.f, 0.f};
-#pragma unroll
-        for (int c0 = 0; c0 < kTcKeys / 2; c0 += 32) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {   // 8 pairs of keys a block
-            const int blk = c0 / 8 + b;
-            const float4 sc = i8_sc[blk];
-            const float f = sc.x * sl2, add = sc.y + neg_mu;
-            const uint64_t f2 = tc::pack_f32x2(f, f), a2 = tc::pack_f32x2(add, add);
-            uint64_t acc = 0;
-#pragma unroll
-            for (int c = 8 * b; c < 8 * b + 8; ++c) {
-              const int k = 2 * (c0 + c);
-              float y0, y1;
-              tc::fma_f32x2(x[k], x[k + 1], f2, a2, y0, y1);
-              y0 = ex2(y0);
-              y1 = ex2(y1);
-              pk[c] = pack_f16(y0, y1);
-              tc::add_f32x2(acc, y0, y1);
-            }
-            part[b & 1] = fmaf(tc::sum_f32x2(acc), sc.z, part[b & 1]);
+            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+            tc::st32(tO + c0, o);
           }
-          tc::st32(tP + c0, pk);
         }
-        ls = part[0] + part[1];
-      } else {
+        // P = 2^(s * scale*log2(e) - max): packed FMA, MUFU ex2, bf16 pairs
+        // written over S's first 64 columns; the row sum adds the fp32 weights
         uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int c0 = 0; c0 < kTcKeys / 2; c0 += 32) {
@@ -1027,15 +1071,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           tc::st32(tP + c0, pk);
         }
-        ls = (tc::sum_f32x2(acc[0]) + tc::sum_f32x2(acc[1])) +
+        const float ls = (tc::sum_f32x2(acc[0]) + tc::sum_f32x2(acc[1])) +
                          (tc::sum_f32x2(acc[2]) + tc::sum_f32x2(acc[3]));
+        l = l * alpha + ls;
       }
-      l = l * alpha + ls;
       tc::wait_st();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_pfull);
-      if (I8 && lane == 0) mbar_arrive(smem_u32(&sh->sc_empty[j % kScaleRing]));
       if (quarter == 0 && lane == 0) TC_MARK(900 + 64 * t + (j & 63));
       if (t == 0 && lane == 0) TC_MARK(1700 + 64 * quarter + (j & 63));
       if (issuer) {
