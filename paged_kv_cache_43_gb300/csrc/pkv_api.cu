@@ -200,6 +200,30 @@ int encode_cache_map(CUtensorMap* map, const void* base, const pkv_cache_desc& c
   return r == CUDA_SUCCESS ? PKV_OK : PKV_E_CUDA;
 }
 
+// TMA descriptor of an int8 cache for copies of one block of `heads` kv heads:
+// the 3-D tensor (head_size, num_blocks * 16, num_kv_heads), the box a head
+// row x 16 rows x `heads`, so that each head's rows land together, swizzled as
+// above.
+int encode_heads_map(CUtensorMap* map, const void* base, const pkv_cache_desc& c, int heads) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn;
+  if (int st = encode_fn(&fn)) return st;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.head_size),
+                              static_cast<cuuint64_t>(c.num_blocks) * c.block_size,
+                              static_cast<cuuint64_t>(c.num_kv_heads)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(c.num_kv_heads) * c.head_size,
+                                 static_cast<cuuint64_t>(c.head_size)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(c.head_size),
+                             static_cast<cuuint32_t>(c.block_size), static_cast<cuuint32_t>(heads)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  c.head_size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  c.head_size == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                    : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PKV_OK : PKV_E_CUDA;
+}
+
 // TMA descriptor of the bf16 query tensor [num_tokens, num_q_heads, D] viewed
 // as (D, Hq, T) with a box of 64 columns x `group` heads x 128/group tokens:
 // one box is the 128-row (token, head) tile of one kv head, 128 bytes wide.
@@ -952,27 +976,33 @@ int check_cache_int8(const pkv_cache_desc* c) {
 }
 
 // How the decode sequences of an int8 batch are cut: their blocks on one line,
-// in equal ranges (pkv_decode_int8.cu).
+// in ranges (pkv_decode_int8.cu).
 struct Int8Plan {
   int num_decode = 0;
-  int col_groups = 1;
-  int num_ranges = 1;     // ranges that give every resident warp one (range, head)
+  int col_groups = 1;     // groups of 8 q heads per kv head
+  int team_heads = 1, team_warps = 1;
+  int teams_per_range = 1;
+  int num_ranges = 1;     // ranges that give every resident team one
   int max_ranges = 1;     // that there can be: the workspace has two slots for each
   size_t ws_o_bytes = 0, ws_lse_bytes = 0, ws_bytes = 0;
 };
-
-// Blocks of a range at least: below this a warp's start and its partial cost
-// more than the keys it reads.
-constexpr int kMinRangeBlocks = 8;
 
 int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms, Int8Plan* p) {
   *p = Int8Plan{};
   p->num_decode = m->max_query_len <= 1 ? m->num_seqs : std::max(m->num_decode_seqs, 0);
   if (p->num_decode == 0) return PKV_OK;
   p->col_groups = (m->num_q_heads / c->num_kv_heads + 7) / 8;
-  const int64_t heads = static_cast<int64_t>(c->num_kv_heads) * p->col_groups;
-  const int64_t warps = static_cast<int64_t>(num_sms) * kDecInt8CtasPerSm * 4;
-  p->num_ranges = static_cast<int>(std::max<int64_t>(warps / heads, 1));
+  // a team: kv heads side by side, read in one copy (the largest power of two
+  // that divides their number), times the groups of 8 q heads that share them
+  int cols = 1;
+  while (2 * cols <= std::min(p->col_groups, kDecInt8Warps)) cols *= 2;
+  p->team_heads = 1;
+  while (2 * p->team_heads * cols <= kDecInt8Warps && c->num_kv_heads % (2 * p->team_heads) == 0)
+    p->team_heads *= 2;
+  p->team_warps = p->team_heads * cols;
+  p->teams_per_range = c->num_kv_heads / p->team_heads * ((p->col_groups + cols - 1) / cols);
+  p->num_ranges = std::max(
+      num_sms * kDecInt8CtasPerSm * (kDecInt8Warps / p->team_warps) / p->teams_per_range, 1);
   int64_t longest = (static_cast<int64_t>(m->max_context_len) + kBlock - 1) / kBlock;
   if (m->sliding_window > 0)   // W keys span at most (W + 14) / 16 + 1 blocks
     longest = std::min(longest, (static_cast<int64_t>(m->sliding_window) + 14) / kBlock + 1);
@@ -980,8 +1010,9 @@ int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms,
   const int64_t ranges =
       m->kv_split_tokens > 0
           ? (blocks + m->kv_split_tokens / kBlock - 1) / (m->kv_split_tokens / kBlock)
-          : std::min<int64_t>(p->num_ranges, (blocks + kMinRangeBlocks - 1) / kMinRangeBlocks);
-  if (ranges * heads > INT32_MAX / 2 || blocks / p->num_ranges > INT32_MAX / 2) return PKV_E_SHAPE;
+          : std::min<int64_t>(static_cast<int64_t>(kMaxRangeWaves) * p->num_ranges,
+                              (blocks + kMinRangeBlocks - 1) / kMinRangeBlocks);
+  if (ranges * p->teams_per_range > INT32_MAX / 2 || blocks / p->num_ranges > INT32_MAX / 2) return PKV_E_SHAPE;
   p->max_ranges = static_cast<int>(std::max<int64_t>(ranges, 1));
   if (p->max_ranges > 1) {
     const size_t rows = 2 * static_cast<size_t>(p->max_ranges) * m->num_q_heads;
@@ -1080,10 +1111,10 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
   const cudaStream_t st = as_stream(stream);
   const float scale_log2 = scale * 1.4426950408889634f;
   const int G = meta->num_q_heads / cache->num_kv_heads;
-  CUtensorMap kmap, vmap;
-  if (int e = encode_cache_map(&kmap, k_cache, *cache)) return e;
-  if (int e = encode_cache_map(&vmap, v_cache, *cache)) return e;
   auto decode_part = [&](cudaStream_t st) -> int {
+    CUtensorMap kmap, vmap;
+    if (int e = encode_heads_map(&kmap, k_cache, *cache, p.team_heads)) return e;
+    if (int e = encode_heads_map(&vmap, v_cache, *cache, p.team_heads)) return e;
     DecodeInt8Args d{};
     d.out = out;
     d.q = q;
@@ -1110,13 +1141,14 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     d.max_context_len = meta->max_context_len;
     d.window = meta->sliding_window;
     d.range_blocks = meta->kv_split_tokens / kBlock;
-    d.min_range_blocks = kMinRangeBlocks;
     d.num_ranges = p.num_ranges;
     d.max_ranges = p.max_ranges;
-    const int64_t items =
-        static_cast<int64_t>(p.max_ranges) * cache->num_kv_heads * p.col_groups;
-    d.grid = static_cast<uint32_t>(
-        std::min<int64_t>((items + 3) / 4, static_cast<int64_t>(sms) * kDecInt8CtasPerSm));
+    d.team_warps = p.team_warps;
+    d.team_heads = p.team_heads;
+    d.teams_per_range = p.teams_per_range;
+    const int cta_teams = kDecInt8Warps / p.team_warps;
+    d.grid = static_cast<uint32_t>((static_cast<int64_t>(p.max_ranges) * p.teams_per_range +
+                                    cta_teams - 1) / cta_teams);
     d.scale_log2 = scale_log2;
     PKV_TRY(launch_decode_int8(kmap, vmap, d, cache->head_size, p.max_ranges > 1, st));
     return PKV_OK;
@@ -1171,7 +1203,9 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     f.longest_first = p.num_decode == 0 ? 1 : 0;   // alone on the GPU, or beside decode
     const int toks = prefill_tc_tokens_per_cta(G);
     f.num_mtiles = (meta->max_query_len + toks - 1) / toks;
-    CUtensorMap qmap, omap;
+    CUtensorMap qmap, omap, kmap, vmap;
+    if (int e = encode_cache_map(&kmap, k_cache, *cache)) return e;
+    if (int e = encode_cache_map(&vmap, v_cache, *cache)) return e;
     if (int e = encode_query_map(&qmap, q, meta->num_tokens, meta->num_q_heads, cache->head_size, G))
       return e;
     if (int e =

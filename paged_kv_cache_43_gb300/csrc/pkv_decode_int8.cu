@@ -13,20 +13,26 @@
 // not rounded at all; Q is scaled by a power of two into fp16's range.
 //
 // Split.  The decode sequences' blocks, one sequence after the other, form
-// one line of NB blocks; it is cut into equal ranges, and a warp takes one
-// range of one kv head (and 8 of its q heads): every warp of the GPU streams
-// the same number of bytes, whatever the lengths are, with no second wave and
-// no CTA that finds nothing to do.  The ranges come from the lengths on the
-// device (each CTA adds them up when it starts).  Consecutive warps take the
-// kv heads of one range, so the rows of a token are read together.  Where a
-// range ends inside a sequence the warp writes a partial (normalised O and
-// log2-sum-exp); each range holds at most two, so the workspace does not grow
-// with the context.  A second launch merges them (fixed order: the same
-// inputs give the same bits).
+// one line, which is cut into ranges; a team of up to 8 warps walks a range,
+// whatever sequences lie in it, each warp with its own kv head (or group of 8
+// q heads of one), over blocks that one TMA copy of K and one of V brings in
+// for all their heads.  Where a range ends inside a sequence its warps write
+// partials (normalised O and log2-sum-exp); a range holds at most two a head,
+// so the workspace does not grow with the context.  A second launch merges
+// them (fixed order: the same inputs give the same bits).  The ranges come
+// from the lengths on the device: each CTA adds them up when it starts.
 //
-// Bound by HBM: every code is read once, by TMA (one 16-row box of a head's K
-// and of V a block, 4 KB a stage at head_size 128) into a ring per warp; a
-// block goes to registers, its stage is refilled, and the block is computed.
+// Bound by HBM: every code is read once.  What the layout answers to:
+//  * a head's 128 bytes of a token lie beside the next head's; read at
+//    different times they cost a DRAM row each (a warp per head and nothing
+//    that keeps the heads together: 5.1 TB/s, against 7.1 where they happened
+//    to run side by side), so a team reads its heads in one copy;
+//  * SMs of some GPCs get 15 % less bandwidth than the others: with equal
+//    ranges, one a team, they were waited for (183 us for 64 sequences of 32
+//    heads, the warps' mean being done at 154).  So the first ranges, one for every
+//    team that the GPU holds at a time, take only kBigShare of the line, and
+//    the rest goes out in parts of kSmallShare of an even share, which the
+//    block scheduler hands to the SMs that are done first.
 #include <float.h>
 
 #include "pkv_common.cuh"
@@ -36,12 +42,16 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 4;
+// In 1 / 64 of a team's even share of the line.
+constexpr int kBigShare = 44, kSmallShare = 10;
+
+constexpr int kWarps = kDecInt8Warps;
 constexpr int kThreads = kWarps * 32;
 
+// A CTA's rings: NS stages of a K and a V block for each of its heads.
 template <int D, int NS>
 constexpr int dec8_smem_bytes() {
-  return 1024 /* alignment slack */ + kWarps * NS * 2 * D * kBlock + kWarps * NS * 8 +
+  return 1024 /* alignment slack */ + kWarps * NS * 2 * D * kBlock + kWarps * NS * 2 * 8 +
          (kThreads + 1) * 8;
 }
 
@@ -79,28 +89,34 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
     pkv_decode_int8_kernel(const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap, const DecodeInt8Args a) {
   constexpr int kTile = D * kBlock;        // one block of one head, K or V: bytes
-  constexpr int kStage = 2 * kTile;
   // (the merge launch may be scheduled beside this grid's last CTAs; it waits
   // for the grid's completion itself)
   asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * NS * kStage);
-  int64_t* upto = reinterpret_cast<int64_t*>(bars + kWarps * NS);   // [kThreads + 1]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * NS * 2 * kTile);
+  int64_t* upto = reinterpret_cast<int64_t*>(bars + kWarps * NS * 2);   // [kThreads + 1]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.group, Hq = a.num_q_heads;
+  // the team: team_heads kv heads x (team_warps / team_heads) groups of 8 q heads
+  const int team_warps = a.team_warps, team_heads = a.team_heads;
+  const int team = warp / team_warps, mate = warp - team * team_warps;
+  const int mate_cols = team_warps / team_heads;
+  const uint32_t stage_bytes = static_cast<uint32_t>(team_heads) * 2 * kTile;
+  const uint32_t ring = smem_u32(smem) + team * NS * stage_bytes;
+  const uint32_t full = smem_u32(bars) + team * NS * 16, empty = full + NS * 8;
   if (threadIdx.x == 0) {
     prefetch_tensor_map(&kmap);
     prefetch_tensor_map(&vmap);
   }
-  uint8_t* wbase = smem + warp * NS * kStage;
-  const uint32_t wbase_u = smem_u32(wbase);
-  const uint32_t bar0 = smem_u32(bars + warp * NS);
-  if (lane == 0) {
+  if (mate == 0 && lane == 0) {
 #pragma unroll
-    for (int st = 0; st < NS; ++st) mbar_init(bar0 + 8 * st, 1);
+    for (int st = 0; st < NS; ++st) {
+      mbar_init(full + 8 * st, 1);
+      mbar_init(empty + 8 * st, team_warps);
+    }
     fence_barrier_init();
   }
 
@@ -139,54 +155,87 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
     if (threadIdx.x == 0) upto[0] = 0;
     __syncthreads();
   }
-  const int heads = a.num_kv_heads * a.col_groups;
-  // blocks of a range: what the caller asked for, or an equal share of the
-  // warps' (a.num_ranges of them for each head); fits 32 bits: a range is cut
-  // from at most max_ranges of them
-  __shared__ int range_blocks;
-  int items;
+  // The ranges: num_big of big_blocks blocks each, then of small_blocks (a
+  // range's blocks fit 32 bits: the host sees to it).
+  __shared__ int big_blocks, small_blocks, num_big;
+  int ranges;
   {
     const int64_t total = upto[kThreads];
-    const int64_t R = a.range_blocks > 0
-                          ? a.range_blocks
-                          : max((total + a.num_ranges - 1) / a.num_ranges,
-                                static_cast<int64_t>(a.min_range_blocks));
-    items = static_cast<int>((total + R - 1) / R) * heads;
-    if (threadIdx.x == 0) range_blocks = static_cast<int>(R);
+    int64_t big = 0, small = a.range_blocks;   // what the caller asked for
+    if (small == 0) {
+      const int64_t share = (total + a.num_ranges - 1) / a.num_ranges;
+      if (share * kSmallShare >= 64 * kMinRangeBlocks) {
+        big = share * kBigShare / 64;
+        small = (share * kSmallShare + 63) / 64;
+      } else {   // little work: equal ranges, one a team
+        small = max(share, static_cast<int64_t>(kMinRangeBlocks));
+      }
+    }
+    const int n_big = big > 0 ? a.num_ranges : 0;
+    ranges = n_big + static_cast<int>((total - n_big * big + small - 1) / small);
+    if (threadIdx.x == 0) {
+      big_blocks = static_cast<int>(big);
+      small_blocks = static_cast<int>(small);
+      num_big = n_big;
+    }
     __syncthreads();
   }
+  // first block of range r, and the range of block x
+  auto range_begin = [&](int r) {
+    return r < num_big ? static_cast<int64_t>(r) * big_blocks
+                       : static_cast<int64_t>(num_big) * big_blocks +
+                             static_cast<int64_t>(r - num_big) * small_blocks;
+  };
+  auto range_of = [&](int64_t x) {
+    const int64_t y = x - static_cast<int64_t>(num_big) * big_blocks;
+    return y < 0 ? static_cast<int>(x / big_blocks) : num_big + static_cast<int>(y / small_blocks);
+  };
 
   const uint64_t policy = policy_evict_first();
   const uint64_t wlim = wait_limit(a.wait_limit_ns);
   const int t = lane & 3, r0 = lane >> 2;
   const int c0 = 2 * t;                       // this lane's two q-head columns: c0, c0 + 1
-  // fragment offsets inside a block's code tiles (see the loop)
+  // ---- this warp's work: a range, a kv head, a group of 8 q heads
+  const int unit = blockIdx.x * (kWarps / team_warps) + team;   // team's number
+  const int range = unit / a.teams_per_range;
+  const int rest = unit - range * a.teams_per_range;
+  const int col_teams = (a.col_groups + mate_cols - 1) / mate_cols;
+  const int kvh0 = rest / col_teams * team_heads;    // the team's first kv head
+  const int head_of = mate / mate_cols;              // the warp's, counted from there
+  const int kvh = kvh0 + head_of;
+  const int gsub = rest % col_teams * mate_cols + mate % mate_cols;   // (past G: zero columns)
+  // Fragment addresses of stage 0 (see the loop): K row r0 at its first chunk
+  // and, D = 128, its second; V rows 2t and 2t + 1.  Rows 8 further on lie 8 row
+  // lengths behind (the swizzle repeats every 8 rows).
   constexpr int KC = D / 64;
-  uint32_t koff[2][KC], voff[4];
+  constexpr int kRows8 = 8 * D;
+  uint32_t k_at[KC], v_at[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int c = 0; c < KC; ++c) k_at[c] = ring + head_of * kTile + swz8<D>(r0, KC * t + c);
 #pragma unroll
-    for (int c = 0; c < KC; ++c) koff[h][c] = swz8<D>(r0 + 8 * h, KC * t + c);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int row = 2 * t + (q & 1) + 8 * (q >> 1);
-    voff[q] = D == 128 ? swz8<D>(row, r0) : swz8<D>(row, r0 >> 1) + 8 * (r0 & 1);
-  }
-  uint32_t fill = 0, used = 0;   // stages filled and consumed so far, all segments
-  // Test hook: warp 0 of a CTA withholds its first block, so that its wait runs out.
-  const bool withheld = a.debug_stall != 0 && warp == 0;
+  for (int x = 0; x < 2; ++x)
+    v_at[x] = ring + (team_heads + head_of) * kTile +
+              (D == 128 ? swz8<D>(2 * t + x, r0) : swz8<D>(2 * t + x, r0 >> 1) + 8 * (r0 & 1));
+  // The team counts its blocks through all its segments: block c is in stage c %
+  // NS.  A warp of the team starts each copy, in turn: when it has read block c,
+  // the one that takes the stage of block c - lag (which the others have
+  // probably read by then, too).
+  const int lag = team_warps > 1 ? 1 : 0;
+  uint32_t seg0 = 0;            // blocks of the segments before
+  int st = 0;                   // stage of the next block, parity of its phase
+  uint32_t phase = 0;
+  uint32_t next_issue = 0;      // blocks below this that are this warp's to start are started
   bool alive = true;
+  // Test hook: the team of warp 0 withholds its first block, so that its waits run out.
+  const bool withheld = a.debug_stall != 0 && team == 0;
 
-  for (int item = blockIdx.x * kWarps + warp; item < items && alive; item += gridDim.x * kWarps) {
-    const int range = item / heads;
-    const int hc = item - range * heads;
-    const int kvh = hc / a.col_groups, gsub = hc - kvh * a.col_groups;
+  if (range < ranges) {
     // ---- the sequence that holds the range's first block, which one of its
     // blocks that is, and how many blocks the range still has
     int s, b0, left;
     {
-      const int64_t begin = static_cast<int64_t>(range) * range_blocks;
-      left = static_cast<int>(min(static_cast<int64_t>(range_blocks), upto[kThreads] - begin));
+      const int64_t begin = range_begin(range);
+      left = static_cast<int>(min(range_begin(range + 1), upto[kThreads]) - begin);
       int64_t base;
       int th = 0;   // the last thread run that begins at or before `begin`
 #pragma unroll
@@ -217,44 +266,53 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
       }
       b0 = static_cast<int>(begin - base);
     }
-    for (; left > 0 && s < a.num_seqs; ++s) {
+    int n;
+    for (; left > 0 && s < a.num_seqs && alive; ++s, left -= n, b0 = 0, seg0 += n) {
       DecSeq q;
       int32_t bits;
+      n = 0;
       if (!dec_seq(a, s, &q, &bits)) continue;
       const int nblk = q.blocks();
-      const int n = min(left, nblk - b0);   // the segment: blocks [b0, b0 + n)
-      const int32_t* bt = a.block_tables + static_cast<int64_t>(s) * a.bt_stride + q.blk0() + b0;
+      n = min(left, nblk - b0);   // the segment: blocks [b0, b0 + n)
+      const int32_t* bt =
+          a.block_tables + static_cast<int64_t>(s) * a.bt_stride + q.blk0() + b0;
 
       // ids of 32 blocks at a time, lane i the i-th; the next 32 a group ahead
-      auto ids_of = [&](int g) {
-        const int i = 32 * g + lane;
-        return i < n ? __ldg(bt + i) : -1;
+      auto ids_of = [&](int i0) { return i0 + lane < n ? __ldg(bt + i0 + lane) : -1; };
+      auto valid = [&](int bid) {
+        return static_cast<uint32_t>(bid) < static_cast<uint32_t>(a.num_blocks);
       };
-      auto valid = [&](int bid) { return bid >= 0 && bid < a.num_blocks; };
       auto scales_of = [&](int bid, float* ks, float* vs) {
         const int64_t i = static_cast<int64_t>(valid(bid) ? bid : 0) * a.num_kv_heads + kvh;
         *ks = __ldg(a.k_scales + i);
         *vs = __ldg(a.v_scales + i);
       };
-      int cur = ids_of(0), nxt = ids_of(1);
-      float ks_c, lv_c, ks_n = 1.f, vs_n = 1.f;   // K scales, log2 of the V scales
-      auto issue = [&](int i, int g) {   // block i of the segment, group g = the current one
-        const int bid = __shfl_sync(0xffffffffu, (i >> 5) == g ? cur : nxt, i & 31);
-        if (lane == 0 && !(withheld && fill == 0)) {
-          const int st = fill % NS;
-          const uint32_t dst = wbase_u + st * kStage, bar = bar0 + 8 * st;
-          if (valid(bid)) {
-            mbar_arrive_expect_tx(bar, kStage);
-            tma_load_3d(dst, &kmap, bar, 0, kvh, bid * kBlock, policy);
-            tma_load_3d(dst + kTile, &vmap, bar, 0, kvh, bid * kBlock, policy);
-          } else {
-            mbar_arrive(bar);   // nothing to load: complete the phase empty
-          }
+      int cur = ids_of(0), nxt = ids_of(32);
+      // Starts the team's block c, which is block `bid` (lane 0 acts): waits until
+      // every warp of the team has read what its stage held.
+      auto issue = [&](uint32_t c, int bid) {
+        next_issue = c + 1;
+        if (lane != 0 || (withheld && c == 0)) return;
+        const int stage = c % NS;
+        const uint32_t dst = ring + stage * stage_bytes, bar = full + 8 * stage;
+        if (c >= NS && !mbar_wait(empty + 8 * stage, (c / NS - 1) & 1, wlim)) {
+          mbar_arrive(bar);   // (given up: the wait for this block will see it)
+          raise_error(a.err, PKV_ERR_TIMEOUT);
+        } else if (valid(bid)) {
+          fence_proxy_async();
+          mbar_arrive_expect_tx(bar, stage_bytes);
+          tma_load_3d(dst, &kmap, bar, 0, bid * kBlock, kvh0, policy);
+          tma_load_3d(dst + team_heads * kTile, &vmap, bar, 0, bid * kBlock, kvh0, policy);
+        } else {
+          mbar_arrive(bar);   // nothing to load: complete the phase empty
         }
-        ++fill;
       };
-      const int ahead = min(n, NS);
-      for (int i = 0; i < ahead; ++i) issue(i, 0);
+      if (mate == 0) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+          if (i < n) issue(seg0 + i, __shfl_sync(0xffffffffu, cur, i));
+      }
+      float ks_c, lv_c, ks_n = 1.f, vs_n = 1.f;   // K scales, log2 of the V scales
       scales_of(cur, &ks_c, &lv_c);
       ks_c = int8_scale(ks_c);
       lv_c = log2f(int8_scale(lv_c));
@@ -295,57 +353,65 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
       for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
+      // blocks with keys that the row does not see: the first, the last
+      const int edge_lo = b0 == 0 && q.first % kBlock != 0 ? 0 : -1;
+      const int edge_hi = b0 + n == nblk && q.L % kBlock != 0 ? n - 1 : -1;
+      uint32_t ok_mask = 0;
       for (int i = 0; i < n; ++i) {
-        const int g = i >> 5;
-        if ((i & 31) == 0 && i > 0) {
-          cur = nxt;
-          ks_c = int8_scale(ks_n);
-          lv_c = log2f(int8_scale(vs_n));
-          nxt = ids_of(g + 1);
+        if ((i & 31) == 0) {
+          if (i > 0) {
+            cur = nxt;
+            ks_c = int8_scale(ks_n);
+            lv_c = log2f(int8_scale(vs_n));
+            nxt = ids_of(i + 32);
+          }
+          ok_mask = __ballot_sync(0xffffffffu, valid(cur));
+          if (mate == 0 && !valid(cur) && i + lane < n) raise_error(a.err, PKV_ERR_BLOCK_ID);
         }
-        if ((i & 31) == 8) scales_of(nxt, &ks_n, &vs_n);
-        if ((i & 31) == 0 && !valid(cur) && 32 * g + lane < n) raise_error(a.err, PKV_ERR_BLOCK_ID);
-        const bool ok = valid(__shfl_sync(0xffffffffu, cur, i & 31));
         const float ks = __shfl_sync(0xffffffffu, ks_c, i & 31);
         const float lv = __shfl_sync(0xffffffffu, lv_c, i & 31);
-        const int st = used % NS;
-        if (!mbar_wait(bar0 + 8 * st, (used / NS) & 1, wlim)) {
+        if (!mbar_wait(full + 8 * st, phase, wlim)) {
           alive = false;
           break;
         }
-        ++used;
         // The whole block goes to registers first, so that its stage is
         // refilled before the block is computed.  K: rows r0 and r0 + 8, bytes
         // [(D/4) t, (D/4) t + D/4).  V: rows 2t, 2t+1, 2t+8, 2t+9, bytes
         // [(D/8) r0, (D/8) r0 + D/8): the output rows of step dt are d =
         // (D/8) r0 + 2 dt + {0, 1}.
         constexpr int VW = D / 32;
+        const uint32_t off = st * stage_bytes;
         uint4 kw[2][KC];
         uint32_t vw[4][VW];
-        if (ok) {
-          const uint8_t* kt = wbase + st * kStage;
-          const uint8_t* vt = kt + kTile;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int c = 0; c < KC; ++c) {
+          kw[0][c] = lds128(k_at[c] + off);
+          kw[1][c] = lds128(k_at[c] + off + kRows8);
+        }
 #pragma unroll
-            for (int c = 0; c < KC; ++c) kw[h][c] = *reinterpret_cast<const uint4*>(kt + koff[h][c]);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            if constexpr (D == 128) {
-              const uint4 u = *reinterpret_cast<const uint4*>(vt + voff[x]);
-              vw[x][0] = u.x; vw[x][1] = u.y; vw[x][2] = u.z; vw[x][3] = u.w;
-            } else {
-              const uint2 u = *reinterpret_cast<const uint2*>(vt + voff[x]);
-              vw[x][0] = u.x; vw[x][1] = u.y;
-            }
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t at = v_at[x & 1] + off + (x >> 1) * kRows8;
+          if constexpr (D == 128) {
+            const uint4 u = lds128(at);
+            vw[x][0] = u.x; vw[x][1] = u.y; vw[x][2] = u.z; vw[x][3] = u.w;
+          } else {
+            const uint2 u = lds64(at);
+            vw[x][0] = u.x; vw[x][1] = u.y;
           }
         }
         __syncwarp();
-        if (i + NS < n) {
-          if (lane == 0) fence_proxy_async();
-          issue(i + NS, g);
+        if (lane == 0) mbar_arrive(empty + 8 * st);
+        if (++st == NS) {
+          st = 0;
+          phase ^= 1;
         }
-        if (!ok) continue;
+        {
+          const int k = i - lag + NS;   // the segment's block to start now, and whose turn it is
+          if (i >= lag && k < n && (i & (team_warps - 1)) == mate)
+            issue(seg0 + k, __shfl_sync(0xffffffffu, (k ^ i) < 32 ? cur : nxt, k & 31));
+        }
+        if ((i & 31) == 8) scales_of(nxt, &ks_n, &vs_n);
+        if (!(ok_mask >> (i & 31) & 1)) continue;   // (its stage holds something else)
         // ---- S^T = K . Q^T (16 keys x 8 heads), even and odd steps apart to
         // halve the chain of dependent products
         float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
@@ -364,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
         y[1] = fmaf(sc[1] + sd[1], col_scale[1] * ks, lv);
         y[2] = fmaf(sc[2] + sd[2], col_scale[0] * ks, lv);
         y[3] = fmaf(sc[3] + sd[3], col_scale[1] * ks, lv);
-        const int p0 = (q.blk0() + b0 + i) * kBlock;
-        if (p0 + kBlock > q.L || p0 < q.first) {   // the sequence's edge blocks
+        if (i == edge_lo || i == edge_hi) {
+          const int p0 = (q.blk0() + b0 + i) * kBlock;
           const bool v0 = p0 + r0 < q.L && p0 + r0 >= q.first;
           const bool v1 = p0 + r0 + 8 < q.L && p0 + r0 + 8 >= q.first;
           if (!v0) y[0] = y[1] = -INFINITY;
@@ -421,8 +487,10 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
       }
       // (a row all of whose blocks were bad, or a wait that gave up, has l = 0)
       const bool whole = b0 == 0 && n == nblk;
-      if (b0 == 0 && hc == 0 && lane == 0 && a.span != nullptr)
-        a.span[s] = make_int2(range, 1 + (nblk - left + range_blocks - 1) / range_blocks);
+      if (b0 == 0 && kvh == 0 && gsub == 0 && lane == 0 && a.span != nullptr)
+        a.span[s] = make_int2(
+            range, range_of(min(range_begin(range + 1), upto[kThreads]) - left + nblk - 1) - range + 1);
+      const int64_t slot = 2 * static_cast<int64_t>(range) + (b0 == 0 ? 1 : 0);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int g = gsub * 8 + c0 + c;
@@ -440,43 +508,47 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
           for (int i = 0; i < D / 64; ++i)
             dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         } else {
-          const int64_t slot = (2 * static_cast<int64_t>(range) + (b0 == 0 ? 1 : 0)) * Hq + hq;
-          float4* dst = reinterpret_cast<float4*>(a.ws_o + slot * D + (D / 8) * r0);
+          float4* dst = reinterpret_cast<float4*>(a.ws_o + (slot * Hq + hq) * D + (D / 8) * r0);
 #pragma unroll
           for (int i = 0; i < D / 32; ++i)
             dst[i] = make_float4(o[2 * i][c] * inv, o[2 * i][2 + c] * inv, o[2 * i + 1][c] * inv,
                                  o[2 * i + 1][2 + c] * inv);
           // (the exponent reference m carries log2 sv; l has it divided out)
-          if (r0 == 0) a.ws_lse[slot] = l[c] == 0.f ? -INFINITY : m[c] + log2f(l[c]);
+          if (r0 == 0) a.ws_lse[slot * Hq + hq] = l[c] == 0.f ? -INFINITY : m[c] + log2f(l[c]);
         }
       }
-      left -= n;
-      b0 = 0;
-      if (!alive) break;
-    }
-  }
-  if (!alive) {
-    if (lane == 0) raise_error(a.err, PKV_ERR_TIMEOUT);
-    // every copy this warp started lands before the CTA's memory is released
-    for (uint32_t f = used; f < fill; ++f) {
-      if (withheld && f == 0) continue;   // (never started)
-      (void)mbar_wait(bar0 + 8 * (f % NS), (f / NS) & 1);
+      if (!alive) {
+        if (lane == 0) raise_error(a.err, PKV_ERR_TIMEOUT);
+        // every copy that this warp started lands before the CTA's memory is
+        // released: of the segment's blocks from the one not read on, the first NS
+        // are warp 0's, the later ones went round
+        for (uint32_t c = seg0; c < next_issue; ++c) {
+          const int k = static_cast<int>(c - seg0);
+          const int by = k < NS ? 0 : (k - NS + lag) & (team_warps - 1);
+          if (by == mate && !(withheld && c == 0) && c + NS >= next_issue)
+            (void)mbar_wait(full + 8 * (c % NS), (c / NS) & 1);
+        }
+      }
     }
   }
 }
 
-// One warp per (sequence, q head) with more than one partial:
-// out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M), in range order.
-template <int D>
+// WARPS warps per (sequence, q head) with more than one partial:
+// out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).  Bound by the latency of
+// its loads: a warp has those of 8 partials in flight together, and rows of
+// many partials (long contexts, few sequences) get 4 warps, which meet in
+// shared memory (fixed order: the same inputs give the same bits).
+template <int D, int WARPS>
 __global__ void __launch_bounds__(128) pkv_merge_int8_kernel(const DecodeInt8Args a) {
-  constexpr int PER = D / 32;
-  constexpr int kUnroll = 8;   // partials whose loads are in flight together
+  constexpr int PER = D / 32, kUnroll = 8;
+  __shared__ float sm_o[WARPS][D], sm_l[WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t gw = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int s = static_cast<int>(gw / a.num_q_heads);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = WARPS == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + warp : blockIdx.x;
+  const int me = WARPS == 1 ? 0 : warp;
+  const int s = static_cast<int>(row / a.num_q_heads);
   if (s >= a.num_seqs) return;
-  const int hq = static_cast<int>(gw - static_cast<int64_t>(s) * a.num_q_heads);
+  const int hq = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q_heads);
   const int2 span = a.span[s];
   if (span.y <= 1) return;   // nothing, or the decode kernel wrote the row
   if (span.x < 0 || span.y > a.max_ranges - span.x) return;   // (a launch that gave up)
@@ -490,12 +562,13 @@ __global__ void __launch_bounds__(128) pkv_merge_int8_kernel(const DecodeInt8Arg
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   float acc[PER] = {}, den = 0.f;
-  for (int i0 = 0; i0 < span.y; i0 += kUnroll) {
+  for (int i0 = me; i0 < span.y; i0 += kUnroll * WARPS) {
     float v[kUnroll][PER], lse[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int64_t k = slot(min(i0 + u, span.y - 1));
-      lse[u] = i0 + u < span.y ? a.ws_lse[k] : -INFINITY;
+      const int i = i0 + u * WARPS;
+      const int64_t k = slot(min(i, span.y - 1));
+      lse[u] = i < span.y ? a.ws_lse[k] : -INFINITY;
       const float* src = a.ws_o + k * D + lane * PER;
       if constexpr (PER == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src);
       else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src);
@@ -506,6 +579,19 @@ __global__ void __launch_bounds__(128) pkv_merge_int8_kernel(const DecodeInt8Arg
       den += w;
 #pragma unroll
       for (int e = 0; e < PER; ++e) acc[e] = w == 0.f ? acc[e] : fmaf(w, v[u][e], acc[e]);
+    }
+  }
+  if constexpr (WARPS > 1) {
+#pragma unroll
+    for (int e = 0; e < PER; ++e) sm_o[me][lane * PER + e] = acc[e];
+    if (lane == 0) sm_l[me] = den;
+    __syncthreads();
+    if (me != 0) return;
+#pragma unroll
+    for (int w = 1; w < WARPS; ++w) {
+      den += sm_l[w];
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] += sm_o[w][lane * PER + e];
     }
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
@@ -532,7 +618,9 @@ cudaError_t launch_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const Dec
   // a programmatic dependent of the decode launch: its CTAs are scheduled
   // beside the decode's last ones and wait for that grid's completion
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.num_seqs) * a.num_q_heads + 3) / 4));
+  const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
+  const bool wide = a.max_ranges / a.num_seqs >= 8;   // partials of a row, about
+  cfg.gridDim = dim3(static_cast<unsigned>(wide ? rows : (rows + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -540,7 +628,8 @@ cudaError_t launch_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const Dec
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pkv_merge_int8_kernel<D>, b);
+  return wide ? cudaLaunchKernelEx(&cfg, pkv_merge_int8_kernel<D, 4>, b)
+              : cudaLaunchKernelEx(&cfg, pkv_merge_int8_kernel<D, 1>, b);
 }
 
 }  // namespace

@@ -201,7 +201,14 @@ struct AttnInt8Args {
 };
 
 // Decode over sequences [0, num_seqs) of an int8 cache.
-constexpr int kDecInt8CtasPerSm = 4;   // resident CTAs (of 4 warps) per SM
+constexpr int kDecInt8Warps = 8;       // of a CTA
+constexpr int kDecInt8CtasPerSm = 2;   // resident CTAs per SM
+// Blocks of a range at least: below this a CTA's start and its partial cost
+// more than the keys it reads.
+constexpr int kMinRangeBlocks = 16;
+// Ranges at most, in multiples of num_ranges (the big ones, then what they
+// leave in small parts; see pkv_decode_int8.cu).
+constexpr int kMaxRangeWaves = 5;
 struct DecodeInt8Args {
   void* out;                     // bf16 [T, Hq, D]
   const void* q;
@@ -224,9 +231,11 @@ struct DecodeInt8Args {
   int32_t num_blocks;
   int32_t max_context_len;
   int32_t window;
-  int32_t range_blocks;          // blocks of a range (0: an equal share)
-  int32_t min_range_blocks;
-  int32_t num_ranges;            // ranges that fill the GPU (equal shares)
+  int32_t range_blocks;          // blocks of a range (0: chosen on the device)
+  int32_t num_ranges;            // ranges that give every resident team one
+  int32_t team_warps;            // 1, 2, 4 or 8 warps that walk a range together:
+  int32_t team_heads;            // this many kv heads (dividing num_kv_heads) x groups of 8 q heads
+  int32_t teams_per_range;
   int32_t max_ranges;            // ranges the workspace holds
   uint32_t grid;
   float scale_log2;
