@@ -976,7 +976,7 @@ int check_cache_int8(const pkv_cache_desc* c) {
 }
 
 // How the decode sequences of an int8 batch are cut: their blocks on one line,
-// in ranges (pkv_decode_int8.cu).
+// in equal ranges (pkv_decode_int8.cu).
 struct Int8Plan {
   int num_decode = 0;
   int col_groups = 1;     // groups of 8 q heads per kv head
@@ -1010,8 +1010,7 @@ int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms,
   const int64_t ranges =
       m->kv_split_tokens > 0
           ? (blocks + m->kv_split_tokens / kBlock - 1) / (m->kv_split_tokens / kBlock)
-          : std::min<int64_t>(static_cast<int64_t>(kMaxRangeWaves) * p->num_ranges,
-                              (blocks + kMinRangeBlocks - 1) / kMinRangeBlocks);
+          : std::min<int64_t>(p->num_ranges, (blocks + kMinRangeBlocks - 1) / kMinRangeBlocks);
   if (ranges * p->teams_per_range > INT32_MAX / 2 || blocks / p->num_ranges > INT32_MAX / 2) return PKV_E_SHAPE;
   p->max_ranges = static_cast<int>(std::max<int64_t>(ranges, 1));
   if (p->max_ranges > 1) {

@@ -13,8 +13,9 @@
 // not rounded at all; Q is scaled by a power of two into fp16's range.
 //
 // Split.  The decode sequences' blocks, one sequence after the other, form
-// one line, which is cut into ranges; a team of up to 8 warps walks a range,
-// whatever sequences lie in it, each warp with its own kv head (or group of 8
+// one line, which is cut into equal ranges, one for every team that the GPU
+// holds at a time; a team of up to 8 warps walks a range, whatever sequences
+// lie in it, each warp with its own kv head (or group of 8
 // q heads of one), over blocks that one TMA copy of K and one of V brings in
 // for all their heads.  Where a range ends inside a sequence its warps write
 // partials (normalised O and log2-sum-exp); a range holds at most two a head,
@@ -27,12 +28,11 @@
 //    different times they cost a DRAM row each (a warp per head and nothing
 //    that keeps the heads together: 5.1 TB/s, against 7.1 where they happened
 //    to run side by side), so a team reads its heads in one copy;
-//  * SMs of some GPCs get 15 % less bandwidth than the others: with equal
-//    ranges, one a team, they were waited for (183 us for 64 sequences of 32
-//    heads, the warps' mean being done at 154).  So the first ranges, one for every
-//    team that the GPU holds at a time, take only kBigShare of the line, and
-//    the rest goes out in parts of kSmallShare of an even share, which the
-//    block scheduler hands to the SMs that are done first.
+//  * with equal ranges the SMs of some GPCs, which get less bandwidth than the
+//    others, are waited for: 64 sequences of 32 heads are done at 150 us on
+//    the median and at 153 to 160 on the last SM.  Handing the last third out in small
+//    ranges to whoever is done costs more than that (their starts, their
+//    partials, and heads read out of step): 173 us against 165.
 #include <float.h>
 
 #include "pkv_common.cuh"
@@ -41,9 +41,6 @@
 namespace pkv {
 
 namespace {
-
-// In 1 / 64 of a team's even share of the line.
-constexpr int kBigShare = 44, kSmallShare = 10;
 
 constexpr int kWarps = kDecInt8Warps;
 constexpr int kThreads = kWarps * 32;
@@ -155,41 +152,20 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
     if (threadIdx.x == 0) upto[0] = 0;
     __syncthreads();
   }
-  // The ranges: num_big of big_blocks blocks each, then of small_blocks (a
-  // range's blocks fit 32 bits: the host sees to it).
-  __shared__ int big_blocks, small_blocks, num_big;
+  // blocks of a range: what the caller asked for, or an equal share (they fit
+  // 32 bits: the host sees to it)
+  __shared__ int range_blocks;
   int ranges;
   {
     const int64_t total = upto[kThreads];
-    int64_t big = 0, small = a.range_blocks;   // what the caller asked for
-    if (small == 0) {
-      const int64_t share = (total + a.num_ranges - 1) / a.num_ranges;
-      if (share * kSmallShare >= 64 * kMinRangeBlocks) {
-        big = share * kBigShare / 64;
-        small = (share * kSmallShare + 63) / 64;
-      } else {   // little work: equal ranges, one a team
-        small = max(share, static_cast<int64_t>(kMinRangeBlocks));
-      }
-    }
-    const int n_big = big > 0 ? a.num_ranges : 0;
-    ranges = n_big + static_cast<int>((total - n_big * big + small - 1) / small);
-    if (threadIdx.x == 0) {
-      big_blocks = static_cast<int>(big);
-      small_blocks = static_cast<int>(small);
-      num_big = n_big;
-    }
+    const int64_t R = a.range_blocks > 0
+                          ? a.range_blocks
+                          : max((total + a.num_ranges - 1) / a.num_ranges,
+                                static_cast<int64_t>(kMinRangeBlocks));
+    ranges = static_cast<int>((total + R - 1) / R);
+    if (threadIdx.x == 0) range_blocks = static_cast<int>(R);
     __syncthreads();
   }
-  // first block of range r, and the range of block x
-  auto range_begin = [&](int r) {
-    return r < num_big ? static_cast<int64_t>(r) * big_blocks
-                       : static_cast<int64_t>(num_big) * big_blocks +
-                             static_cast<int64_t>(r - num_big) * small_blocks;
-  };
-  auto range_of = [&](int64_t x) {
-    const int64_t y = x - static_cast<int64_t>(num_big) * big_blocks;
-    return y < 0 ? static_cast<int>(x / big_blocks) : num_big + static_cast<int>(y / small_blocks);
-  };
 
   const uint64_t policy = policy_evict_first();
   const uint64_t wlim = wait_limit(a.wait_limit_ns);
@@ -234,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
     // blocks that is, and how many blocks the range still has
     int s, b0, left;
     {
-      const int64_t begin = range_begin(range);
-      left = static_cast<int>(min(range_begin(range + 1), upto[kThreads]) - begin);
+      const int64_t begin = static_cast<int64_t>(range) * range_blocks;
+      left = static_cast<int>(min(static_cast<int64_t>(range_blocks), upto[kThreads] - begin));
       int64_t base;
       int th = 0;   // the last thread run that begins at or before `begin`
 #pragma unroll
@@ -488,8 +464,7 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
       // (a row all of whose blocks were bad, or a wait that gave up, has l = 0)
       const bool whole = b0 == 0 && n == nblk;
       if (b0 == 0 && kvh == 0 && gsub == 0 && lane == 0 && a.span != nullptr)
-        a.span[s] = make_int2(
-            range, range_of(min(range_begin(range + 1), upto[kThreads]) - left + nblk - 1) - range + 1);
+        a.span[s] = make_int2(range, 1 + (nblk - left + range_blocks - 1) / range_blocks);
       const int64_t slot = 2 * static_cast<int64_t>(range) + (b0 == 0 ? 1 : 0);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {

@@ -206,9 +206,6 @@ constexpr int kDecInt8CtasPerSm = 2;   // resident CTAs per SM
 // Blocks of a range at least: below this a CTA's start and its partial cost
 // more than the keys it reads.
 constexpr int kMinRangeBlocks = 16;
-// Ranges at most, in multiples of num_ranges (the big ones, then what they
-// leave in small parts; see pkv_decode_int8.cu).
-constexpr int kMaxRangeWaves = 5;
 struct DecodeInt8Args {
   void* out;                     // bf16 [T, Hq, D]
   const void* q;
@@ -231,7 +228,7 @@ struct DecodeInt8Args {
   int32_t num_blocks;
   int32_t max_context_len;
   int32_t window;
-  int32_t range_blocks;          // blocks of a range (0: chosen on the device)
+  int32_t range_blocks;          // blocks of a range (0: an equal share)
   int32_t num_ranges;            // ranges that give every resident team one
   int32_t team_warps;            // 1, 2, 4 or 8 warps that walk a range together:
   int32_t team_heads;            // this many kv heads (dividing num_kv_heads) x groups of 8 q heads
