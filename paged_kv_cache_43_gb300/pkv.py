@@ -489,7 +489,14 @@ def _int8_shapes(x, y, k_cache, v_cache, block_tables, context_lens, query_start
             and query_start_loc.shape[0] > S[0])
 
 
+# (the current stream's handle without the Stream object around it: 1 us of a
+# call that takes 10)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_on(dev: int, stream) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
     return (stream if stream is not None else torch.cuda.current_stream(dev)).cuda_stream
 
 
