@@ -975,28 +975,45 @@ int check_cache_int8(const pkv_cache_desc* c) {
   return check_cache(&as_bytes);
 }
 
-// How the decode sequences of an int8 batch are cut: their blocks on one line,
-// in equal ranges (pkv_decode_int8.cu).
+// How an int8 batch's decode sequences are cut.  Two kernels:
+//  * the split kernel (pkv_decode.cu) with the e4m3 plan: a CTA per (split of a
+//    sequence, kv head), merged in the CTA;
+//  * teams (pkv_decode_int8.cu): the sequences' blocks on one line in equal
+//    ranges, a team of warps reading 4 or 8 heads (or groups of 8 q heads) in one
+//    copy.
+// Teams where they have 4 warps or more and a range gets 32 blocks or more, by
+// max_context_len.  Measured, split against teams, us (q / kv heads, head_size
+// 128): 32 / 8, 16 sequences of 8K to 16K keys 85 - 78, 64 of 64 to 8192 102 - 94,
+// 512 of 64 to 512 71 - 63; 32 / 32, 128 of 1K to 3K 328 - 306; 128 / 8, 128 of 1K to
+// 3K 183 - 136; below the rule 32 / 8, 8 of 2000 15 - 25, 128 of 100 to 1000 36 - 38;
+// teams of one warp (10 / 5), 16 of 8K to 16K 58 - 62.
+constexpr int kTeamRangeBlocks = 32;
+
 struct Int8Plan {
-  int num_decode = 0;
-  int col_groups = 1;     // groups of 8 q heads per kv head
+  Plan split;              // num_decode, and the split kernel's cut
+  bool teams = false;
+  int col_groups = 1;      // groups of 8 q heads per kv head
   int team_heads = 1, team_warps = 1;
   int teams_per_range = 1;
-  int num_ranges = 1;     // ranges that give every resident team one
-  int max_ranges = 1;     // that there can be: the workspace has two slots for each
-  size_t ws_o_bytes = 0, ws_lse_bytes = 0, ws_bytes = 0;
+  int num_ranges = 1;      // ranges that give every resident team one
+  int max_ranges = 1;      // that there can be: the workspace has two slots for each
+  size_t ws_o_bytes = 0, ws_lse_bytes = 0;
+  size_t ws_bytes = 0;     // of the kernel taken
 };
 
 int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms, Int8Plan* p) {
   *p = Int8Plan{};
-  p->num_decode = m->max_query_len <= 1 ? m->num_seqs : std::max(m->num_decode_seqs, 0);
-  if (p->num_decode == 0) return PKV_OK;
+  pkv_cache_desc as_bytes = *c;
+  as_bytes.dtype = PKV_FP8_E4M3;
+  if (int st = make_plan(&as_bytes, m, num_sms, &p->split)) return st;
+  p->ws_bytes = p->split.ws_bytes;
+  const int nd = p->split.num_decode;
+  if (nd == 0) return PKV_OK;
   p->col_groups = (m->num_q_heads / c->num_kv_heads + 7) / 8;
   // a team: kv heads side by side, read in one copy (the largest power of two
   // that divides their number), times the groups of 8 q heads that share them
   int cols = 1;
   while (2 * cols <= std::min(p->col_groups, kDecInt8Warps)) cols *= 2;
-  p->team_heads = 1;
   while (2 * p->team_heads * cols <= kDecInt8Warps && c->num_kv_heads % (2 * p->team_heads) == 0)
     p->team_heads *= 2;
   p->team_warps = p->team_heads * cols;
@@ -1006,19 +1023,25 @@ int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms,
   int64_t longest = (static_cast<int64_t>(m->max_context_len) + kBlock - 1) / kBlock;
   if (m->sliding_window > 0)   // W keys span at most (W + 14) / 16 + 1 blocks
     longest = std::min(longest, (static_cast<int64_t>(m->sliding_window) + 14) / kBlock + 1);
-  const int64_t blocks = longest * p->num_decode;
+  const int64_t blocks = longest * nd;
+  if (p->team_warps < 4 || blocks < static_cast<int64_t>(kTeamRangeBlocks) * p->num_ranges)
+    return PKV_OK;
   const int64_t ranges =
       m->kv_split_tokens > 0
           ? (blocks + m->kv_split_tokens / kBlock - 1) / (m->kv_split_tokens / kBlock)
           : std::min<int64_t>(p->num_ranges, (blocks + kMinRangeBlocks - 1) / kMinRangeBlocks);
-  if (ranges * p->teams_per_range > INT32_MAX / 2 || blocks / p->num_ranges > INT32_MAX / 2) return PKV_E_SHAPE;
+  // (counts that the kernel holds in 32 bits)
+  if (ranges * p->teams_per_range > INT32_MAX / 2 || blocks / p->num_ranges > INT32_MAX / 2)
+    return PKV_OK;
+  p->teams = true;
   p->max_ranges = static_cast<int>(std::max<int64_t>(ranges, 1));
+  p->ws_bytes = 0;
   if (p->max_ranges > 1) {
     const size_t rows = 2 * static_cast<size_t>(p->max_ranges) * m->num_q_heads;
     p->ws_o_bytes = round_up(rows * c->head_size * sizeof(float), 256);
     p->ws_lse_bytes = round_up(rows * sizeof(float), 256);
     p->ws_bytes = p->ws_o_bytes + p->ws_lse_bytes +
-                  round_up(static_cast<size_t>(p->num_decode) * sizeof(int2), 256);
+                  round_up(static_cast<size_t>(nd) * sizeof(int2), 256);
   }
   return PKV_OK;
 }
@@ -1110,11 +1133,17 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
   const cudaStream_t st = as_stream(stream);
   const float scale_log2 = scale * 1.4426950408889634f;
   const int G = meta->num_q_heads / cache->num_kv_heads;
-  auto decode_part = [&](cudaStream_t st) -> int {
-    CUtensorMap kmap, vmap;
-    if (int e = encode_heads_map(&kmap, k_cache, *cache, p.team_heads)) return e;
-    if (int e = encode_heads_map(&vmap, v_cache, *cache, p.team_heads)) return e;
-    DecodeInt8Args d{};
+  const int nd = p.split.num_decode, npf = meta->num_seqs - nd;
+  CUtensorMap kmap, vmap;   // one head's block a copy: the split and the prefill kernels
+  if (!p.teams || npf > 0) {
+    if (int e = encode_cache_map(&kmap, k_cache, *cache)) return e;
+    if (int e = encode_cache_map(&vmap, v_cache, *cache)) return e;
+  }
+  auto team_part = [&](cudaStream_t st) -> int {
+    CUtensorMap khmap, vhmap;
+    if (int e = encode_heads_map(&khmap, k_cache, *cache, p.team_heads)) return e;
+    if (int e = encode_heads_map(&vhmap, v_cache, *cache, p.team_heads)) return e;
+    TeamDecodeArgs d{};
     d.out = out;
     d.q = q;
     d.k_scales = k_scales;
@@ -1130,7 +1159,7 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     }
     d.err = err;
     d.bt_stride = meta->block_table_stride;
-    d.num_seqs = p.num_decode;
+    d.num_seqs = nd;
     d.num_tokens = meta->num_tokens;
     d.num_q_heads = meta->num_q_heads;
     d.num_kv_heads = cache->num_kv_heads;
@@ -1149,10 +1178,39 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     d.grid = static_cast<uint32_t>((static_cast<int64_t>(p.max_ranges) * p.teams_per_range +
                                     cta_teams - 1) / cta_teams);
     d.scale_log2 = scale_log2;
-    PKV_TRY(launch_decode_int8(kmap, vmap, d, cache->head_size, p.max_ranges > 1, st));
+    PKV_TRY(launch_team_decode(khmap, vhmap, d, cache->head_size, p.max_ranges > 1, st));
     return PKV_OK;
   };
-  const int npf = meta->num_seqs - p.num_decode;
+  auto decode_part = [&](cudaStream_t st) -> int {
+    if (p.teams) return team_part(st);
+    DecodeArgs d{};
+    d.out = out;
+    d.q = q;
+    d.block_tables = block_tables;
+    d.context_lens = context_lens;
+    d.query_start_loc = query_start_loc;
+    d.ws_o = p.ws_bytes ? static_cast<float*>(workspace) : nullptr;
+    d.ws_lse = p.ws_bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.split.ws_o_bytes)
+                          : nullptr;
+    d.err = err;
+    d.bt_stride = meta->block_table_stride;
+    d.num_seqs = nd;
+    d.num_q_heads = meta->num_q_heads;
+    d.num_kv_heads = cache->num_kv_heads;
+    d.group = G;
+    d.num_blocks = cache->num_blocks;
+    d.split_blocks = p.split.split_blocks;
+    d.max_splits = p.split.max_splits;
+    d.num_tokens = meta->num_tokens;
+    d.max_context_len = meta->max_context_len;
+    d.window = meta->sliding_window;
+    d.k_scales = k_scales;
+    d.v_scales = v_scales;
+    d.scale_log2 = scale_log2;
+    PKV_TRY(launch_decode_int8(kmap, vmap, d, cache->head_size, st));
+    PKV_TRY(launch_combine_bf16(d, cache->head_size, st, /*after_decode=*/true));
+    return PKV_OK;
+  };
   auto prefill_part = [&](cudaStream_t st) -> int {
     if (G > 128) {   // more q heads on a kv head than a query tile has rows
       AttnInt8Args a{};
@@ -1167,7 +1225,7 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
       a.query_start_loc = query_start_loc;
       a.err = err;
       a.bt_stride = meta->block_table_stride;
-      a.seq_begin = p.num_decode;
+      a.seq_begin = nd;
       a.num_seqs = meta->num_seqs;
       a.num_tokens = meta->num_tokens;
       a.num_q_heads = meta->num_q_heads;
@@ -1187,7 +1245,7 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     f.query_start_loc = query_start_loc;
     f.err = err;
     f.bt_stride = meta->block_table_stride;
-    f.seq_begin = p.num_decode;
+    f.seq_begin = nd;
     f.num_seqs = npf;
     f.num_q_heads = meta->num_q_heads;
     f.num_kv_heads = cache->num_kv_heads;
@@ -1199,12 +1257,10 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     f.k_scales = k_scales;
     f.v_scales = v_scales;
     f.scale_log2 = scale_log2;
-    f.longest_first = p.num_decode == 0 ? 1 : 0;   // alone on the GPU, or beside decode
+    f.longest_first = nd == 0 ? 1 : 0;   // alone on the GPU, or beside decode
     const int toks = prefill_tc_tokens_per_cta(G);
     f.num_mtiles = (meta->max_query_len + toks - 1) / toks;
-    CUtensorMap qmap, omap, kmap, vmap;
-    if (int e = encode_cache_map(&kmap, k_cache, *cache)) return e;
-    if (int e = encode_cache_map(&vmap, v_cache, *cache)) return e;
+    CUtensorMap qmap, omap;
     if (int e = encode_query_map(&qmap, q, meta->num_tokens, meta->num_q_heads, cache->head_size, G))
       return e;
     if (int e =
@@ -1213,7 +1269,7 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     PKV_TRY(launch_prefill_tc_int8(qmap, kmap, vmap, omap, f, cache->head_size, st));
     return PKV_OK;
   };
-  if (p.num_decode == 0) return prefill_part(st);
+  if (nd == 0) return prefill_part(st);
   if (npf == 0) return decode_part(st);
   // decode and prefill rows in one batch: as pkv_attention
   SideFork fork(dev, st);

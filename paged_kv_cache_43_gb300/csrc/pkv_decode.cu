@@ -37,6 +37,21 @@ namespace {
 
 constexpr int kDecodeWarps = 4;
 
+// What the caches hold (the kernel's template switch).
+constexpr int kBf16 = 0, kE4m3 = 1, kInt8 = 2;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool I8>
+__device__ __forceinline__ uint2 codes_to_f16x4(uint32_t codes) {
+  if constexpr (I8) return i8x4_to_f16x4(codes);
+  else return e4m3x4_to_f16x4(codes);
+}
+
 template <int D, bool FP8>
 struct DecodeTile {
   static constexpr int kHalves = D / 64;             // 64-column TMA boxes per row
@@ -59,10 +74,12 @@ constexpr int decode_smem_bytes() {
 // sequence gc / G, q head kvh * G + gc % G), all reading the shared prefix
 // keys [0, prefix_len) through sequence 0's block table; every column writes
 // a partial.  Otherwise the columns are q heads of one sequence's query row.
-template <int D, int NS, bool FP8, bool PREFIX>
+template <int D, int NS, int FMT, bool PREFIX>
 __global__ void __launch_bounds__(kDecodeWarps * 32)
     pkv_decode_bf16_kernel(const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap, const DecodeArgs a) {
+  constexpr bool FP8 = FMT != kBf16;   // one-byte codes, widened to fp16
+  constexpr bool I8 = FMT == kInt8;
   using T = DecodeTile<D, FP8>;
   constexpr int NW = kDecodeWarps;
   // Every CTA of this grid is resident once it runs this: the combine launch
@@ -194,6 +211,17 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
   for (int i = 0; i < n_pro; ++i) issue(i);
   int issued = n_pro;  // blocks whose copies have been started
 
+  // Int8: lane i holds the scales of its i-th block (K scale, log2 of the V
+  // scale; a block with a bad id is not computed).
+  float my_ks = 1.f, my_lv = 0.f;
+  if constexpr (I8) {
+    if (lane < nb_w && my_ok) {
+      const int64_t at = static_cast<int64_t>(my_bid) * a.num_kv_heads + kvh;
+      my_ks = int8_scale(__ldg(a.k_scales + at));
+      my_lv = int8_scale(__ldg(a.v_scales + at));
+    }
+  }
+
   // Q^T as the B operand: lane holds Q[g = lane/4][kk*16 + 2*(lane%4) + {0,1}]
   // (qb[kk][0]) and the same +8 (qb[kk][1]); heads past the group are zero.
   // FP8: the contraction runs over a permutation of d instead (any order
@@ -232,8 +260,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
   float scale_log2 = a.scale_log2, out_scale = 1.f;
   float col_scale[2] = {scale_log2, scale_log2};  // score scale of head columns c0, c0 + 1
   if constexpr (FP8) {
-    scale_log2 *= __ldg(a.k_descale + static_cast<int64_t>(s) * a.num_kv_heads + kvh);
-    out_scale = __ldg(a.v_descale + static_cast<int64_t>(s) * a.num_kv_heads + kvh);
+    if constexpr (!I8) {
+      scale_log2 *= __ldg(a.k_descale + static_cast<int64_t>(s) * a.num_kv_heads + kvh);
+      out_scale = __ldg(a.v_descale + static_cast<int64_t>(s) * a.num_kv_heads + kvh);
+    }
     float amax = 0.f;
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
@@ -242,7 +272,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
         amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(qb[kk][j])), fabsf(bf16_hi(qb[kk][j]))));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));  // the 4 lanes of head lane/4
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const int e = f16_row_exponent(amax);
+    const int e = I8 ? f16_fit_exponent(amax) : f16_row_exponent(amax);
     const float down = pow2f(-e);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
@@ -319,6 +349,58 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
     pb1 = movmatrix_trans(pk1);
   };
 
+  // Int8: the same step with the block's scales.  The weight that meets the V
+  // codes is w = 2^(x + log2 sv - m), m following the largest x + log2 sv: w in
+  // fp16 is at most 2^8 and exact to 2^-11 of the numerator's largest terms
+  // whatever the scales' sizes; the denominator adds w / sv, in fp32 and before
+  // the rounding.
+  auto softmax_step_i8 = [&](const float (&sc)[4], int i, int p0, uint32_t& pb0, uint32_t& pb1) {
+    const float ks = __shfl_sync(0xffffffffu, my_ks, i);
+    const float lv = __shfl_sync(0xffffffffu, my_lv, i);
+    const float f0 = col_scale[0] * ks, f1 = col_scale[1] * ks;
+    float y[4] = {fmaf(sc[0], f0, lv), fmaf(sc[1], f1, lv), fmaf(sc[2], f0, lv),
+                  fmaf(sc[3], f1, lv)};
+    if (p0 + kBlock > L || p0 < kfirst) {
+      const bool v0 = p0 + r0 < L && p0 + r0 >= kfirst;
+      const bool v1 = p0 + r0 + 8 < L && p0 + r0 + 8 >= kfirst;
+      if (!v0) y[0] = y[1] = -INFINITY;
+      if (!v1) y[2] = y[3] = -INFINITY;
+    }
+    const float lim0 = m[0] + 8.f, lim1 = m[1] + 8.f;
+    if (__any_sync(0xffffffffu, y[0] > lim0 || y[1] > lim1 || y[2] > lim0 || y[3] > lim1)) {
+      float mx0 = fmaxf(y[0], y[2]), mx1 = fmaxf(y[1], y[3]);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+      }
+      const float mn0 = fmaxf(m[0], mx0), mn1 = fmaxf(m[1], mx1);
+      const float alpha0 = mn0 == -INFINITY ? 1.f : ex2(m[0] - mn0);
+      const float alpha1 = mn1 == -INFINITY ? 1.f : ex2(m[1] - mn1);
+      m[0] = mn0;
+      m[1] = mn1;
+      l[0] *= alpha0;
+      l[1] *= alpha1;
+#pragma unroll
+      for (int dt = 0; dt < D / 16; ++dt) {
+        o[dt][0] *= alpha0;
+        o[dt][1] *= alpha1;
+        o[dt][2] *= alpha0;
+        o[dt][3] *= alpha1;
+      }
+    }
+    const float mu0 = m[0] == -INFINITY ? 0.f : m[0];   // every key so far masked
+    const float mu1 = m[1] == -INFINITY ? 0.f : m[1];
+    const float w0 = ex2(y[0] - mu0), w1 = ex2(y[1] - mu1);
+    const float w2 = ex2(y[2] - mu0), w3 = ex2(y[3] - mu1);
+    const float ivs = ex2(-lv);
+    l[0] = fmaf(w0 + w2, ivs, l[0]);
+    l[1] = fmaf(w1 + w3, ivs, l[1]);
+    pb0 = movmatrix_trans(pack_f16(w0, w1));
+    pb1 = movmatrix_trans(pack_f16(w2, w3));
+  };
+  if constexpr (I8) my_lv = log2f(my_lv == 0.f ? 1.f : my_lv);   // (0: no block)
+
   // FP8: this lane's fragment offsets inside a block's code tiles (the same
   // for every block): K rows r0, r0 + 8 at chunks (D/64) t + c; V rows 2t,
   // 2t+1, 2t+8, 2t+9 at the lane's D/8 bytes (see the loop below).
@@ -373,7 +455,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
             vw[q][0] = u.x; vw[q][1] = u.y;
           }
         }
-        if (p0 + kBlock > L) {  // the last block: rows past the context hold stale codes
+        if (!I8 && p0 + kBlock > L) {  // the last block: rows past the context hold stale codes
+                                       // (int8: finite, and their weights are zero)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             if (p0 + 2 * t + (q & 1) + 8 * (q >> 1) >= L) {
@@ -397,20 +480,21 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&kw[0][kk / 4]);
           const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&kw[1][kk / 4]);
-          const uint2 x = e4m3x4_to_f16x4(w0[kk % 4]), y = e4m3x4_to_f16x4(w1[kk % 4]);
+          const uint2 x = codes_to_f16x4<I8>(w0[kk % 4]), y = codes_to_f16x4<I8>(w1[kk % 4]);
           mma_16816<true>((kk & 1) ? sd : sc, x.x, y.x, x.y, y.y, qb[kk][0], qb[kk][1]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) sc[j] += sd[j];
         uint32_t pb0, pb1;
-        softmax_step(sc, p0, pb0, pb1);
+        if constexpr (I8) softmax_step_i8(sc, i, p0, pb0, pb1);
+        else softmax_step(sc, p0, pb0, pb1);
         // ---- O^T += V^T . P^T
 #pragma unroll
         for (int dt = 0; dt < D / 16; ++dt) {
           // bytes 2dt, 2dt+1 of rows (2t, 2t+1) interleaved: (k0,d0) (k1,d0) (k0,d1) (k1,d1)
           const uint32_t sel = (dt & 1) ? 0x7362u : 0x5140u;
-          const uint2 lo = e4m3x4_to_f16x4(prmt(vw[0][dt / 2], vw[1][dt / 2], sel));
-          const uint2 hi = e4m3x4_to_f16x4(prmt(vw[2][dt / 2], vw[3][dt / 2], sel));
+          const uint2 lo = codes_to_f16x4<I8>(prmt(vw[0][dt / 2], vw[1][dt / 2], sel));
+          const uint2 hi = codes_to_f16x4<I8>(prmt(vw[2][dt / 2], vw[3][dt / 2], sel));
           mma_16816<true>(o[dt], lo.x, lo.y, hi.x, hi.y, pb0, pb1);
         }
       }
@@ -658,11 +742,11 @@ __global__ void __launch_bounds__(128) pkv_combine_bf16_kernel(const DecodeArgs 
         __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <int D, int NS, bool FP8, bool PREFIX = false>
+template <int D, int NS, int FMT, bool PREFIX = false>
 cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
                             const DecodeArgs& a, cudaStream_t stream) {
-  constexpr int smem = decode_smem_bytes<D, NS, FP8>();
-  auto kfn = pkv_decode_bf16_kernel<D, NS, FP8, PREFIX>;
+  constexpr int smem = decode_smem_bytes<D, NS, FMT != kBf16>();
+  auto kfn = pkv_decode_bf16_kernel<D, NS, FMT, PREFIX>;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // prefix launch: (prefix split, kv head x column group); otherwise (split of
@@ -688,18 +772,25 @@ cudaError_t launch_decode_bf16(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                cudaStream_t stream) {
   if (a.num_seqs == 0) return cudaSuccess;
   if (fp8) {
-    if (head_size == 128) return launch_decode_t<128, 3, true>(kmap, vmap, a, stream);
-    return launch_decode_t<64, 6, true>(kmap, vmap, a, stream);
+    if (head_size == 128) return launch_decode_t<128, 3, kE4m3>(kmap, vmap, a, stream);
+    return launch_decode_t<64, 6, kE4m3>(kmap, vmap, a, stream);
   }
-  if (head_size == 128) return launch_decode_t<128, 3, false>(kmap, vmap, a, stream);
-  return launch_decode_t<64, 4, false>(kmap, vmap, a, stream);
+  if (head_size == 128) return launch_decode_t<128, 3, kBf16>(kmap, vmap, a, stream);
+  return launch_decode_t<64, 4, kBf16>(kmap, vmap, a, stream);
+}
+
+cudaError_t launch_decode_int8(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const DecodeArgs& a, int head_size, cudaStream_t stream) {
+  if (a.num_seqs == 0) return cudaSuccess;
+  if (head_size == 128) return launch_decode_t<128, 3, kInt8>(kmap, vmap, a, stream);
+  return launch_decode_t<64, 6, kInt8>(kmap, vmap, a, stream);
 }
 
 cudaError_t launch_cascade_prefix_bf16(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                        const DecodeArgs& a, int head_size, cudaStream_t stream) {
   if (a.num_seqs == 0 || a.prefix_splits == 0) return cudaSuccess;
-  if (head_size == 128) return launch_decode_t<128, 3, false, true>(kmap, vmap, a, stream);
-  return launch_decode_t<64, 4, false, true>(kmap, vmap, a, stream);
+  if (head_size == 128) return launch_decode_t<128, 3, kBf16, true>(kmap, vmap, a, stream);
+  return launch_decode_t<64, 4, kBf16, true>(kmap, vmap, a, stream);
 }
 
 cudaError_t launch_combine_bf16(const DecodeArgs& a, int head_size, cudaStream_t stream,

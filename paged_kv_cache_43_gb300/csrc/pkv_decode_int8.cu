@@ -1,5 +1,7 @@
 // pkv_decode_int8.cu -- decode attention (one query row per sequence) over
-// int8 caches with one fp32 scale per (block of 16 tokens, kv head).
+// int8 caches with one fp32 scale per (block of 16 tokens, kv head), for large
+// batches; small ones take the split kernel of pkv_decode.cu (make_int8_plan in
+// pkv_api.cu has the rule and both sides' times).
 //
 // Mathematics.  With codes c, block scales sk and sv, and x_p = scale log2(e)
 // sk[b(p)] (q . ck_p):
@@ -66,7 +68,7 @@ struct DecSeq {
   __device__ __forceinline__ int blocks() const { return (L + kBlock - 1) / kBlock - first / kBlock; }
 };
 
-__device__ __forceinline__ bool dec_seq(const DecodeInt8Args& a, int s, DecSeq* r, int32_t* bits) {
+__device__ __forceinline__ bool dec_seq(const TeamDecodeArgs& a, int s, DecSeq* r, int32_t* bits) {
   *bits = 0;
   r->q0 = __ldg(a.query_start_loc + s);
   const int qn = __ldg(a.query_start_loc + s + 1) - r->q0;
@@ -83,8 +85,8 @@ __device__ __forceinline__ bool dec_seq(const DecodeInt8Args& a, int s, DecSeq* 
 
 template <int D, int NS>
 __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
-    pkv_decode_int8_kernel(const __grid_constant__ CUtensorMap kmap,
-                           const __grid_constant__ CUtensorMap vmap, const DecodeInt8Args a) {
+    pkv_team_decode_kernel(const __grid_constant__ CUtensorMap kmap,
+                           const __grid_constant__ CUtensorMap vmap, const TeamDecodeArgs a) {
   constexpr int kTile = D * kBlock;        // one block of one head, K or V: bytes
   // (the merge launch may be scheduled beside this grid's last CTAs; it waits
   // for the grid's completion itself)
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
 // many partials (long contexts, few sequences) get 4 warps, which meet in
 // shared memory (fixed order: the same inputs give the same bits).
 template <int D, int WARPS>
-__global__ void __launch_bounds__(128) pkv_merge_int8_kernel(const DecodeInt8Args a) {
+__global__ void __launch_bounds__(128) pkv_team_merge_kernel(const TeamDecodeArgs a) {
   constexpr int PER = D / 32, kUnroll = 8;
   __shared__ float sm_o[WARPS][D], sm_l[WARPS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -579,13 +581,13 @@ __global__ void __launch_bounds__(128) pkv_merge_int8_kernel(const DecodeInt8Arg
 }
 
 template <int D, int NS>
-cudaError_t launch_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeInt8Args& a,
+cudaError_t launch_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const TeamDecodeArgs& a,
                      bool merge, cudaStream_t stream) {
   constexpr int smem = dec8_smem_bytes<D, NS>();
-  auto kfn = pkv_decode_int8_kernel<D, NS>;
+  auto kfn = pkv_team_decode_kernel<D, NS>;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  DecodeInt8Args b = a;
+  TeamDecodeArgs b = a;
   debug_wait_settings(&b.wait_limit_ns, &b.debug_stall);
   kfn<<<a.grid, kThreads, smem, stream>>>(kmap, vmap, b);
   e = cudaGetLastError();
@@ -603,14 +605,14 @@ cudaError_t launch_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const Dec
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return wide ? cudaLaunchKernelEx(&cfg, pkv_merge_int8_kernel<D, 4>, b)
-              : cudaLaunchKernelEx(&cfg, pkv_merge_int8_kernel<D, 1>, b);
+  return wide ? cudaLaunchKernelEx(&cfg, pkv_team_merge_kernel<D, 4>, b)
+              : cudaLaunchKernelEx(&cfg, pkv_team_merge_kernel<D, 1>, b);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_int8(const CUtensorMap& kmap, const CUtensorMap& vmap,
-                               const DecodeInt8Args& a, int head_size, bool merge,
+cudaError_t launch_team_decode(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const TeamDecodeArgs& a, int head_size, bool merge,
                                cudaStream_t stream) {
   if (head_size == 128) return launch_t<128, 3>(kmap, vmap, a, merge, stream);
   return launch_t<64, 6>(kmap, vmap, a, merge, stream);

@@ -71,6 +71,9 @@ struct DecodeArgs {
   // that its wait runs out.
   uint64_t wait_limit_ns;
   int32_t debug_stall;
+  // Int8 cache: block scales [num_blocks, Hkv] (null otherwise)
+  const float* k_scales;
+  const float* v_scales;
 };
 
 // Varlen causal attention over sequences [seq_begin, seq_begin + num_seqs).
@@ -200,13 +203,14 @@ struct AttnInt8Args {
   float scale_log2;
 };
 
-// Decode over sequences [0, num_seqs) of an int8 cache.
+// Decode over sequences [0, num_seqs) of an int8 cache by teams of warps
+// (pkv_decode_int8.cu): large batches.
 constexpr int kDecInt8Warps = 8;       // of a CTA
 constexpr int kDecInt8CtasPerSm = 2;   // resident CTAs per SM
 // Blocks of a range at least: below this a CTA's start and its partial cost
 // more than the keys it reads.
 constexpr int kMinRangeBlocks = 16;
-struct DecodeInt8Args {
+struct TeamDecodeArgs {
   void* out;                     // bf16 [T, Hq, D]
   const void* q;
   const float* k_scales;
@@ -261,9 +265,12 @@ struct CopyArgs {
 cudaError_t launch_write(const WriteArgs& a, cudaStream_t stream, int num_sms);
 cudaError_t launch_write_int8(const WriteInt8Args& a, cudaStream_t stream);
 cudaError_t launch_attention_int8(const AttnInt8Args& a, int head_size, cudaStream_t stream);
-cudaError_t launch_decode_int8(const CUtensorMap& kmap, const CUtensorMap& vmap,
-                               const DecodeInt8Args& a, int head_size, bool merge,
+cudaError_t launch_team_decode(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const TeamDecodeArgs& a, int head_size, bool merge,
                                cudaStream_t stream);
+// The decode kernel over int8 caches with block scales (a.k_scales, a.v_scales).
+cudaError_t launch_decode_int8(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                               const DecodeArgs& a, int head_size, cudaStream_t stream);
 cudaError_t launch_copy_blocks(const CopyArgs& a, unsigned units, cudaStream_t stream);
 cudaError_t launch_write_fp8(const WriteArgs& a, cudaStream_t stream, int num_sms);
 // fp8 = true: the caches hold e4m3 codes (the maps are uint8, unswizzled).

@@ -105,7 +105,7 @@ def tolerance(ref, vmax):
 def attend(cache, q, bt, cl, qsl, scale, window=0, out=None, **kw):
     """GPU output and the oracle's (fp64), with the tolerance."""
     kw.setdefault("max_query_len", int((qsl[1:] - qsl[:-1]).max()))
-    kw.setdefault("max_context_len", int(cl.max()))
+    kw["max_context_len"] = kw.get("max_context_len") or int(cl.max())
     out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda") if out is None else out
     pkv.attention_int8(out, q.cuda(), cache.gpu[0], cache.gpu[1], bt.cuda(), cl.cuda(), qsl.cuda(),
                        scale, cache.gpu[2], cache.gpu[3], sliding_window=window, **kw)
@@ -244,6 +244,12 @@ def test_write_many_sequences_of_a_few_rows(seqs):
 
 # -------------------------------------------------------------- attention
 
+# max_context_len decides between the two decode kernels: the longest context
+# (small batches: a CTA per split and head), or a bound of this many tokens
+# (teams of warps over equal ranges of all the batch's blocks).
+LOOSE = 20000
+BOUNDS = [None, LOOSE]
+
 EDGE_CTX = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 300, 511, 513, 700]
 
 
@@ -256,12 +262,37 @@ def batch(ctx, q, hq, hkv, d, seed, step=None, pad=0):
     return cache, rows(gen, sum(q), hq, d), bt, i32(ctx), starts(q), d ** -0.5
 
 
+@pytest.mark.parametrize("bound", BOUNDS)
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 2), (8, 1), (12, 4), (32, 2), (5, 1), (24, 2)])
-def test_decode_edge_lengths_and_groups(hq, hkv, d):
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 2), (8, 1), (12, 4), (32, 2), (5, 1), (24, 2),
+                                    (8, 8), (24, 24), (70, 2), (100, 1), (12, 12), (60, 20)])
+def test_decode_edge_lengths_and_groups(hq, hkv, d, bound):
     b = batch(EDGE_CTX, [1] * len(EDGE_CTX), hq, hkv, d, seed=hq * 100 + hkv + d, step=100, pad=2)
     for split in (0, 64, 192):
-        check_attention(*b, kv_split_tokens=split)
+        check_attention(*b, kv_split_tokens=split, max_context_len=bound)
+    assert pkv.get_error() == 0
+
+
+@pytest.mark.parametrize("seqs", [1, 3, 255, 256, 257, 600])
+def test_decode_many_short_sequences_and_empty_ones(seqs):
+    """Ranges with many sequences in them; sequences without rows, single keys."""
+    rng = np.random.default_rng(seqs)
+    ctx = rng.integers(1, 70, seqs)
+    ctx[seqs // 2] = 900
+    full = batch(ctx.tolist(), [1] * seqs, 8, 8, 64, seed=seqs)
+    for bound in BOUNDS:
+        check_attention(*full, max_context_len=bound)
+    cache, qs, bt, cl, qsl, scale = full
+    live = rng.random(seqs) < 0.6
+    live[seqs // 2] = True
+    cl2 = torch.where(torch.from_numpy(live), cl, 0)
+    qsl2 = starts(live.astype(int).tolist())
+    for bound in BOUNDS:
+        got, ref, tol = attend(cache, qs, bt, cl2.to(torch.int32), qsl2, scale,
+                               max_context_len=bound,
+                               out=torch.full(qs.shape, 7.0, dtype=torch.bfloat16, device="cuda"))
+        n = int(live.sum())
+        assert (np.abs(got - ref) / tol)[:n].max() <= 1 and (got[n:] == 7.0).all()
     assert pkv.get_error() == 0
 
 
@@ -282,46 +313,52 @@ def test_prefill_full_tiles(d):
     check_attention(*batch([128, 500, 256, 700, 50], q, 12, 4, d, seed=10 + d))
 
 
+@pytest.mark.parametrize("bound", BOUNDS)
 @pytest.mark.parametrize("window", [1, 17, 100, 1000])
-def test_sliding_window_never_reads_blocks_before_it(window):
+def test_sliding_window_never_reads_blocks_before_it(window, bound):
     q, ctx = [1, 1, 1, 40, 1, 64], [1, 300, 1000, 400, 1500, 1200]
     cache, qs, bt, cl, qsl, scale = batch(ctx, q, 16, 4, 128, seed=window)
     for nd in (-1, 3):
-        check_attention(cache, qs, bt, cl, qsl, scale, window=window, num_decode_seqs=nd)
+        check_attention(cache, qs, bt, cl, qsl, scale, window=window, num_decode_seqs=nd,
+                        max_context_len=bound)
     # blocks wholly before every window: null entries give the same result
     for s in range(len(q)):
         first = max(0, ctx[s] - q[s] - window + 1) // 16
         bt[s, :first] = -1
     out = torch.empty_like(qs.cuda())
     pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], bt.cuda(), cl.cuda(), qsl.cuda(), scale,
-                       *cache.gpu[2:], max_query_len=64, max_context_len=1500, num_decode_seqs=3,
+                       *cache.gpu[2:], max_query_len=64, max_context_len=bound or 1500,
+                       num_decode_seqs=3,
                        sliding_window=window)
     assert pkv.get_error() == 0 and torch.isfinite(out.float()).all()
 
 
+@pytest.mark.parametrize("bound", [None, 200000])
 @pytest.mark.parametrize("nd", [-1, 0, 3, 6])
-def test_mixed_batches_and_declared_decode_runs(nd):
+def test_mixed_batches_and_declared_decode_runs(nd, bound):
     q, ctx = [1, 1, 1, 1, 1, 1, 70, 1, 33], [5, 700, 64, 1, 333, 90, 300, 17, 33]
-    check_attention(*batch(ctx, q, 16, 4, 128, seed=5), num_decode_seqs=nd)
+    check_attention(*batch(ctx, q, 16, 4, 128, seed=5), num_decode_seqs=nd, max_context_len=bound)
 
 
 def test_rows_behind_the_last_sequence_and_empty_sequences_are_left_alone():
     ctx, q = [20, 0, 37, 9, 0], [1, 0, 1, 1, 0]
-    cache, qs, bt, cl, qsl, scale = batch([20, 1, 37, 9, 1], [1] * 5, 8, 2, 64, seed=3)
+    cache, qs, bt, cl, qsl, scale = batch([20, 1, 37, 9, 1], [1] * 5, 8, 4, 64, seed=3)
     cl, qsl = i32(ctx), starts(q)
     qs = torch.cat([qs, qs])
-    for kw in (dict(max_query_len=1), dict(max_query_len=4, num_decode_seqs=0)):
+    for kw in (dict(max_query_len=1, max_context_len=37),
+               dict(max_query_len=1, max_context_len=200000),
+               dict(max_query_len=4, num_decode_seqs=0, max_context_len=37)):
         out = torch.full(qs.shape, 7.0, dtype=torch.bfloat16, device="cuda")
         pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], bt.cuda(), cl.cuda(), qsl.cuda(), scale,
-                           *cache.gpu[2:], max_context_len=37, **kw)
+                           *cache.gpu[2:], **kw)
         assert (out[3:] == 7.0).all() and (out[:3] != 7.0).any(-1).all()
     assert pkv.get_error() == 0
 
 
-@pytest.mark.parametrize("chunk", [1, 20])
-def test_bad_sequences_are_zero_and_flagged_the_others_right(chunk):
+@pytest.mark.parametrize("chunk,bound", [(1, 200), (1, 200000), (20, 200)])
+def test_bad_sequences_are_zero_and_flagged_the_others_right(chunk, bound):
     ctx, q = [100, 50, 200, 64, 90], [chunk] * 5
-    b = batch(ctx, q, 8, 2, 64, seed=21)
+    b = batch(ctx, q, 8, 4, 64, seed=21)
     cache, qs, bt, cl, qsl, scale = b
     good, ref, tol = attend(*b)
     for bad_len, bits in ((0, pkv.ERR_CONTEXT_LEN), (16 * bt.shape[1] + 1, pkv.ERR_CONTEXT_LEN),
@@ -334,7 +371,7 @@ def test_bad_sequences_are_zero_and_flagged_the_others_right(chunk):
             # (max_query_len 2 sends single rows through the prefill path)
             mq = chunk if nd < 0 else 2
             pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], bt.cuda(), cl2.cuda(), qsl.cuda(),
-                               scale, *cache.gpu[2:], max_query_len=mq, max_context_len=200,
+                               scale, *cache.gpu[2:], max_query_len=mq, max_context_len=bound,
                                num_decode_seqs=nd)
             assert pkv.get_error() == bits
             got = out.float().cpu().numpy()
@@ -348,18 +385,18 @@ def test_bad_sequences_are_zero_and_flagged_the_others_right(chunk):
     bt2[3, 0] = -1
     out = torch.full(qs.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
     pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], bt2.cuda(), cl.cuda(), qsl.cuda(), scale,
-                       *cache.gpu[2:], max_query_len=chunk, max_context_len=200)
+                       *cache.gpu[2:], max_query_len=chunk, max_context_len=bound)
     assert pkv.get_error() == pkv.ERR_BLOCK_ID
     got = out.float().cpu().numpy()
     keep = np.r_[0:chunk, 2 * chunk:3 * chunk, 4 * chunk:5 * chunk]
     assert (np.abs(got - ref) / tol)[keep].max() <= 1
 
 
-@pytest.mark.parametrize("chunk", [1, 30])
-def test_scales_of_very_different_size(chunk):
+@pytest.mark.parametrize("chunk,bound", [(1, None), (1, 200000), (30, None)])
+def test_scales_of_very_different_size(chunk, bound):
     """Blocks whose V is 2^-30 of, or 2^20 times, the others', zero scales and
     large and tiny queries: every element to the tolerance of what it sums."""
-    b = batch([400, 90, 700], [chunk] * 3, 8, 2, 128, seed=31)
+    b = batch([400, 90, 700], [chunk] * 3, 8, 4, 128, seed=31)
     cache, qs, bt, cl, qsl, scale = b
     rng = np.random.default_rng(1)
     cache.vs *= (2.0 ** rng.integers(-30, 20, cache.vs.shape)).astype(np.float32)
@@ -368,26 +405,29 @@ def test_scales_of_very_different_size(chunk):
     cache.ks[bt[0, 4]] = 0.0
     cache.gpu[2].copy_(torch.from_numpy(cache.ks))
     cache.gpu[3].copy_(torch.from_numpy(cache.vs))
-    check_attention(*b)
+    check_attention(*b, max_context_len=bound)
     check_attention(cache, (qs.float() * 2.0 ** 16).to(torch.bfloat16), bt, cl, qsl,
-                    scale * 2.0 ** -16)
+                    scale * 2.0 ** -16, max_context_len=bound)
     check_attention(cache, (qs.float() * 2.0 ** -40).to(torch.bfloat16), bt, cl, qsl,
-                    scale * 2.0 ** 40)
+                    scale * 2.0 ** 40, max_context_len=bound)
+    # a negative and a zero softmax scale
+    check_attention(cache, qs, bt, cl, qsl, -scale, max_context_len=bound)
+    check_attention(cache, qs, bt, cl, qsl, 0.0, max_context_len=bound)
 
 
-@pytest.mark.parametrize("chunk", [1, 30])
-def test_a_sharp_softmax_on_a_block_of_tiny_values(chunk):
+@pytest.mark.parametrize("chunk,bound", [(1, None), (1, 400000), (30, None)])
+def test_a_sharp_softmax_on_a_block_of_tiny_values(chunk, bound):
     """All weight on keys of one block whose V is 2^-20 of the others': the
     tiny output keeps its relative precision."""
-    b = batch([200], [chunk], 4, 1, 64, seed=41)
+    b = batch([200], [chunk], 8, 4, 64, seed=41)
     cache, qs, bt, cl, qsl, scale = b
     k, _ = cache.values()
     blk = int(bt[0, 2])
-    key = k[blk, 5, 0]
-    qs = torch.from_numpy(np.tile(key * 30, (chunk, 4, 1))).to(torch.bfloat16)
+    key = np.repeat(k[blk, 5], 2, 0)      # (each head's own key)
+    qs = torch.from_numpy(np.tile(key * 30, (chunk, 1, 1))).to(torch.bfloat16)
     cache.vs[blk] *= np.float32(2.0 ** -20)
     cache.gpu[3].copy_(torch.from_numpy(cache.vs))
-    got, ref, _ = attend(cache, qs, bt, cl, qsl, scale)
+    got, ref, _ = attend(cache, qs, bt, cl, qsl, scale, max_context_len=bound)
     own = np.abs(O8.widen(cache.vc, cache.vs)[blk]).max()
     assert np.abs(ref).max() < 1.01 * own       # nothing but that block counts
     assert np.abs(got - ref).max() <= tolerance(np.abs(ref).max(), own)
@@ -395,11 +435,12 @@ def test_a_sharp_softmax_on_a_block_of_tiny_values(chunk):
 
 def test_prefix_shared_blocks():
     ctx = [70, 80, 100]
-    b = batch(ctx, [1, 1, 1], 8, 2, 128, seed=51)
+    b = batch(ctx, [1, 1, 1], 8, 4, 128, seed=51)
     cache, qs, bt, cl, qsl, scale = b
     bt[1, :3] = bt[0, :3]
     bt[2, :3] = bt[0, :3]
-    check_attention(cache, qs, bt, cl, qsl, scale)
+    for bound in (None, 200000):
+        check_attention(cache, qs, bt, cl, qsl, scale, max_context_len=bound)
 
 
 def test_offsets_past_32_bits():
@@ -415,25 +456,27 @@ def test_offsets_past_32_bits():
     for bt, cache in ((far, gpu), (near, [t[:4].clone() for t in gpu])):
         pkv.write_int8(k.cuda(), v.cuda(), bt.cuda(), i32([n]).cuda(), i32([0, n]).cuda(), *cache,
                        max_query_len=n)
-        for m in (1, qn):
+        for m, bound in ((1, n), (1, 400000), (qn, n)):
             q = rows(torch.Generator().manual_seed(m), m, 16, d).cuda()
             out = torch.empty_like(q)
             pkv.attention_int8(out, q, *cache[:2], bt.cuda(), i32([n]).cuda(), i32([0, m]).cuda(),
-                               d ** -0.5, *cache[2:], max_query_len=m, max_context_len=n)
+                               d ** -0.5, *cache[2:], max_query_len=m, max_context_len=bound)
             outs.append(out)
     assert pkv.get_error() == 0
-    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[3])
+    assert all(torch.equal(a, b) for a, b in zip(outs[:3], outs[3:]))
     assert all(torch.isfinite(o.float()).all() and o.float().abs().max() > 0 for o in outs)
 
 
 def test_same_call_twice_gives_the_same_bits():
-    b = batch([3000, 17, 900, 1200], [1, 1, 1, 1], 16, 2, 128, seed=61, step=500)
-    one = attend(*b)[0]
-    for _ in range(3):
-        assert np.array_equal(one, attend(*b)[0])
+    b = batch([3000, 17, 900, 1200], [1, 1, 1, 1], 16, 4, 128, seed=61, step=500)
+    for bound in (None, 100000):
+        one = attend(*b, max_context_len=bound)[0]
+        for _ in range(3):
+            assert np.array_equal(one, attend(*b, max_context_len=bound)[0])
 
 
-def test_other_stream_and_two_graphs():
+@pytest.mark.parametrize("bound", [900, 100000])
+def test_other_stream_and_two_graphs(bound):
     """A write and an attention captured on their own streams into two graphs
     with a workspace each, replayed together with new inputs."""
     parts = []
@@ -444,7 +487,7 @@ def test_other_stream_and_two_graphs():
         k, v = rows(gen, 63, 4, 128), rows(gen, 63, 4, 128)
         dev = [t.cuda() for t in (qs, k, v, bt, cl, qsl)]
         out = torch.empty_like(dev[0])
-        meta = pkv.attn_meta(dev[0], dev[3], dev[4], max_query_len=60, max_context_len=900,
+        meta = pkv.attn_meta(dev[0], dev[3], dev[4], max_query_len=60, max_context_len=bound,
                              num_decode_seqs=3)
         ws = torch.empty(max(pkv.workspace_size_int8(cache.gpu[0], meta), 1), dtype=torch.uint8,
                          device="cuda")
@@ -455,7 +498,7 @@ def test_other_stream_and_two_graphs():
             q, k, v, bt, cl, qsl = dev
             pkv.write_int8(k, v, bt, cl, qsl, *cache.gpu, max_query_len=60, stream=stream)
             pkv.attention_int8(out, q, *cache.gpu[:2], bt, cl, qsl, scale, *cache.gpu[2:],
-                               max_query_len=60, max_context_len=900, num_decode_seqs=3,
+                               max_query_len=60, max_context_len=bound, num_decode_seqs=3,
                                workspace=ws, stream=stream)
 
         step()
