@@ -998,15 +998,20 @@ struct Int8Plan {
   int num_ranges = 1;      // ranges that give every resident team one
   int max_ranges = 1;      // that there can be: the workspace has two slots for each
   size_t ws_o_bytes = 0, ws_lse_bytes = 0;
-  size_t ws_bytes = 0;     // of the kernel taken
+  size_t decode_bytes = 0;   // workspace of the decode kernel taken
+  // prefill: parts of the keys, and their workspace behind the decode's
+  int key_splits = 1;
+  size_t pf_o_bytes = 0;
+  size_t ws_bytes = 0;
 };
 
-int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms, Int8Plan* p) {
+int make_int8_decode_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms,
+                          Int8Plan* p) {
   *p = Int8Plan{};
   pkv_cache_desc as_bytes = *c;
   as_bytes.dtype = PKV_FP8_E4M3;
   if (int st = make_plan(&as_bytes, m, num_sms, &p->split)) return st;
-  p->ws_bytes = p->split.ws_bytes;
+  p->decode_bytes = p->split.ws_bytes;
   const int nd = p->split.num_decode;
   if (nd == 0) return PKV_OK;
   p->col_groups = (m->num_q_heads / c->num_kv_heads + 7) / 8;
@@ -1035,14 +1040,36 @@ int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms,
     return PKV_OK;
   p->teams = true;
   p->max_ranges = static_cast<int>(std::max<int64_t>(ranges, 1));
-  p->ws_bytes = 0;
+  p->decode_bytes = 0;
   if (p->max_ranges > 1) {
     const size_t rows = 2 * static_cast<size_t>(p->max_ranges) * m->num_q_heads;
     p->ws_o_bytes = round_up(rows * c->head_size * sizeof(float), 256);
     p->ws_lse_bytes = round_up(rows * sizeof(float), 256);
-    p->ws_bytes = p->ws_o_bytes + p->ws_lse_bytes +
-                  round_up(static_cast<size_t>(nd) * sizeof(int2), 256);
+    p->decode_bytes = p->ws_o_bytes + p->ws_lse_bytes +
+                      round_up(static_cast<size_t>(nd) * sizeof(int2), 256);
   }
+  return PKV_OK;
+}
+
+int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms, Int8Plan* p) {
+  if (int st = make_int8_decode_plan(c, m, num_sms, p)) return st;
+  const int npf = m->num_seqs - p->split.num_decode;
+  const int G = m->num_q_heads / c->num_kv_heads;
+  if (npf > 0 && G <= 128) {
+    // keys a CTA's rows see at most: the context, or the window before each of them
+    int64_t keys = m->max_context_len;
+    const int toks = prefill_tc_tokens_per_cta(G);
+    if (m->sliding_window > 0) keys = std::min<int64_t>(keys, int64_t{m->sliding_window} + toks);
+    const int64_t ctas = static_cast<int64_t>(npf) * ((m->max_query_len + toks - 1) / toks) *
+                         c->num_kv_heads;
+    p->key_splits = prefill_int8_key_splits(ctas, static_cast<int>((keys + 127) / 128), num_sms);
+    if (p->key_splits > 1) {
+      const size_t rows = static_cast<size_t>(m->num_tokens) * m->num_q_heads * p->key_splits;
+      p->pf_o_bytes = round_up(rows * c->head_size * sizeof(float), 256);
+      p->ws_bytes = p->pf_o_bytes + round_up(rows * sizeof(float), 256);
+    }
+  }
+  p->ws_bytes += p->decode_bytes;
   return PKV_OK;
 }
 
@@ -1151,7 +1178,7 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     d.block_tables = block_tables;
     d.context_lens = context_lens;
     d.query_start_loc = query_start_loc;
-    if (p.ws_bytes > 0) {
+    if (p.decode_bytes > 0) {
       char* ws = static_cast<char*>(workspace);
       d.ws_o = reinterpret_cast<float*>(ws);
       d.ws_lse = reinterpret_cast<float*>(ws + p.ws_o_bytes);
@@ -1189,8 +1216,8 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     d.block_tables = block_tables;
     d.context_lens = context_lens;
     d.query_start_loc = query_start_loc;
-    d.ws_o = p.ws_bytes ? static_cast<float*>(workspace) : nullptr;
-    d.ws_lse = p.ws_bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.split.ws_o_bytes)
+    d.ws_o = p.decode_bytes ? static_cast<float*>(workspace) : nullptr;
+    d.ws_lse = p.decode_bytes ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.split.ws_o_bytes)
                           : nullptr;
     d.err = err;
     d.bt_stride = meta->block_table_stride;
@@ -1258,6 +1285,12 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     f.v_scales = v_scales;
     f.scale_log2 = scale_log2;
     f.longest_first = nd == 0 ? 1 : 0;   // alone on the GPU, or beside decode
+    f.key_splits = p.key_splits;
+    if (p.key_splits > 1) {
+      char* ws = static_cast<char*>(workspace) + p.decode_bytes;
+      f.ws_o = reinterpret_cast<float*>(ws);
+      f.ws_lse = reinterpret_cast<float*>(ws + p.pf_o_bytes);
+    }
     const int toks = prefill_tc_tokens_per_cta(G);
     f.num_mtiles = (meta->max_query_len + toks - 1) / toks;
     CUtensorMap qmap, omap;

@@ -595,8 +595,13 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
       f[w] = (M == -INFINITY) ? 0.f : exp2f(ww[8 * D + c] - M);
       den += f[w] * ww[8 * D + 8 + c];
     }
-    for (int w = 0; w < NW; ++w) merge_f[w * 8 + c] = den > 0.f ? f[w] * out_scale / den : 0.f;
-    merge_f[NW * 8 + c] = den > 0.f ? M + log2f(den) : -INFINITY;
+    if constexpr (I8) {   // a NaN stays one (the combine makes it of an infinite lse)
+      for (int w = 0; w < NW; ++w) merge_f[w * 8 + c] = den == 0.f ? 0.f : f[w] / den;
+      merge_f[NW * 8 + c] = den == 0.f ? -INFINITY : (den > 0.f ? M + log2f(den) : INFINITY);
+    } else {
+      for (int w = 0; w < NW; ++w) merge_f[w * 8 + c] = den > 0.f ? f[w] * out_scale / den : 0.f;
+      merge_f[NW * 8 + c] = den > 0.f ? M + log2f(den) : -INFINITY;
+    }
   }
   __syncthreads();
 

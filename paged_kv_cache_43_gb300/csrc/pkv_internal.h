@@ -127,9 +127,12 @@ struct PrefillArgs {
   // tile so that the waits for it run out.
   uint64_t wait_limit_ns;
   int32_t debug_stall;
-  // Int8 cache: block scales [num_blocks, Hkv] (null otherwise)
+  // Int8 cache: block scales [num_blocks, Hkv] (null otherwise), and the parts
+  // each row's keys are cut into (> 1: partials to ws_o [token, q head,
+  // key_splits, D] and ws_lse, then a merge)
   const float* k_scales;
   const float* v_scales;
+  int32_t key_splits;
 };
 
 // Settings of the test hook, applied to the decode and tcgen05 prefill
@@ -306,6 +309,7 @@ cudaError_t launch_prefill_tc(const CUtensorMap& qmap, const CUtensorMap& kmap,
 
 // The same kernel over int8 caches with block scales (a.k_scales, a.v_scales);
 // any group of at most 128.
+int prefill_int8_key_splits(int64_t ctas, int tiles, int num_sms);
 cudaError_t launch_prefill_tc_int8(const CUtensorMap& qmap, const CUtensorMap& kmap,
                                    const CUtensorMap& vmap, const CUtensorMap& omap,
                                    const PrefillArgs& a, int head_size, cudaStream_t stream);

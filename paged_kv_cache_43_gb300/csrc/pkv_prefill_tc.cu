@@ -69,7 +69,12 @@
 //    shared memory of its own, read by broadcast loads, while it has S to wait
 //    for: a warp that fetched them for all (handing them over by mbarriers)
 //    put 0.2-0.5 us a tile into the chain.  Every code is finite, so rows no key may
-//    see need no zeroing.
+//    see need no zeroing.  A launch with few CTAs cuts each one's keys into
+//    parts (key_splits, grid.z), whose normalised partials a second kernel
+//    merges: a CTA's key tiles come one after the other, 2 to 3 us each (one
+//    512-token chunk over 8192 keys, 32 q / 8 kv heads: 178 -> 102 us).
+#include <algorithm>
+
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 #include "pkv_tc.cuh"
@@ -380,9 +385,12 @@ __device__ __forceinline__ TcWork pick_work(const PrefillArgs& a, int toks, int3
   return TcWork{a.seq_begin + u / a.num_mtiles, b % a.num_kv_heads, u % a.num_mtiles};
 }
 
-// LPT: the longest-first instantiation (a separate kernel, so that the plain
-// one keeps its work indices as launch coordinates and its register budget).
-template <int D, int FMT, bool LPT>
+// kLongestFirst: the longest-first instantiation (a separate kernel, so that
+// the plain one keeps its work indices as launch coordinates and its register
+// budget); kKeyParts: the one that cuts the keys into parts (int8; apart for
+// the same reason: within the plain one it cost 5 %).
+constexpr int kPlain = 0, kLongestFirst = 1, kKeyParts = 2;
+template <int D, int FMT, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1)
     pkv_prefill_tc_kernel(const __grid_constant__ CUtensorMap qmap,
                           const __grid_constant__ CUtensorMap kmap,
@@ -391,6 +399,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   using Lt = TcLayout<D>;
   constexpr bool FP8 = FMT != kBf16;   // one-byte codes, widened to fp16
   constexpr bool I8 = FMT == kInt8;
+  constexpr bool LPT = MODE == kLongestFirst;
+  constexpr bool PARTS = MODE == kKeyParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -416,7 +426,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     kvh = w.kvh;
     mtile = w.mtile;
   } else {
-    s = casc ? 0 : a.seq_begin + blockIdx.z;
+    if constexpr (PARTS) s = a.seq_begin + blockIdx.z / a.key_splits;
+    else s = casc ? 0 : a.seq_begin + blockIdx.z;
     kvh = blockIdx.y;
     mtile = a.num_mtiles - 1 - blockIdx.x;  // heaviest pair of each sequence first
   }
@@ -444,6 +455,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // zeroes the rows of the sequence)
   const bool before_prefix = a.key_begin > 0 && L - qn < a.key_begin;
   if (!casc && (bad_len || qn > L || qn > a.max_query_len || before_prefix)) {
+    if constexpr (PARTS)
+      if (blockIdx.z % a.key_splits != 0) return;   // (part 0 does this)
     if (threadIdx.x == 0 && mtile == 0 && kvh == 0)
       raise_error(a.err, (bad_len || before_prefix) ? PKV_ERR_CONTEXT_LEN : PKV_ERR_QUERY_LEN);
     if (a.key_begin > 0) return;   // (the merge writes the output rows)
@@ -467,17 +480,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // first key some row here sees: the lowest row's window start, or the end
   // of the shared prefix (cascade suffix launch)
   const int lo_min = max(a.window > 0 ? pos_min - a.window + 1 : 0, a.key_begin);
-  const int j0 = casc ? static_cast<int>(blockIdx.z) * a.prefix_tiles
-                      : (lo_min > 0 ? lo_min / kTcKeys : 0);
-  const int ntiles =
+  int j0 = casc ? static_cast<int>(blockIdx.z) * a.prefix_tiles
+                : (lo_min > 0 ? lo_min / kTcKeys : 0);
+  int ntiles =
       casc ? min(j0 + a.prefix_tiles, (L + kTcKeys - 1) / kTcKeys) : (pos_max + kTcKeys) / kTcKeys;
+  [[maybe_unused]] int key_part = 0;   // this CTA's part of the tiles
+  if constexpr (PARTS) {
+    key_part = blockIdx.z % a.key_splits;
+    const int per = (ntiles - j0 + a.key_splits - 1) / a.key_splits;
+    j0 += key_part * per;
+    ntiles = min(ntiles, j0 + per);
+    if (ntiles <= j0) {   // a part without key tiles: its partials count for nothing
+      for (int i = threadIdx.x; i < (tok_last + 1 - tok0) * G; i += blockDim.x)
+        a.ws_lse[(static_cast<int64_t>(q0 + tok0 + i / G) * Hq + kvh * G + i % G) * a.key_splits +
+                 key_part] = -INFINITY;
+    }
+  }
   const int n_rel = ntiles - j0;
   if (n_rel <= 0) return;
   // First cache block holding a key some row can see; blocks before it in
   // tile j0 are not loaded (their entries may be null) and their V rows are
   // zeroed instead.
-  const int b_lo = casc ? j0 * (kTcKeys / kBlock) : (lo_min > 0 ? lo_min / kBlock : 0);
-  const int nblk = (pos_max + kBlock) / kBlock;
+  int b_lo = casc ? j0 * (kTcKeys / kBlock) : (lo_min > 0 ? lo_min / kBlock : 0);
+  int nblk = (pos_max + kBlock) / kBlock;
+  if constexpr (PARTS) {
+    b_lo = max(b_lo, j0 * (kTcKeys / kBlock));
+    nblk = min(nblk, ntiles * (kTcKeys / kBlock));
+  }
   // V rows of the first tile before the first loaded block, and of the last
   // tile past pos_max, are zeroed once the tile has landed (zero_v_rows).
   const int v_lead = min(kTcKeys, b_lo * kBlock - j0 * kTcKeys);
@@ -1113,15 +1142,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       (void)mbar_wait(smem_u32(&sh->drain[t]), 0);
     }
     __syncwarp();
-    if (casc || a.key_begin > 0) {
+    if (PARTS || casc || a.key_begin > 0) {
       if (done && warp_wait(b_pvdone, (n_rel - 1) & 1, abort, a.err, wlim)) {
         // cascade prefix (split blockIdx.z) or suffix (split split_base): the
         // row's normalised partial and log2-sum-exp (in the scaled log2 domain
         // of m_used) for the merge
         tc::fence_after_sync();
         const float inv = l > 0.f ? out_scale / l : 0.f;
-        const int64_t wrow = (static_cast<int64_t>(q0 + tok) * Hq + kvh * G + g) * a.max_splits +
-                             (casc ? static_cast<int>(blockIdx.z) : a.split_base);
+        const int64_t wrow =
+            PARTS ? (static_cast<int64_t>(q0 + tok) * Hq + kvh * G + g) * a.key_splits + key_part
+                  : (static_cast<int64_t>(q0 + tok) * Hq + kvh * G + g) * a.max_splits +
+                        (casc ? static_cast<int>(blockIdx.z) : a.split_base);
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t o[32];
@@ -1136,7 +1167,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                    __uint_as_float(o[4 * v + 3]) * inv);
           }
         }
-        if (valid) a.ws_lse[wrow] = l > 0.f ? m_used + log2f(l) : -INFINITY;
+        if (valid)   // (key parts: NaN stays)
+          a.ws_lse[wrow] = (PARTS ? l != 0.f : l > 0.f) ? m_used + log2f(l) : -INFINITY;
       }
     } else if (t < ntq) {
       const bool ok = done && warp_wait(b_pvdone, (n_rel - 1) & 1, abort, a.err, wlim);
@@ -1223,19 +1255,73 @@ extern "C" int pkv_tc_timeline_clear() {
 namespace {
 #endif
 
+// Merges the key_splits partials of every prefill row, one warp per (row, q
+// head): out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).  Rows of decode
+// sequences, of no sequence and of sequences with bad lengths (zeroed by the
+// prefill kernel) are left alone.
+constexpr int kMaxKeySplits = 8;
+
+template <int D>
+__global__ void __launch_bounds__(128) pkv_prefill_merge_kernel(const PrefillArgs a) {
+  constexpr int PER = D / 32;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int tok = static_cast<int>(w / a.num_q_heads);
+  if (tok >= a.num_tokens) return;
+  const int s = seq_of_row(a.query_start_loc, a.seq_begin + a.num_seqs, tok);
+  if (s < a.seq_begin) return;
+  const int q0 = __ldg(a.query_start_loc + s), L = __ldg(a.context_lens + s);
+  const int qn = __ldg(a.query_start_loc + s + 1) - q0;
+  if (q0 < 0 || static_cast<int64_t>(q0) + qn > a.num_tokens || L < 1 ||
+      static_cast<int64_t>(L) > a.bt_stride * kBlock || qn > L || qn > a.max_query_len)
+    return;
+  const int64_t row = w * a.key_splits;
+  float lse[kMaxKeySplits], v[kMaxKeySplits][PER], M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kMaxKeySplits; ++i) {
+    lse[i] = i < a.key_splits ? a.ws_lse[row + i] : -INFINITY;
+    M = fmaxf(M, lse[i]);
+    if (lse[i] != -INFINITY) {
+      const float* src = a.ws_o + (row + i) * D + lane * PER;
+      if constexpr (PER == 4) *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(src);
+      else *reinterpret_cast<float2*>(v[i]) = *reinterpret_cast<const float2*>(src);
+    }
+  }
+  float acc[PER] = {}, den = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxKeySplits; ++i)
+    if (lse[i] != -INFINITY) {
+      const float f = exp2f(lse[i] - M);
+      den += f;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, v[i][e], acc[e]);
+    }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + w * D + lane * PER;
+#pragma unroll
+  for (int e = 0; e < PER; e += 2)
+    *reinterpret_cast<__nv_bfloat162*>(out + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+}
+
 template <int D, int FMT>
 cudaError_t launch_tc_t(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                         const CUtensorMap& omap, const PrefillArgs& a, cudaStream_t stream) {
   constexpr int smem = tc_smem_bytes<D>();
   const bool lpt = a.longest_first && !a.cascade_prefix &&
                    static_cast<int64_t>(a.num_seqs) * a.num_mtiles <= kLptUnits;
-  auto kfn = lpt ? pkv_prefill_tc_kernel<D, FMT, true> : pkv_prefill_tc_kernel<D, FMT, false>;
+  auto kfn = lpt ? pkv_prefill_tc_kernel<D, FMT, kLongestFirst>
+                 : pkv_prefill_tc_kernel<D, FMT, kPlain>;
+  // cascade prefix: grid.z = prefix key splits
+  int gz = a.cascade_prefix ? (a.prefix_len + a.prefix_tiles * kTcKeys - 1) /
+                                  (a.prefix_tiles * kTcKeys)
+                            : a.num_seqs;
+  if constexpr (FMT == kInt8)
+    if (a.key_splits > 1) {
+      kfn = pkv_prefill_tc_kernel<D, FMT, kKeyParts>;
+      gz *= a.key_splits;
+    }
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // cascade prefix: grid.z = prefix key splits
-  const int gz = a.cascade_prefix ? (a.prefix_len + a.prefix_tiles * kTcKeys - 1) /
-                                        (a.prefix_tiles * kTcKeys)
-                                  : a.num_seqs;
   dim3 grid(a.num_mtiles, a.num_kv_heads, gz);
   PrefillArgs b = a;
   debug_wait_settings(&b.wait_limit_ns, &b.debug_stall);
@@ -1268,8 +1354,26 @@ cudaError_t launch_prefill_tc_int8(const CUtensorMap& qmap, const CUtensorMap& k
                                    const CUtensorMap& vmap, const CUtensorMap& omap,
                                    const PrefillArgs& a, int head_size, cudaStream_t stream) {
   if (a.num_seqs == 0 || a.num_mtiles == 0) return cudaSuccess;
-  if (head_size == 128) return launch_tc_t<128, kInt8>(qmap, kmap, vmap, omap, a, stream);
-  return launch_tc_t<64, kInt8>(qmap, kmap, vmap, omap, a, stream);
+  const cudaError_t e = head_size == 128
+                            ? launch_tc_t<128, kInt8>(qmap, kmap, vmap, omap, a, stream)
+                            : launch_tc_t<64, kInt8>(qmap, kmap, vmap, omap, a, stream);
+  if (e != cudaSuccess || a.key_splits == 1) return e;
+  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
+  const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
+  if (head_size == 128) pkv_prefill_merge_kernel<128><<<blocks, 128, 0, stream>>>(a);
+  else pkv_prefill_merge_kernel<64><<<blocks, 128, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// Parts of the keys for a launch of `ctas` CTAs whose longest walks `tiles` key
+// tiles: as many as fill the SMs, of at least two tiles, and none below six
+// tiles, where the merge costs what the parts save (one 512-token prompt, 4
+// tiles: whole 21 us, two parts 24; 4 x 64 tokens over 1000 keys, 8 tiles: two
+// parts 27.5, four 23).
+int prefill_int8_key_splits(int64_t ctas, int tiles, int num_sms) {
+  if (ctas <= 0 || tiles < 6) return 1;
+  const int64_t n = std::min<int64_t>({num_sms / ctas, tiles / 2, kMaxKeySplits});
+  return static_cast<int>(std::max<int64_t>(n, 1));
 }
 
 }  // namespace pkv

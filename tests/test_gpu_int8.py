@@ -296,13 +296,54 @@ def test_decode_many_short_sequences_and_empty_ones(seqs):
     assert pkv.get_error() == 0
 
 
+@pytest.mark.parametrize("bound", BOUNDS)   # (a loose one cuts the keys into parts)
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 2), (32, 8), (3, 1), (10, 2), (16, 1), (128, 1),
                                     (130, 1)])
-def test_prefill_edge_chunks(hq, hkv, d):
+def test_prefill_edge_chunks(hq, hkv, d, bound):
     q = [1, 5, 16, 63, 64, 65, 97, 1, 40, 130]
     ctx = [1, 5, 40, 63, 130, 65, 97, 2, 200, 333]
-    check_attention(*batch(ctx, q, hq, hkv, d, seed=7 * hq + d))
+    check_attention(*batch(ctx, q, hq, hkv, d, seed=7 * hq + d), max_context_len=bound)
+    assert pkv.get_error() == 0
+
+
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("q,ctx,hq,hkv,d", [
+    ([40], [3000], 8, 2, 128), ([1, 1, 33, 200], [5, 2000, 1100, 2500], 12, 4, 64),
+    ([300], [300], 4, 1, 64), ([128, 2], [4000, 2], 16, 2, 128), ([2, 2, 2], [1, 2, 5], 4, 2, 64)])
+def test_prefill_with_few_rows_over_parts_of_the_keys(q, ctx, hq, hkv, d, window):
+    """Few row tiles: the keys are cut into parts and merged; parts that rows of
+    the tile see nothing of, and short sequences that have fewer tiles."""
+    ctx = [max(a, b) for a, b in zip(q, ctx)]
+    b = batch(ctx, q, hq, hkv, d, seed=sum(q) + d, step=600)
+    nd = next((i for i, n in enumerate(q) if n > 1), len(q))
+    for bound in (None, 9000):
+        check_attention(*b, window=window, num_decode_seqs=nd, max_context_len=bound)
+    assert pkv.get_error() == 0
+
+
+@pytest.mark.parametrize("bound", [None, 9000])
+@pytest.mark.parametrize("chunk", [1, 20])
+def test_nan_queries_and_scales_reach_their_rows_only(chunk, bound):
+    b = batch([1200, 90], [chunk] * 2, 8, 4, 64, seed=71)
+    cache, qs, bt, cl, qsl, scale = b
+    good = attend(*b, max_context_len=bound)[0]
+    bad = qs.clone()
+    bad[chunk - 1, 3, 5] = float("nan")          # the first sequence's last row, head 3
+    out = torch.zeros(qs.shape, dtype=torch.bfloat16, device="cuda")
+    args = (*cache.gpu[:2], bt.cuda(), cl.cuda(), qsl.cuda(), scale, *cache.gpu[2:])
+    kw = dict(max_query_len=chunk, max_context_len=bound or 1200)
+    pkv.attention_int8(out, bad.cuda(), *args, **kw)
+    got = out.float().cpu().numpy()
+    assert np.isnan(got[chunk - 1, 3]).all()
+    got[chunk - 1, 3] = good[chunk - 1, 3]
+    assert np.array_equal(got, good)
+    cache.gpu[3][int(bt[1, 0]), 2] = float("nan")   # V scale of the other's first block, head 2
+    pkv.attention_int8(out, qs.cuda(), *args, **kw)
+    got = out.float().cpu().numpy()
+    assert np.isnan(got[chunk:, 4:6]).all()
+    got[chunk:, 4:6] = good[chunk:, 4:6]
+    assert np.array_equal(got, good)
     assert pkv.get_error() == 0
 
 
