@@ -1005,6 +1005,18 @@ struct Int8Plan {
   size_t ws_bytes = 0;
 };
 
+// A batch's meta with its bounds no looser than they have to be (and far from
+// the ends of 32 bits): no context is longer than its table row holds, no
+// sequence has more rows than the batch, and a window of 2^30 keys hides none.
+pkv_attn_meta int8_meta(const pkv_attn_meta& m) {
+  pkv_attn_meta t = m;
+  t.max_context_len = static_cast<int32_t>(std::min<int64_t>(
+      {m.max_context_len, static_cast<int64_t>(m.block_table_stride) * kBlock, 1 << 30}));
+  if (t.sliding_window >= 1 << 30) t.sliding_window = 0;
+  t.max_query_len = std::min(m.max_query_len, m.num_tokens);
+  return t;
+}
+
 int make_int8_decode_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms,
                           Int8Plan* p) {
   *p = Int8Plan{};
@@ -1029,15 +1041,17 @@ int make_int8_decode_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int n
   if (m->sliding_window > 0)   // W keys span at most (W + 14) / 16 + 1 blocks
     longest = std::min(longest, (static_cast<int64_t>(m->sliding_window) + 14) / kBlock + 1);
   const int64_t blocks = longest * nd;
-  if (p->team_warps < 4 || blocks < static_cast<int64_t>(kTeamRangeBlocks) * p->num_ranges)
+  if (nd <= 65535 && (p->team_warps < 4 ||   // (the split kernel's grid.z: sequences)
+                      blocks < static_cast<int64_t>(kTeamRangeBlocks) * p->num_ranges))
     return PKV_OK;
+  const int64_t line = blocks + static_cast<int64_t>(kSeqCost) * nd;
   const int64_t ranges =
       m->kv_split_tokens > 0
-          ? (blocks + m->kv_split_tokens / kBlock - 1) / (m->kv_split_tokens / kBlock)
-          : std::min<int64_t>(p->num_ranges, (blocks + kMinRangeBlocks - 1) / kMinRangeBlocks);
+          ? (line + m->kv_split_tokens / kBlock - 1) / (m->kv_split_tokens / kBlock)
+          : std::min<int64_t>(p->num_ranges, (line + kMinRangeBlocks - 1) / kMinRangeBlocks);
   // (counts that the kernel holds in 32 bits)
-  if (ranges * p->teams_per_range > INT32_MAX / 2 || blocks / p->num_ranges > INT32_MAX / 2)
-    return PKV_OK;
+  if (ranges * p->teams_per_range > INT32_MAX / 2 || line / p->num_ranges > INT32_MAX / 2)
+    return nd <= 65535 ? PKV_OK : PKV_E_SHAPE;
   p->teams = true;
   p->max_ranges = static_cast<int>(std::max<int64_t>(ranges, 1));
   p->decode_bytes = 0;
@@ -1055,6 +1069,7 @@ int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms,
   if (int st = make_int8_decode_plan(c, m, num_sms, p)) return st;
   const int npf = m->num_seqs - p->split.num_decode;
   const int G = m->num_q_heads / c->num_kv_heads;
+  if (npf > 65535 && G <= 128) return PKV_E_SHAPE;   // (the prefill kernel's grid.z)
   if (npf > 0 && G <= 128) {
     // keys a CTA's rows see at most: the context, or the window before each of them
     int64_t keys = m->max_context_len;
@@ -1126,7 +1141,8 @@ extern "C" size_t pkv_attention_int8_workspace_size(const pkv_cache_desc* cache,
   int32_t* err;
   int sms;
   Int8Plan p;
-  if (device_state(&err, &sms) != PKV_OK || make_int8_plan(cache, meta, sms, &p) != PKV_OK)
+  const pkv_attn_meta tight = int8_meta(*meta);
+  if (device_state(&err, &sms) != PKV_OK || make_int8_plan(cache, &tight, sms, &p) != PKV_OK)
     return static_cast<size_t>(-1);
   return p.ws_bytes;
 }
@@ -1135,10 +1151,12 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
                                   const void* v_cache, const int32_t* block_tables,
                                   const int32_t* context_lens, const int32_t* query_start_loc,
                                   float scale, const float* k_scales, const float* v_scales,
-                                  const pkv_cache_desc* cache, const pkv_attn_meta* meta,
+                                  const pkv_cache_desc* cache, const pkv_attn_meta* given,
                                   void* workspace, size_t workspace_bytes, void* stream) {
   if (int st = check_cache_int8(cache)) return st;
-  if (int st = check_meta(cache, meta)) return st;
+  if (int st = check_meta(cache, given)) return st;
+  const pkv_attn_meta tight = int8_meta(*given);
+  const pkv_attn_meta* meta = &tight;
   if (meta->num_seqs == 0 || meta->num_tokens == 0) return PKV_OK;
   if (cache->num_blocks == 0) return PKV_E_SHAPE;
   if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start_loc ||
@@ -1334,10 +1352,11 @@ class PairSet {
   void clear() { std::fill(flag_, flag_ + kSlots, uint8_t{0}); }
 
  private:
-  static constexpr int kSlots = 4 * kCopyPairs;   // at most half full
+  static constexpr int kLog2Slots = 11, kSlots = 1 << kLog2Slots;
+  static_assert(kSlots >= 4 * kCopyPairs, "at most half full");
   static constexpr uint8_t kRead = 1, kWritten = 2;
   int find(int block) const {
-    unsigned i = (static_cast<uint32_t>(block) * 2654435769u) >> 22;
+    unsigned i = (static_cast<uint32_t>(block) * 2654435769u) >> (32 - kLog2Slots);
     while (flag_[i] != 0 && key_[i] != block) i = (i + 1) % kSlots;
     return static_cast<int>(i);
   }
@@ -1349,7 +1368,6 @@ class PairSet {
   }
   int32_t key_[kSlots];
   uint8_t flag_[kSlots] = {};
-  static_assert(kSlots == 1 << 10, "the hash keeps the top 10 bits");
 };
 
 }  // namespace

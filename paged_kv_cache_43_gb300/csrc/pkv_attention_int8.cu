@@ -5,8 +5,11 @@
 // K_p = code * k_scale[block of p][kv head] (likewise V), over the keys that
 // row t sees (causal inside a chunk, optional window).
 //
-// One CTA per (query row, q head), 4 warps taking every 4th key, a warp-wide
-// dot product per key, the running maximum and sum in fp32.
+// The path of chunk rows with more than 128 q heads on a kv head, which a query
+// tile of the tcgen05 kernel cannot hold: one CTA per (query row, q head), 4
+// warps taking every 4th key, a warp-wide dot product per key, the running
+// maximum and sum in fp32.  Bound by its instructions (5 TFLOP/s; K and V come
+// from L1 and L2 again for every row).
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 

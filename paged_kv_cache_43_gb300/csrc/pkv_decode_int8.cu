@@ -15,8 +15,9 @@
 // not rounded at all; Q is scaled by a power of two into fp16's range.
 //
 // Split.  The decode sequences' blocks, one sequence after the other, form
-// one line, which is cut into equal ranges, one for every team that the GPU
-// holds at a time; a team of up to 8 warps walks a range, whatever sequences
+// one line (with kSeqCost blocks of nothing before each sequence, for what its
+// start and its end cost a team), which is cut into equal ranges, one for every
+// team that the GPU holds at a time; a team of up to 8 warps walks a range, whatever sequences
 // lie in it, each warp with its own kv head (or group of 8
 // q heads of one), over blocks that one TMA copy of K and one of V brings in
 // for all their heads.  Where a range ends inside a sequence its warps write
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
       DecSeq q;
       int32_t bits;
       if (dec_seq(a, s, &q, &bits)) {
-        mine += q.blocks();
+        mine += kSeqCost + q.blocks();
       } else if (blockIdx.x == 0) {
         // nothing to attend: rows of a sequence with a bad length are zero
         if (a.span != nullptr) a.span[s] = make_int2(0, 0);
@@ -208,9 +209,9 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
   const bool withheld = a.debug_stall != 0 && team == 0;
 
   if (range < ranges) {
-    // ---- the sequence that holds the range's first block, which one of its
-    // blocks that is, and how many blocks the range still has
-    int s, b0, left;
+    // ---- the sequence in which the range begins, how far into it, and how
+    // much of the range is left
+    int s, into, left;
     {
       const int64_t begin = static_cast<int64_t>(range) * range_blocks;
       left = static_cast<int>(min(static_cast<int64_t>(range_blocks), upto[kThreads] - begin));
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
       while (true) {   // 32 sequences of the run at a time
         DecSeq q;
         int32_t bits;
-        const int n = s + lane < a.num_seqs && dec_seq(a, s + lane, &q, &bits) ? q.blocks() : 0;
+        const int n = s + lane < a.num_seqs && dec_seq(a, s + lane, &q, &bits) ? kSeqCost + q.blocks() : 0;
         int64_t sum = n;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -242,16 +243,20 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
         s += 32;
         if (s >= a.num_seqs) return;   // (cannot be: begin < total)
       }
-      b0 = static_cast<int>(begin - base);
+      into = static_cast<int>(begin - base);
     }
-    int n;
-    for (; left > 0 && s < a.num_seqs && alive; ++s, left -= n, b0 = 0, seg0 += n) {
+    int n, steps;   // blocks of a segment, and its length on the line
+    for (; left > 0 && s < a.num_seqs && alive; ++s, left -= steps, into = 0, seg0 += n) {
       DecSeq q;
       int32_t bits;
-      n = 0;
+      n = steps = 0;
       if (!dec_seq(a, s, &q, &bits)) continue;
       const int nblk = q.blocks();
-      n = min(left, nblk - b0);   // the segment: blocks [b0, b0 + n)
+      const int rest_of_seq = kSeqCost + nblk - into;
+      steps = min(left, rest_of_seq);
+      const int b0 = max(into - kSeqCost, 0);   // the segment: blocks [b0, b0 + n)
+      n = max(into + steps - kSeqCost, 0) - b0;
+      if (n == 0) continue;   // (the sequence's blocks begin in the next range)
       const int32_t* bt =
           a.block_tables + static_cast<int64_t>(s) * a.bt_stride + q.blk0() + b0;
 
@@ -466,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
       // (a row all of whose blocks were bad, or a wait that gave up, has l = 0)
       const bool whole = b0 == 0 && n == nblk;
       if (b0 == 0 && kvh == 0 && gsub == 0 && lane == 0 && a.span != nullptr)
-        a.span[s] = make_int2(range, 1 + (nblk - left + range_blocks - 1) / range_blocks);
+        a.span[s] = make_int2(range, 1 + (rest_of_seq - left + range_blocks - 1) / range_blocks);
       const int64_t slot = 2 * static_cast<int64_t>(range) + (b0 == 0 ? 1 : 0);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {

@@ -126,11 +126,8 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
   const int end = min(r.L, static_cast<int>(blk * kBlock) + kBlock);
   const int o0 = begin % kBlock, n = end - begin;
   const int bid = __ldg(a.block_tables + static_cast<int64_t>(s) * a.bt_stride + blk);
-  if (bid < 0 || bid >= a.num_blocks) {
-    if (rem == 0 && lane == 0) raise_error(a.err, PKV_ERR_BLOCK_ID);
-    return;
-  }
-  // this warp's rows, 8 elements a lane
+  // this warp's rows, 8 elements a lane; on their way before the block id is
+  // looked at
   const uint4* src = reinterpret_cast<const uint4*>(is_v ? a.v : a.k) +
                      (static_cast<int64_t>(r.q0 + (begin - p0)) * hkv + h) * kLanesPerRow;
   const int row0 = lane / kLanesPerRow, col = lane % kLanesPerRow;
@@ -140,6 +137,10 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
     const int row = i * kRowsPerLoad + row0;
     x[i] = make_uint4(0u, 0u, 0u, 0u);
     if (row < n) x[i] = __ldg(src + static_cast<int64_t>(row) * hkv * kLanesPerRow + col);
+  }
+  if (bid < 0 || bid >= a.num_blocks) {
+    if (rem == 0 && lane == 0) raise_error(a.err, PKV_ERR_BLOCK_ID);
+    return;
   }
   float* scale_at = (is_v ? a.v_scales : a.k_scales) + static_cast<int64_t>(bid) * hkv + h;
   float old = 0.f;

@@ -557,13 +557,18 @@ def copy_blocks(buffers, pairs, stream=None) -> None:
     [num_blocks, ...]: the K and V caches and scales of all layers) along
     ``pairs`` (host ints [n, 2]: from, to), in order."""
     lib = _lib or load()
-    pairs = np.ascontiguousarray(pairs, dtype=np.int32)
+    pairs = np.asarray(pairs)
     if pairs.size == 0 or len(buffers) == 0:
         return
-    if pairs.ndim != 2 or pairs.shape[1] != 2:
-        raise PkvError("pairs must be [n, 2] (from, to)")
+    if pairs.ndim != 2 or pairs.shape[1] != 2 or pairs.dtype.kind not in "iu":
+        raise PkvError("pairs must be integers [n, 2] (from, to)")
     dev = _current_device()
     nb = buffers[0].shape[0] if buffers[0].dim() else 0
+    if pairs.dtype != np.int32:
+        if pairs.min() < 0 or pairs.max() >= nb:   # (before 32 bits cut them short)
+            raise PkvError("pairs name a block that there is not")
+        pairs = pairs.astype(np.int32)
+    pairs = np.ascontiguousarray(pairs)
     for t in buffers:
         if t.get_device() != dev or not t.is_contiguous() or t.dim() == 0 or t.shape[0] != nb:
             _refuse(dev, buffers=(t, None))

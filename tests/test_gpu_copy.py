@@ -38,7 +38,7 @@ PAGES = [4, 12, 32, 64, 100, 512, 4096, 8192, 8208, 16384, 16400, 32768, 50000]
 
 
 @pytest.mark.parametrize("page", PAGES)
-@pytest.mark.parametrize("n", [1, 2, 15, 255, 256, 257])
+@pytest.mark.parametrize("n", [1, 2, 15, 511, 512, 513])
 def test_disjoint_pairs(page, n):
     ids = np.random.default_rng(n).permutation(2 * n + 3)
     run([(2 * n + 3, page)], np.stack([ids[:n], ids[n:2 * n]], 1))

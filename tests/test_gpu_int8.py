@@ -107,8 +107,9 @@ def attend(cache, q, bt, cl, qsl, scale, window=0, out=None, **kw):
     kw.setdefault("max_query_len", int((qsl[1:] - qsl[:-1]).max()))
     kw["max_context_len"] = kw.get("max_context_len") or int(cl.max())
     out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda") if out is None else out
-    pkv.attention_int8(out, q.cuda(), cache.gpu[0], cache.gpu[1], bt.cuda(), cl.cuda(), qsl.cuda(),
-                       scale, cache.gpu[2], cache.gpu[3], sliding_window=window, **kw)
+    pkv.attention_int8(out, q.cuda(), cache.gpu[0], cache.gpu[1],
+                       wide(bt, kw["max_context_len"]).cuda(), cl.cuda(), qsl.cuda(), scale,
+                       cache.gpu[2], cache.gpu[3], sliding_window=window, **kw)
     k, v = cache.values()
     ref, st = oracle.attention(q.float().numpy(), k, v, bt.numpy(), cl.numpy(), qsl.numpy(), scale,
                                window=window)
@@ -244,11 +245,18 @@ def test_write_many_sequences_of_a_few_rows(seqs):
 
 # -------------------------------------------------------------- attention
 
-# max_context_len decides between the two decode kernels: the longest context
-# (small batches: a CTA per split and head), or a bound of this many tokens
-# (teams of warps over equal ranges of all the batch's blocks).
+# The bound on the contexts (max_context_len and the table's width) decides
+# between the two decode kernels: the longest context (small batches: a CTA per
+# split and head), or a bound of this many tokens (teams of warps over equal
+# ranges of all the batch's blocks).
 LOOSE = 20000
 BOUNDS = [None, LOOSE]
+
+
+def wide(bt, bound):
+    """The table with room for `bound` tokens a sequence."""
+    more = -(-(bound or 0) // 16) - bt.shape[1]
+    return bt if more <= 0 else torch.nn.functional.pad(bt, (0, more), value=-1)
 
 EDGE_CTX = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 300, 511, 513, 700]
 
@@ -331,7 +339,7 @@ def test_nan_queries_and_scales_reach_their_rows_only(chunk, bound):
     bad = qs.clone()
     bad[chunk - 1, 3, 5] = float("nan")          # the first sequence's last row, head 3
     out = torch.zeros(qs.shape, dtype=torch.bfloat16, device="cuda")
-    args = (*cache.gpu[:2], bt.cuda(), cl.cuda(), qsl.cuda(), scale, *cache.gpu[2:])
+    args = (*cache.gpu[:2], wide(bt, bound).cuda(), cl.cuda(), qsl.cuda(), scale, *cache.gpu[2:])
     kw = dict(max_query_len=chunk, max_context_len=bound or 1200)
     pkv.attention_int8(out, bad.cuda(), *args, **kw)
     got = out.float().cpu().numpy()
@@ -367,8 +375,9 @@ def test_sliding_window_never_reads_blocks_before_it(window, bound):
         first = max(0, ctx[s] - q[s] - window + 1) // 16
         bt[s, :first] = -1
     out = torch.empty_like(qs.cuda())
-    pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], bt.cuda(), cl.cuda(), qsl.cuda(), scale,
-                       *cache.gpu[2:], max_query_len=64, max_context_len=bound or 1500,
+    pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], wide(bt, bound).cuda(), cl.cuda(),
+                       qsl.cuda(), scale, *cache.gpu[2:], max_query_len=64,
+                       max_context_len=bound or 1500,
                        num_decode_seqs=3,
                        sliding_window=window)
     assert pkv.get_error() == 0 and torch.isfinite(out.float()).all()
@@ -390,8 +399,8 @@ def test_rows_behind_the_last_sequence_and_empty_sequences_are_left_alone():
                dict(max_query_len=1, max_context_len=200000),
                dict(max_query_len=4, num_decode_seqs=0, max_context_len=37)):
         out = torch.full(qs.shape, 7.0, dtype=torch.bfloat16, device="cuda")
-        pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], bt.cuda(), cl.cuda(), qsl.cuda(), scale,
-                           *cache.gpu[2:], **kw)
+        pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], wide(bt, kw["max_context_len"]).cuda(),
+                           cl.cuda(), qsl.cuda(), scale, *cache.gpu[2:], **kw)
         assert (out[3:] == 7.0).all() and (out[:3] != 7.0).any(-1).all()
     assert pkv.get_error() == 0
 
@@ -402,6 +411,7 @@ def test_bad_sequences_are_zero_and_flagged_the_others_right(chunk, bound):
     b = batch(ctx, q, 8, 4, 64, seed=21)
     cache, qs, bt, cl, qsl, scale = b
     good, ref, tol = attend(*b)
+    bt = wide(bt, bound)
     for bad_len, bits in ((0, pkv.ERR_CONTEXT_LEN), (16 * bt.shape[1] + 1, pkv.ERR_CONTEXT_LEN),
                           (-5, pkv.ERR_CONTEXT_LEN)) + (((chunk - 1, pkv.ERR_QUERY_LEN),)
                                                         if chunk > 1 else ()):
@@ -500,12 +510,42 @@ def test_offsets_past_32_bits():
         for m, bound in ((1, n), (1, 400000), (qn, n)):
             q = rows(torch.Generator().manual_seed(m), m, 16, d).cuda()
             out = torch.empty_like(q)
-            pkv.attention_int8(out, q, *cache[:2], bt.cuda(), i32([n]).cuda(), i32([0, m]).cuda(),
-                               d ** -0.5, *cache[2:], max_query_len=m, max_context_len=bound)
+            pkv.attention_int8(out, q, *cache[:2], wide(bt, bound).cuda(), i32([n]).cuda(),
+                               i32([0, m]).cuda(), d ** -0.5, *cache[2:], max_query_len=m,
+                               max_context_len=bound)
             outs.append(out)
     assert pkv.get_error() == 0
     assert all(torch.equal(a, b) for a, b in zip(outs[:3], outs[3:]))
     assert all(torch.isfinite(o.float()).all() and o.float().abs().max() > 0 for o in outs)
+
+
+def test_workspace_refusals_and_extreme_bounds():
+    b = batch([900, 40], [1, 1], 8, 4, 64, seed=81)
+    cache, qs, bt, cl, qsl, scale = b
+    out = torch.zeros_like(qs, device="cuda")
+    args = (out, qs.cuda(), *cache.gpu[:2], bt.cuda(), cl.cuda(), qsl.cuda(), scale, *cache.gpu[2:])
+    kw = dict(max_query_len=1, max_context_len=900, kv_split_tokens=64)
+    meta = pkv.attn_meta(args[1], args[4], args[5], **kw)
+    need = pkv.workspace_size_int8(cache.gpu[0], meta)
+    assert need > 0
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(pkv.PkvError, match="-5"):
+        pkv.attention_int8(*args, workspace=ws[:need - 1], **kw)
+    with pytest.raises(pkv.PkvError, match="-6"):
+        pkv.attention_int8(*args, workspace=ws[16:], **kw)
+    torch.cuda.synchronize()
+    assert not out.any()
+    pkv.attention_int8(*args, workspace=ws, **kw)
+    assert out.any()
+    # bounds at the end of 32 bits are the table's
+    for window in (0, 2 ** 31 - 1):
+        ref = attend(*b, window=window)
+        out = torch.zeros_like(qs, device="cuda")
+        for mq, nd in ((1, -1), (2 ** 31 - 1, 0), (2 ** 31 - 1, 1)):
+            out.zero_()
+            pkv.attention_int8(out, *args[1:], max_query_len=mq, max_context_len=2 ** 31 - 1,
+                               num_decode_seqs=nd, sliding_window=window)
+            assert (np.abs(out.float().cpu().numpy() - ref[1]) <= ref[2]).all()
 
 
 def test_same_call_twice_gives_the_same_bits():
@@ -526,6 +566,7 @@ def test_other_stream_and_two_graphs(bound):
         cache, qs, bt, cl, qsl, scale = batch(ctx, [1, 1, 1, 60], 16, 4, 128, seed=seed)
         gen = torch.Generator().manual_seed(seed + 50)
         k, v = rows(gen, 63, 4, 128), rows(gen, 63, 4, 128)
+        bt = wide(bt, bound)
         dev = [t.cuda() for t in (qs, k, v, bt, cl, qsl)]
         out = torch.empty_like(dev[0])
         meta = pkv.attn_meta(dev[0], dev[3], dev[4], max_query_len=60, max_context_len=bound,

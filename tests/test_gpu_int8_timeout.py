@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from paged_kv_cache_43_gb300 import pkv
-from tests.test_gpu_int8 import _lib, attend, batch  # noqa: F401 (the fixture)
+from tests.test_gpu_int8 import _lib, attend, batch, wide  # noqa: F401 (the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -30,8 +30,8 @@ def test_waits_run_out_then_the_device_recovers(name):
     try:
         for _ in range(2):
             out = torch.zeros_like(qs, device="cuda")
-            pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], bt.cuda(), cl.cuda(), qsl.cuda(),
-                               scale, *cache.gpu[2:], max_query_len=max(q), **kw)
+            pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], wide(bt, bound).cuda(), cl.cuda(),
+                               qsl.cuda(), scale, *cache.gpu[2:], max_query_len=max(q), **kw)
             torch.cuda.synchronize()
             assert pkv.get_error(clear=True) & pkv.ERR_TIMEOUT
     finally:

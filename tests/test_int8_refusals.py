@@ -118,5 +118,6 @@ def test_binding_refuses_host_tensors():
                            max_context_len=1)
     with pytest.raises(pkv.PkvError, match="CUDA"):
         pkv.copy_blocks([c], [(0, 1)])
-    with pytest.raises(pkv.PkvError, match="pairs"):
-        pkv.copy_blocks([c], [0, 1, 2])
+    for bad in ([0, 1, 2], [(0.0, 1.0)], [(0, 2 ** 32)], [(-1, 0)]):
+        with pytest.raises(pkv.PkvError, match="pairs"):
+            pkv.copy_blocks([c], np.asarray(bad))
