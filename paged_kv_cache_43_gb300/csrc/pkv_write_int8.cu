@@ -14,9 +14,8 @@
 //
 // Work: one warp per (touched block, kv head, K or V), heads fastest, so that
 // consecutive warps read consecutive head rows of the same tokens.  A warp
-// holds its up to 16 rows in registers: one pass over the input.  Bound by
-// HBM for chunks of prompts and by the chain of dependent loads (lengths,
-// block id, old scale) for a decode step.
+// holds its up to 16 rows in registers: one pass over the input.  Bound by the
+// chain of dependent loads (lengths, block id, old scale).
 #include <cuda_bf16.h>
 #include <float.h>
 
@@ -73,9 +72,21 @@ __device__ __forceinline__ int find_seq(const WriteInt8Args& a, int64_t u, int l
   return lo;
 }
 
-__device__ __forceinline__ int8_t code_of(float x, float inv) {
-  // (cvt.rni sends NaN to 0 and saturates infinities)
-  return static_cast<int8_t>(max(-127, min(127, __float2int_rn(x * inv))));
+// Codes of two bf16 pairs (four elements, in order).  FINITE: |x| * inv is at
+// most 127 (plus a rounding), and adding 1.5 * 2^23 leaves the product, rounded
+// to the nearest even integer, in the sum's low byte (product and sum rounded
+// apart: no FMA).  Otherwise infinities
+// saturate and NaN becomes 0 (as cvt.rni has it).
+template <bool FINITE>
+__device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float inv) {
+  const float x[4] = {__fmul_rn(bf16_lo(w0), inv), __fmul_rn(bf16_hi(w0), inv),
+                      __fmul_rn(bf16_lo(w1), inv), __fmul_rn(bf16_hi(w1), inv)};
+  uint32_t c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = FINITE ? __float_as_uint(__fadd_rn(x[i], 12582912.f))
+                  : static_cast<uint32_t>(max(-127, min(127, __float2int_rn(x[i]))));
+  return prmt(prmt(c[0], c[1], 0x0040u), prmt(c[2], c[3], 0x0040u), 0x5410u);
 }
 
 __device__ __forceinline__ uint32_t requantise4(uint32_t w, float ratio) {
@@ -149,20 +160,31 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
     // (a block that was never begun: its codes count as zero)
     if (!(old >= kInt8ScaleFloor && old <= FLT_MAX)) old = kInt8ScaleFloor;
   }
-  float amax = 0.f;
-  bool odd = false;   // an infinity or NaN
+  // largest magnitude: bf16 patterns without their sign compare like the values
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const uint32_t q[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float lo = fabsf(bf16_lo(q[e])), hi = fabsf(bf16_hi(q[e]));
-      odd |= !(lo <= FLT_MAX) || !(hi <= FLT_MAX);
-      amax = fmaxf(amax, fmaxf(lo <= FLT_MAX ? lo : 0.f, hi <= FLT_MAX ? hi : 0.f));
-    }
+    for (int e = 0; e < 4; ++e) top = __vmaxu2(top, q[e] & 0x7fff7fffu);
   }
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-  if (__any_sync(0xffffffffu, odd) && lane == 0) raise_error(a.err, PKV_ERR_NONFINITE);
+  top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+  const bool finite = top < 0x7f80u;
+  if (!finite) {   // infinities or NaN: the largest of the others
+    if (lane == 0) raise_error(a.err, PKV_ERR_NONFINITE);
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t q[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = q[e] & 0x7fffu, hi = (q[e] >> 16) & 0x7fffu;
+        top = max(top, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+      }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+  }
+  const float amax = __uint_as_float(top << 16);
   const float want = fmaxf(__fdiv_rn(amax, 127.f), kInt8ScaleFloor);
   const float scale = fmaxf(old, want);
   int8_t* cache = static_cast<int8_t*>(is_v ? a.v_cache : a.k_cache) +
@@ -184,15 +206,10 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
   for (int i = 0; i < kLoads; ++i) {
     const int row = i * kRowsPerLoad + row0;
     if (row >= n) continue;
-    const uint32_t q[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint32_t out[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = static_cast<uint8_t>(code_of(bf16_lo(q[e]), inv));
-      const uint32_t hi = static_cast<uint8_t>(code_of(bf16_hi(q[e]), inv));
-      out[e / 2] |= (lo | (hi << 8)) << (16 * (e & 1));
-    }
-    *(reinterpret_cast<uint2*>(cache + (o0 + row) * row_stride) + col) = make_uint2(out[0], out[1]);
+    const uint2 out = finite
+                          ? make_uint2(codes4<true>(x[i].x, x[i].y, inv), codes4<true>(x[i].z, x[i].w, inv))
+                          : make_uint2(codes4<false>(x[i].x, x[i].y, inv), codes4<false>(x[i].z, x[i].w, inv));
+    *(reinterpret_cast<uint2*>(cache + (o0 + row) * row_stride) + col) = out;
   }
 }
 
