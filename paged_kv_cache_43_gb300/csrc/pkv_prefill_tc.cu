@@ -1337,7 +1337,7 @@ bool prefill_tc_supported(int head_size, int group) {
 }
 
 int prefill_tc_tokens_per_tile(int group) { return kTcRows / group; }
-int prefill_tc_tokens_per_cta(int group) { return kTcTiles * kTcRows / group; }
+int prefill_tc_tokens_per_cta(int group) { return kTcTiles * (kTcRows / group); }
 
 cudaError_t launch_prefill_tc(const CUtensorMap& qmap, const CUtensorMap& kmap,
                               const CUtensorMap& vmap, const CUtensorMap& omap,

@@ -315,6 +315,14 @@ def test_prefill_edge_chunks(hq, hkv, d, bound):
     assert pkv.get_error() == 0
 
 
+@pytest.mark.parametrize("group", [3, 5, 6, 7, 9, 10, 11, 13, 20, 33, 50, 65, 127])
+def test_prefill_row_tiles_of_every_group_size(group):
+    """Chunks that end just past the row tiles' and their pairs' ends."""
+    tile = 128 // group
+    q = sorted({n for m in (1, 2, 4, 6) for n in (m * tile, m * tile + 1, m * 128 // group)})
+    check_attention(*batch([n + 150 for n in q], q, group, 1, 64, seed=group))
+
+
 @pytest.mark.parametrize("window", [0, 700])
 @pytest.mark.parametrize("q,ctx,hq,hkv,d", [
     ([40], [3000], 8, 2, 128), ([1, 1, 33, 200], [5, 2000, 1100, 2500], 12, 4, 64),
