@@ -989,6 +989,14 @@ int check_cache_int8(const pkv_cache_desc* c) {
 // teams of one warp (10 / 5), 16 of 8K to 16K 58 - 62.
 constexpr int kTeamRangeBlocks = 32;
 
+// The split kernel reads contexts of up to kOneSplitBlocks blocks in one split,
+// however few its CTAs: no partials, no merge launch, no workspace to ask for.
+// Measured one split - the general rule's splits, us on the device (32 / 8 heads
+// of 128): 1 sequence of 100 keys 5.2 - 7.2, of 200 6.9 - 7.9, of 300 (32 / 32)
+// 7.5 - 7.9, 4 of 300 7.7 - 8.5; above, 1 of 500 9.8 - 8.3.  The host's side of a
+// call takes 8 us less in one split.
+constexpr int kOneSplitBlocks = 20;
+
 struct Int8Plan {
   Plan split;              // num_decode, and the split kernel's cut
   bool teams = false;
@@ -1023,6 +1031,12 @@ int make_int8_decode_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int n
   pkv_cache_desc as_bytes = *c;
   as_bytes.dtype = PKV_FP8_E4M3;
   if (int st = make_plan(&as_bytes, m, num_sms, &p->split)) return st;
+  if (m->kv_split_tokens == 0 && p->split.max_splits > 1 &&
+      p->split.split_blocks * p->split.max_splits <= kOneSplitBlocks) {
+    p->split.split_blocks *= p->split.max_splits;
+    p->split.max_splits = 1;
+    p->split.ws_o_bytes = p->split.ws_bytes = 0;
+  }
   p->decode_bytes = p->split.ws_bytes;
   const int nd = p->split.num_decode;
   if (nd == 0) return PKV_OK;
