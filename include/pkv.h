@@ -323,7 +323,8 @@ int pkv_use_cascade(const pkv_attn_meta *meta, int32_t common_prefix_blocks);
  * sign and a NaN as zero, and PKV_ERR_NONFINITE is set.  Two sequences that
  * write into the same block in one call: that block's contents are
  * unspecified.  Sequences with bad lengths (the conditions and bits of
- * pkv_attention) and blocks with a bad id are skipped. */
+ * pkv_attention) and blocks with a bad id are skipped (a query_start_loc that
+ * decreases anywhere may leave others unwritten, too). */
 int pkv_write_int8(const void *k, const void *v, const int32_t *block_tables,
                    const int32_t *context_lens, const int32_t *query_start_loc,
                    void *k_cache, void *v_cache, float *k_scales, float *v_scales,
@@ -331,7 +332,9 @@ int pkv_write_int8(const void *k, const void *v, const int32_t *block_tables,
 
 /* PagedAttention over an INT8 cache: as pkv_attention (lengths, masks, window,
  * errors, rows left alone) with q and out in bf16.  A scale below 2^-60 (zero
- * included) counts as 2^-60; scales of blocks that no query sees are not read.
+ * included) counts as 2^-60, an infinite or NaN one makes the rows that see its
+ * block NaN; scales of blocks that no query sees are not read.  A batch's
+ * sequences past num_decode_seqs are 65535 at most (PKV_E_SHAPE).
  * The workspace's size comes from pkv_attention_int8_workspace_size (not from
  * pkv_attention_workspace_size); it is scratch of one call, so calls that may
  * overlap, captured graphs included, need one each. */

@@ -1093,7 +1093,8 @@ int make_int8_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms,
                          c->num_kv_heads;
     p->key_splits = prefill_int8_key_splits(ctas, static_cast<int>((keys + 127) / 128), num_sms);
     if (p->key_splits > 1) {
-      const size_t rows = static_cast<size_t>(m->num_tokens) * m->num_q_heads * p->key_splits;
+      // (max_query_len rows a sequence: few CTAs, few rows)
+      const size_t rows = static_cast<size_t>(npf) * m->max_query_len * m->num_q_heads * p->key_splits;
       p->pf_o_bytes = round_up(rows * c->head_size * sizeof(float), 256);
       p->ws_bytes = p->pf_o_bytes + round_up(rows * sizeof(float), 256);
     }

@@ -32,10 +32,14 @@ __global__ void __launch_bounds__(kWarps * 32) pkv_attention_int8_kernel(const A
   const int q0 = __ldg(a.query_start_loc + s);
   const int qn = __ldg(a.query_start_loc + s + 1) - q0;
   const int L = __ldg(a.context_lens + s);
+  if (q0 < 0 || static_cast<int64_t>(q0) + qn > a.num_tokens) {   // rows that there are not
+    if (threadIdx.x == 0 && hq == 0 && (t == q0 || t == 0)) raise_error(a.err, PKV_ERR_QUERY_LEN);
+    return;
+  }
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
                        (static_cast<int64_t>(t) * a.num_q_heads + hq) * D;
   const bool bad_len = L < 1 || static_cast<int64_t>(L) > a.bt_stride * kBlock;
-  if (bad_len || qn > L || qn > a.max_query_len || q0 < 0) {
+  if (bad_len || qn > L || qn > a.max_query_len) {
     if (threadIdx.x == 0 && hq == 0 && t == q0)
       raise_error(a.err, bad_len ? PKV_ERR_CONTEXT_LEN : PKV_ERR_QUERY_LEN);
     for (int d = threadIdx.x; d < D; d += blockDim.x) out[d] = __float2bfloat16(0.f);

@@ -128,7 +128,7 @@ struct PrefillArgs {
   uint64_t wait_limit_ns;
   int32_t debug_stall;
   // Int8 cache: block scales [num_blocks, Hkv] (null otherwise), and the parts
-  // each row's keys are cut into (> 1: partials to ws_o [token, q head,
+  // each row's keys are cut into (> 1: partials to ws_o [sequence, row, q head,
   // key_splits, D] and ws_lse, then a merge)
   const float* k_scales;
   const float* v_scales;

@@ -73,6 +73,8 @@
 //    parts (key_splits, grid.z), whose normalised partials a second kernel
 //    merges: a CTA's key tiles come one after the other, 2 to 3 us each (one
 //    512-token chunk over 8192 keys, 32 q / 8 kv heads: 178 -> 102 us).
+#include <float.h>
+
 #include <algorithm>
 
 #include "pkv_common.cuh"
@@ -385,6 +387,12 @@ __device__ __forceinline__ TcWork pick_work(const PrefillArgs& a, int toks, int3
   return TcWork{a.seq_begin + u / a.num_mtiles, b % a.num_kv_heads, u % a.num_mtiles};
 }
 
+// Key parts: the row of q head hq of sequence s's token `tok` among the
+// partials, max_query_len rows a sequence.
+__device__ __forceinline__ int64_t part_row(const PrefillArgs& a, int s, int tok, int hq) {
+  return (static_cast<int64_t>(s - a.seq_begin) * a.max_query_len + tok) * a.num_q_heads + hq;
+}
+
 // kLongestFirst: the longest-first instantiation (a separate kernel, so that
 // the plain one keeps its work indices as launch coordinates and its register
 // budget); kKeyParts: the one that cuts the keys into parts (int8; apart for
@@ -492,8 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     ntiles = min(ntiles, j0 + per);
     if (ntiles <= j0) {   // a part without key tiles: its partials count for nothing
       for (int i = threadIdx.x; i < (tok_last + 1 - tok0) * G; i += blockDim.x)
-        a.ws_lse[(static_cast<int64_t>(q0 + tok0 + i / G) * Hq + kvh * G + i % G) * a.key_splits +
-                 key_part] = -INFINITY;
+        a.ws_lse[part_row(a, s, tok0 + i / G, kvh * G + i % G) * a.key_splits + key_part] = -INFINITY;
     }
   }
   const int n_rel = ntiles - j0;
@@ -834,9 +841,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             sl2 = -sl2;
             down = -down;
           }
-          // scores this small are zero; a factor sl2 * K scale (>= 2^-60) that
-          // is itself above zero keeps a masked -inf what it is
-          sl2 = fmaxf(sl2, 0x1p-66f);
         }
 #pragma unroll
         for (int h = 0; h < Lt::kHalves; ++h)
@@ -989,7 +993,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int b = 0; b < kTcKeys / kBlock; ++b) {
             const float4 c = sc[b];
-            const float f = c.x * sl2, add = c.y + neg_mu;
+            // (above zero, so that a masked -inf stays what it is)
+            const float f = fmaf(c.x, sl2, FLT_MIN), add = c.y + neg_mu;
             const uint64_t f2 = tc::pack_f32x2(f, f), a2 = tc::pack_f32x2(add, add);
             uint64_t acc = 0;
 #pragma unroll
@@ -1150,7 +1155,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc::fence_after_sync();
         const float inv = l > 0.f ? out_scale / l : 0.f;
         const int64_t wrow =
-            PARTS ? (static_cast<int64_t>(q0 + tok) * Hq + kvh * G + g) * a.key_splits + key_part
+            PARTS ? part_row(a, s, tok, kvh * G + g) * a.key_splits + key_part
                   : (static_cast<int64_t>(q0 + tok) * Hq + kvh * G + g) * a.max_splits +
                         (casc ? static_cast<int>(blockIdx.z) : a.split_base);
 #pragma unroll 1
@@ -1256,9 +1261,8 @@ namespace {
 #endif
 
 // Merges the key_splits partials of every prefill row, one warp per (row, q
-// head): out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).  Rows of decode
-// sequences, of no sequence and of sequences with bad lengths (zeroed by the
-// prefill kernel) are left alone.
+// head): out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).  Rows of
+// sequences with bad lengths (zeroed by the prefill kernel) are left alone.
 constexpr int kMaxKeySplits = 8;
 
 template <int D>
@@ -1266,13 +1270,13 @@ __global__ void __launch_bounds__(128) pkv_prefill_merge_kernel(const PrefillArg
   constexpr int PER = D / 32;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int tok = static_cast<int>(w / a.num_q_heads);
-  if (tok >= a.num_tokens) return;
-  const int s = seq_of_row(a.query_start_loc, a.seq_begin + a.num_seqs, tok);
-  if (s < a.seq_begin) return;
+  const int64_t r = w / a.num_q_heads;   // (sequence, row of max_query_len)
+  const int s = a.seq_begin + static_cast<int>(r / a.max_query_len);
+  const int j = static_cast<int>(r % a.max_query_len);
+  if (s >= a.seq_begin + a.num_seqs) return;
   const int q0 = __ldg(a.query_start_loc + s), L = __ldg(a.context_lens + s);
   const int qn = __ldg(a.query_start_loc + s + 1) - q0;
-  if (q0 < 0 || static_cast<int64_t>(q0) + qn > a.num_tokens || L < 1 ||
+  if (j >= qn || q0 < 0 || static_cast<int64_t>(q0) + qn > a.num_tokens || L < 1 ||
       static_cast<int64_t>(L) > a.bt_stride * kBlock || qn > L || qn > a.max_query_len)
     return;
   const int64_t row = w * a.key_splits;
@@ -1297,7 +1301,9 @@ __global__ void __launch_bounds__(128) pkv_prefill_merge_kernel(const PrefillArg
       for (int e = 0; e < PER; ++e) acc[e] = fmaf(f, v[i][e], acc[e]);
     }
   const float inv = den == 0.f ? 0.f : 1.f / den;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + w * D + lane * PER;
+  const int hq = static_cast<int>(w - r * a.num_q_heads);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                       (static_cast<int64_t>(q0 + j) * a.num_q_heads + hq) * D + lane * PER;
 #pragma unroll
   for (int e = 0; e < PER; e += 2)
     *reinterpret_cast<__nv_bfloat162*>(out + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
@@ -1358,7 +1364,7 @@ cudaError_t launch_prefill_tc_int8(const CUtensorMap& qmap, const CUtensorMap& k
                             ? launch_tc_t<128, kInt8>(qmap, kmap, vmap, omap, a, stream)
                             : launch_tc_t<64, kInt8>(qmap, kmap, vmap, omap, a, stream);
   if (e != cudaSuccess || a.key_splits == 1) return e;
-  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
+  const int64_t warps = static_cast<int64_t>(a.num_seqs) * a.max_query_len * a.num_q_heads;
   const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
   if (head_size == 128) pkv_prefill_merge_kernel<128><<<blocks, 128, 0, stream>>>(a);
   else pkv_prefill_merge_kernel<64><<<blocks, 128, 0, stream>>>(a);

@@ -114,6 +114,12 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
   const int rem = static_cast<int>(w - u * 2 * hkv);
   const bool is_v = rem >= hkv;
   const int h = is_v ? rem - hkv : rem;
+  if (rem == 0 && u < a.num_seqs && lane == 0) {   // sequence u's lengths, once
+    SeqRows r;
+    int32_t bad;
+    (void)load_seq(a, static_cast<int>(u), &r, &bad);
+    if (bad) raise_error(a.err, bad);
+  }
   int s, j;   // sequence, touched block of it
   if (a.max_query_len == 1) {
     s = static_cast<int>(u);
@@ -126,10 +132,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
   }
   SeqRows r;
   int32_t bad;
-  if (!load_seq(a, s, &r, &bad)) {
-    if (bad && j == 0 && rem == 0 && lane == 0) raise_error(a.err, bad);
-    return;
-  }
+  if (!load_seq(a, s, &r, &bad)) return;
   const int p0 = r.L - r.qn;                       // position of the first new row
   const int64_t blk = static_cast<int64_t>(p0 / kBlock) + j;
   if (blk * kBlock >= r.L) return;

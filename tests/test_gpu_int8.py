@@ -474,6 +474,52 @@ def test_scales_of_very_different_size(chunk, bound):
     check_attention(cache, qs, bt, cl, qsl, 0.0, max_context_len=bound)
 
 
+@pytest.mark.parametrize("chunk,bound", [(1, None), (1, 200000), (30, None), (30, 9000)])
+@pytest.mark.parametrize("power", [100, -50])
+def test_queries_and_keys_of_opposite_extreme_size(chunk, bound, power):
+    """Keys of about 2^power, queries of 2^-power: ordinary scores."""
+    ctx, q = [400, 90, 700], [chunk] * 3
+    nb = 90
+    cache, bt = Cache(nb, 4, 128, seed=1), tables(ctx, nb, 3)
+    gen = torch.Generator().manual_seed(5)
+    cache.write(rows(gen, sum(ctx), 4, 128, size=2.0 ** power), rows(gen, sum(ctx), 4, 128), bt,
+                i32(ctx), starts(ctx), max(ctx))
+    qs = rows(gen, sum(q), 8, 128, size=2.0 ** -power)
+    check_attention(cache, qs, bt, i32(ctx), starts(q), 128 ** -0.5, max_context_len=bound)
+    assert pkv.get_error() == 0
+
+
+@pytest.mark.parametrize("hq,bound", [(8, 400), (8, 9000), (130, 400)])
+def test_chunks_past_the_last_row_are_skipped_and_flagged(hq, bound):
+    """A sequence whose rows end behind the batch's is left out whole."""
+    cache, qs, bt, cl, qsl, scale = batch([300, 200], [40, 60], hq, 1, 64, seed=hq)
+    got, ref, tol = attend(cache, qs, bt, cl, qsl, scale)
+    out = torch.full((90, hq, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    pkv.attention_int8(out, qs[:90].cuda(), *cache.gpu[:2], wide(bt, bound).cuda(), cl.cuda(),
+                       qsl.cuda(), scale, *cache.gpu[2:], max_query_len=60, max_context_len=bound)
+    assert pkv.get_error() == pkv.ERR_QUERY_LEN
+    got = out.float().cpu().numpy()
+    assert (np.abs(got - ref[:90]) / tol[:90])[:40].max() <= 1 and (got[40:] == 7.0).all()
+
+
+def test_write_flags_row_starts_that_decrease():
+    """Whatever is written then lies in the sequences' own blocks."""
+    ctx = [100, 120, 300]
+    bt = tables(ctx, 40, 2)
+    cache = Cache(40, 2, 64, seed=1)
+    gen = torch.Generator().manual_seed(3)
+    k, v = rows(gen, 200, 2, 64), rows(gen, 200, 2, 64)
+    before = [t.clone() for t in cache.gpu]
+    for qsl in ([0, 100, 50, 200], [0, 200, 190, 191], [0, 10, -20, 5], [50, 20, 10, 0]):
+        pkv.write_int8(k.cuda(), v.cuda(), bt.cuda(), i32(ctx).cuda(), i32(qsl).cuda(), *cache.gpu,
+                       max_query_len=200)
+        assert pkv.get_error() & pkv.ERR_QUERY_LEN
+    used = set(bt[bt >= 0].tolist())
+    rest = [b for b in range(40) if b not in used]
+    for a, b in zip(cache.gpu, before):
+        assert torch.equal(a[rest].view(torch.uint8), b[rest].view(torch.uint8))
+
+
 @pytest.mark.parametrize("chunk,bound", [(1, None), (1, 400000), (30, None)])
 def test_a_sharp_softmax_on_a_block_of_tiny_values(chunk, bound):
     """All weight on keys of one block whose V is 2^-20 of the others': the
