@@ -21,8 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libpkv.so")
 SOURCES = ["pkv_api.cu", "pkv_write.cu", "pkv_write_int8.cu", "pkv_decode.cu", "pkv_prefill.cu",
-           "pkv_prefill_tc.cu", "pkv_f32.cu", "pkv_decode_int8.cu", "pkv_attention_int8.cu",
-           "pkv_copy.cu", "pkv_static_scratch.cu", "pkv_pool.cpp"]
+           "pkv_prefill_tc.cu", "pkv_prefill_int8.cu", "pkv_f32.cu", "pkv_decode_int8.cu",
+           "pkv_attention_int8.cu", "pkv_copy.cu", "pkv_static_scratch.cu", "pkv_pool.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1334,7 +1334,7 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     if (int e =
             encode_query_map(&omap, out, meta->num_tokens, meta->num_q_heads, cache->head_size, G))
       return e;
-    PKV_TRY(launch_prefill_tc_int8(qmap, kmap, vmap, omap, f, cache->head_size, st));
+    PKV_TRY(launch_prefill_int8(qmap, kmap, vmap, omap, f, cache->head_size, st));
     return PKV_OK;
   };
   if (nd == 0) return prefill_part(st);

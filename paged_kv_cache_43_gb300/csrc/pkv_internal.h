@@ -311,10 +311,10 @@ cudaError_t launch_prefill_tc(const CUtensorMap& qmap, const CUtensorMap& kmap,
                               const PrefillArgs& a, int head_size, bool fp8,
                               cudaStream_t stream);
 
-// The same kernel over int8 caches with block scales (a.k_scales, a.v_scales);
-// any group of at most 128.
+// Int8 caches with block scales (a.k_scales, a.v_scales; pkv_prefill_int8.cu); any
+// group of at most 128.
 int prefill_int8_key_splits(int64_t ctas, int tiles, int num_sms);
-cudaError_t launch_prefill_tc_int8(const CUtensorMap& qmap, const CUtensorMap& kmap,
+cudaError_t launch_prefill_int8(const CUtensorMap& qmap, const CUtensorMap& kmap,
                                    const CUtensorMap& vmap, const CUtensorMap& omap,
                                    const PrefillArgs& a, int head_size, cudaStream_t stream);
 
