@@ -24,7 +24,7 @@
 //   8, 9      start the TMA copies of K, of V (one box per cache block)
 //   10, 13    widen K codes in place (D = 128: half the rows each; 64: warp 10)
 //   11, 14    widen V codes
-//   12        issues every product: tile 0, tile 1, tile 0, ...
+//   12, 15    issue the products of tile 0, 1
 // Starting a tile's copies and widening it take a warp 1 us each: fewer warps for
 // them (one to start all, two to widen all) bound the step.
 // Weights are first formed against the running reference m, with no pass for
@@ -55,7 +55,8 @@ __device__ __forceinline__ uint32_t col_s(int t, int h) { return 128u * t + 64u 
 __device__ __forceinline__ uint32_t col_o(int t) { return 256u + 128u * t; }
 
 struct Shared {
-  uint64_t q_full, q_conv, drain;
+  uint64_t q_full, q_conv;
+  uint64_t drain[kTcTiles];
   uint64_t s_full[kTcTiles][2], p_full[kTcTiles][2];   // of half step h: [h % 2]
   uint64_t pv_done[kTcTiles];    // P V of each half step
   uint64_t o_done[kTcTiles];     // the last one (a phase of its own: a waiter for one of
@@ -194,7 +195,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensor_map(&omap);
     mbar_init(q_full, 1);
     mbar_init(q_conv, 8);   // one arrival per softmax warp
-    mbar_init(smem_u32(&sh->drain), 1);
     for (int t = 0; t < kTcTiles; ++t) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(smem_u32(&sh->s_full[t][b]), 1);
@@ -202,10 +202,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_init(smem_u32(&sh->pv_done[t]), 1);
       mbar_init(smem_u32(&sh->o_done[t]), 1);
+      mbar_init(smem_u32(&sh->drain[t]), 1);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(smem_u32(&sh->kv_full[i]), D == 128 ? 2 : 1);   // its widening warps
-      mbar_init(smem_u32(&sh->kv_empty[i]), 1);
+      mbar_init(smem_u32(&sh->kv_empty[i]), ntq);               // the tiles' issuers
     }
     for (int i = 0; i < 2 * kRing; ++i) mbar_init(smem_u32(&sh->kv_land[i]), 1);
     sh->abort = 0;
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh->kv_full[ring_slot(e)]));
       }
-    } else if (warp == 12) {
+    } else if (warp == 12 || (warp == 15 && ntq > 1)) {
       // ------------------------------------------------------------ products
       constexpr uint32_t idS = tc::idesc_f16_f32(kTcRows, kHalfKeys, 0, 0);
       constexpr uint32_t idO = tc::idesc_f16_f32(kTcRows, D, 0, 1);
@@ -321,7 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dk0 = tc::smem_desc_sw128(smem_u32(sKV), 16, 1024);
       const uint64_t dv0 = tc::smem_desc_sw128(smem_u32(sKV), Lt::kKvHalf, 1024);
       constexpr int kHalfStep = kHalfKeys * 128 >> 4;   // 64 keys on, in descriptor units
-      auto issue_s = [&](int t, int h) {
+      const int t = warp == 12 ? 0 : 1;
+      auto issue_s = [&](int h) {
         const uint64_t da = dq0 + static_cast<uint64_t>((t * Lt::kQTile) >> 4);
         const uint64_t db = dk0 + static_cast<uint64_t>(
                                       ((ring_slot(h & ~1) * Lt::kTileBytes) >> 4) + (h & 1) * kHalfStep);
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::commit(smem_u32(&sh->s_full[t][h & 1]));
       };
-      auto issue_pv = [&](int t, int h) {
+      auto issue_pv = [&](int h) {
         const uint64_t db =
             dv0 + static_cast<uint64_t>(((ring_slot((h & ~1) + 1) * Lt::kTileBytes) >> 4) +
                                         (h & 1) * kHalfStep);
@@ -354,39 +356,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (go) {
         tc::fence_after_sync();
         if (tc::elect_one()) {
-          for (int h = 0; h < min(H, 2); ++h)
-            for (int t = 0; t < ntq; ++t) issue_s(t, h);
+          issue_s(0);
+          if (H > 1) issue_s(1);
           empty(0);
         }
         __syncwarp();
       }
-      // Half step h of tile t: P V, then S of half step h + 2, whose columns P
-      // was read from (a thread's products execute in the order of their issue).
+      // Half step h: P V, then S of half step h + 2, over the columns that P was
+      // read from (a thread's products execute in the order of their issue).
       for (int h = 0; go && h < H; ++h) {
         const bool more = h + 2 < H;
-        for (int t = 0; go && t < ntq; ++t) {
-          go = quick_wait(smem_u32(&sh->p_full[t][h & 1]), (h >> 1) & 1, abort, a.err, wlim) &&
-               (t > 0 || (h & 1) || full(h + 1));   // (V of this tile: element h + 1)
+        go = quick_wait(smem_u32(&sh->p_full[t][h & 1]), (h >> 1) & 1, abort, a.err, wlim) &&
+             ((h & 1) || full(h + 1));   // (V of this tile: element h + 1)
+        if (!go) break;
+        tc::fence_after_sync();
+        if (tc::elect_one()) issue_pv(h);
+        __syncwarp();
+        if (more) {
+          go = (h & 1) || full(h + 2);   // (K of the next tile)
           if (!go) break;
           tc::fence_after_sync();
-          if (tc::elect_one()) issue_pv(t, h);
-          __syncwarp();
-          if (!more) continue;
-          go = t > 0 || (h & 1) || full(h + 2);     // (K of the next tile)
-          if (!go) break;
-          tc::fence_after_sync();
-          if (tc::elect_one()) issue_s(t, h + 2);
+          if (tc::elect_one()) issue_s(h + 2);
           __syncwarp();
         }
-        if (go && (h & 1) && tc::elect_one()) {   // both halves read: V, then the next K
+        if ((h & 1) && tc::elect_one()) {   // both halves read: V, then the next K
           empty(h);
           if (more) empty(h + 1);
         }
         __syncwarp();
       }
       if (tc::elect_one()) {   // every product completes before TMEM is freed
-        tc::commit(smem_u32(&sh->drain));
-        (void)mbar_wait(smem_u32(&sh->drain), 0);
+        tc::commit(smem_u32(&sh->drain[t]));
+        (void)mbar_wait(smem_u32(&sh->drain[t]), 0);
       }
       __syncwarp();
     }
