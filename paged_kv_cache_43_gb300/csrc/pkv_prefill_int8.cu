@@ -121,6 +121,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    prefetch_tensor_map(&qmap);
+    prefetch_tensor_map(&kmap);
+    prefetch_tensor_map(&vmap);
+    prefetch_tensor_map(&omap);
+  }
   const int G = a.group;
   const int Hq = a.num_q_heads;
   const int tile_toks = kTcRows / G;                // tokens per query tile (its last rows
@@ -187,12 +193,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int b_lo = max(lo_min / kBlock, j0 * (kTcKeys / kBlock));
   const int nblk = min((pos_max + kBlock) / kBlock, ntiles * (kTcKeys / kBlock));
 
+  const int32_t* bt = a.block_tables + static_cast<int64_t>(s) * a.bt_stride;
+  // Block ids of four consecutive tiles per warp-wide load: lane l holds block
+  // l % 8 of ring position 4g + l / 8.  Group g + 1 is loaded while group g is
+  // started, the first one before the barriers are up, so no tile waits on its ids.
+  auto load_ids4 = [&](int g) {
+    const int b = (j0 + 4 * g) * (kTcKeys / kBlock) + lane;
+    return b >= b_lo && b < nblk ? __ldg(bt + b) : -1;
+  };
+  const int first_ids = warp == 8 || warp == 9 ? load_ids4(0) : -1;
+
   const uint32_t q_full = smem_u32(&sh->q_full), q_conv = smem_u32(&sh->q_conv);
   if (threadIdx.x == 0) {
-    prefetch_tensor_map(&qmap);
-    prefetch_tensor_map(&kmap);
-    prefetch_tensor_map(&vmap);
-    prefetch_tensor_map(&omap);
     mbar_init(q_full, 1);
     mbar_init(q_conv, 8);   // one arrival per softmax warp
     for (int t = 0; t < kTcTiles; ++t) {
@@ -228,16 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------- producers
       const bool is_v = warp == 9;
       const uint64_t keep = policy_evict_normal();   // K/V tiles are re-read by the
-      const int32_t* bt = a.block_tables + static_cast<int64_t>(s) * a.bt_stride;  // other row tiles
+                                                     // other row tiles
       constexpr int kBlocks = kTcKeys / kBlock;      // cache blocks per tile
-      // Block ids of four consecutive tiles per warp-wide load: lane l holds
-      // block l % 8 of ring position 4g + l / 8.  Group g + 1 is loaded while
-      // group g is issued, so no tile waits on its ids.
-      auto load_ids4 = [&](int g) {
-        const int b = (j0 + 4 * g) * kBlocks + lane;
-        return b >= b_lo && b < nblk ? __ldg(bt + b) : -1;
-      };
-      int g_cur = load_ids4(0), g_nxt = load_ids4(1);
+      int g_cur = first_ids, g_nxt = load_ids4(1);
       if (!is_v && lane == 0) {
         mbar_arrive_expect_tx(q_full, ntq * Lt::kHalves * tile_toks * G * 128);
         for (int t = 0; t < ntq; ++t)
@@ -405,6 +410,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = lanes + col_o(t);
     const uint32_t pv_done = smem_u32(&sh->pv_done[t]);
     float sl2 = a.scale_log2;
+    // Block scales of a key tile, lanes 0-7 the K, 8-15 the V scales: ids two
+    // tiles and scales one tile ahead.
+    auto id_of = [&](int j) {
+      const int b = (j0 + j) * (kTcKeys / kBlock) + (lane & 7);
+      return lane < 16 && b >= b_lo && b < nblk
+                 ? __ldg(bt + b) : -1;
+    };
+    auto scale_of = [&](int id) {   // (a block that is not read: any finite scale)
+      return id >= 0 && id < a.num_blocks
+                 ? __ldg(((lane & 8) ? a.v_scales : a.k_scales) +
+                         static_cast<int64_t>(id) * a.num_kv_heads + kvh) : 1.f;
+    };
+    float scale_next = scale_of(id_of(0));
+    int id_next = id_of(1);
     // this thread's Q row to fp16
     if (quick_wait(q_full, 0, abort, a.err, wlim)) {
       uint8_t* qrow = sQ + t * Lt::kQTile + row * 128;
@@ -437,20 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(q_conv);
     float m_used = -INFINITY, l = 0.f;
     bool done = t < ntq;
-    // Block scales of a key tile, lanes 0-7 the K, 8-15 the V scales: ids two
-    // tiles and scales one tile ahead.
-    auto id_of = [&](int j) {
-      const int b = (j0 + j) * (kTcKeys / kBlock) + (lane & 7);
-      return lane < 16 && b >= b_lo && b < nblk
-                 ? __ldg(a.block_tables + static_cast<int64_t>(s) * a.bt_stride + b) : -1;
-    };
-    auto scale_of = [&](int id) {   // (a block that is not read: any finite scale)
-      return id >= 0 && id < a.num_blocks
-                 ? __ldg(((lane & 8) ? a.v_scales : a.k_scales) +
-                         static_cast<int64_t>(id) * a.num_kv_heads + kvh) : 1.f;
-    };
-    float scale_next = scale_of(id_of(0));
-    int id_next = id_of(1);
     const int lo = a.window > 0 ? pos - a.window + 1 : 0;   // first key this row sees
     for (int h = 0; done && h < H; ++h) {
       if (!(h & 1)) {   // this tile's scales to shared memory, the next tile's on their way
