@@ -735,14 +735,19 @@ cudaError_t launch_prefill_int8(const CUtensorMap& qmap, const CUtensorMap& kmap
 }
 
 // Parts of the keys for a launch of `ctas` CTAs whose longest walks `tiles` key
-// tiles: as many as fill the SMs, of at least two tiles, and none below six
-// tiles, where the merge costs what the parts save (one 512-token prompt, 4
-// tiles: whole 21 us, two parts 24; 4 x 64 tokens over 1000 keys, 8 tiles: two
-// parts 27.5, four 23).
+// tiles: as many as leave each two tiles and have an SM each, the next power of
+// two if that has them too (2 to 3 us shorter); none below six tiles, where the
+// merge costs what the parts save.  64 tokens, 32 q / 8 kv heads, us in one
+// part - in parts: 3 tiles 15.1 - 19.5 in 3, 4 tiles 17.1 - 16.3 in 4, 6 tiles
+// 21.1 - 18.5 in 4 (21.7 in 3), 8 tiles 25.0 - 18.4 in 4 (22.2 in 2), 12 tiles
+// 32.6 - 18.8 in 8 (22.0 in 6), 64 tiles 133 - 30.8 in 8.
 int prefill_int8_key_splits(int64_t ctas, int tiles, int num_sms) {
   if (ctas <= 0 || tiles < 6) return 1;
-  const int64_t n = std::min<int64_t>({num_sms / ctas, tiles / 2, kMaxKeySplits});
-  return static_cast<int>(std::max<int64_t>(n, 1));
+  const int64_t most = std::min<int64_t>(num_sms / ctas, kMaxKeySplits);
+  const int64_t n = std::max<int64_t>(std::min<int64_t>(most, tiles / 2), 1);
+  int64_t p = 1;
+  while (p < n) p *= 2;
+  return static_cast<int>(p <= most ? p : n);
 }
 
 }  // namespace pkv
