@@ -1317,9 +1317,6 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     f.k_scales = k_scales;
     f.v_scales = v_scales;
     f.scale_log2 = scale_log2;
-    // beside decode rows too (48 of them and 4 x 512 tokens: 154 us in plain
-    // order, 142 longest first; 16 and 2 x 1024: 227, 206)
-    f.longest_first = 1;
     f.key_splits = p.key_splits;
     if (p.key_splits > 1) {
       char* ws = static_cast<char*>(workspace) + p.decode_bytes;
@@ -1328,6 +1325,10 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     }
     const int toks = prefill_tc_tokens_per_cta(G);
     f.num_mtiles = (meta->max_query_len + toks - 1) / toks;
+    // Longest first where the CTAs are more than the SMs, beside decode rows too
+    // (plain - longest first: 4 x 2048 tokens 577 - 562 us, 48 decode rows and 4 x
+    // 512 127 - 124, 16 and 2 x 1024 165 - 156); else the ranking costs 0.8 us.
+    f.longest_first = static_cast<int64_t>(npf) * f.num_mtiles * cache->num_kv_heads > sms;
     CUtensorMap qmap, omap;
     if (int e = encode_query_map(&qmap, q, meta->num_tokens, meta->num_q_heads, cache->head_size, G))
       return e;

@@ -28,6 +28,11 @@
 //    log2 domain; the denominator sums the same rounded weights the MMA uses.
 //  * warps merge through shared memory; a CTA whose sequence needs one split
 //    writes bf16 output, otherwise an fp32 partial + log-sum-exp.
+//  * one-byte caches (e4m3; int8 with block scales, for which pkv_decode_int8.cu
+//    takes the large batches) travel as codes and are widened to fp16 in
+//    registers; int8's K scale multiplies a block's scores and the log of its V
+//    scale joins the exponent.  Int8, 8 kv heads of 128: 1 sequence of 100 keys 5.3
+//    us, of 4000 13; 16 of 300 7.7.
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 

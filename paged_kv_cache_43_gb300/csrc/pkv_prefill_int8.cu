@@ -25,8 +25,15 @@
 //   10, 13    widen K codes in place (D = 128: half the rows each; 64: warp 10)
 //   11, 14    widen V codes
 //   12, 15    issue the products of tile 0, 1
-// Starting a tile's copies and widening it take a warp 1 us each: fewer warps for
-// them (one to start all, two to widen all) bound the step.
+// Starting a tile's copies and widening half of it take a warp 1 us each, and
+// issuing a half step's products of one tile 0.5: with fewer warps for them (one
+// to start all, two to widen all, one to issue all) those bound the step.
+// Measured, 4 x 2048 tokens over 2K to 8K keys (32 q / 8 kv heads, head_size 128):
+// 561 us, 1085 TFLOP/s, 0.57 of the measured bf16 peak (the first form, products of
+// 128 keys as in pkv_prefill_tc.cu: 737).  A step of 128 keys takes 2.1 us, of
+// which the tensor core's reads of shared memory 1.2; an SM is idle or filling
+// for 11 us of each CTA (launch and work choice 2.7, the first K landing, widened
+// and multiplied 5.4, the last rows out 2.8).
 // Weights are first formed against the running reference m, with no pass for
 // the row maximum; only if one may have grown past 2^15 is the maximum found and
 // the 64 weights formed anew.
@@ -708,7 +715,7 @@ cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUt
                      const CUtensorMap& omap, const PrefillArgs& a, cudaStream_t stream) {
   constexpr int smem = smem_bytes<D>();
   const bool parts = a.key_splits > 1;
-  const bool lpt = static_cast<int64_t>(a.num_seqs) * a.num_mtiles <= kLptUnits;
+  const bool lpt = a.longest_first && static_cast<int64_t>(a.num_seqs) * a.num_mtiles <= kLptUnits;
   auto kfn = parts ? pkv_prefill_int8_kernel<D, kKeyParts>
                    : (lpt ? pkv_prefill_int8_kernel<D, kLongestFirst> : pkv_prefill_int8_kernel<D, kPlain>);
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -48,7 +48,8 @@
 //    holds the short ones; beside a decode launch the plain order stays.
 //  * every wait is an mbarrier with a bounded spin and a CTA-wide abort flag;
 //    TMEM is freed on every path.
-//  * FP8 (e4m3) cache: TMA lands each tile's codes (128 keys x D bytes, the
+//  * FP8 (e4m3) cache: warp 9 streams the V tiles; TMA lands each tile's codes
+//    (128 keys x D bytes, the
 //    128- or 64-byte swizzle of the row width) in the first part of its ring
 //    slot and warps 10 and 11 (D = 128: half the rows each; D = 64: warp 10)
 //    widen them in place to fp16 in the bf16 tiles' layout (e4m3 is exact in fp16; codes are read before the fp16
