@@ -403,17 +403,35 @@ def attention_static_scratch(out, q, k_cache, v_cache, block_tables, context_len
         float(scale), ctypes.byref(desc), ctypes.byref(meta), _stream(stream)))
 
 
-def _all_on(dev: int, dtype, *tensors) -> bool:
-    """Whether every tensor is a contiguous one of `dtype` on CUDA device `dev`."""
-    for t in tensors:
-        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-            return False
-    return True
+_BF16, _I8, _I32, _F32, _U8 = (torch.bfloat16, torch.int8, torch.int32, torch.float32,
+                               torch.uint8)
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
+def _int8_fits(dev: int, x, y, kc, vc, bt, cl, qsl, ks, vs) -> bool:
+    """Whether an int8 call's tensors (rows x, y; caches; table, lengths, row
+    starts; scales) are contiguous ones of their types on CUDA device `dev`
+    whose shapes fit (_int8_batch says what does not).  One expression: a small
+    decode step's kernel is over in microseconds, and each of these is 0.07."""
+    c, r, n = kc.shape, x.shape, cl.shape
+    return (x.dtype is _BF16 and y.dtype is _BF16 and kc.dtype is _I8 and vc.dtype is _I8
+            and bt.dtype is _I32 and cl.dtype is _I32 and qsl.dtype is _I32
+            and ks.dtype is _F32 and vs.dtype is _F32
+            and (dev == x.get_device() == y.get_device() == kc.get_device() == vc.get_device()
+                 == bt.get_device() == cl.get_device() == qsl.get_device() == ks.get_device()
+                 == vs.get_device())
+            and x.is_contiguous() and y.is_contiguous() and kc.is_contiguous()
+            and vc.is_contiguous() and bt.is_contiguous() and cl.is_contiguous()
+            and qsl.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
+            and len(c) == 4 and len(r) == 3 and len(n) == 1 and bt.dim() == 2 and qsl.dim() == 1
+            and vc.shape == c and y.shape == r and r[2] == c[3]
+            and ks.shape == vs.shape == (c[0], c[2])
+            and bt.shape[0] >= n[0] and qsl.shape[0] > n[0])
 
 
 def _refuse(dev: int, **tensors) -> None:
     """Says what is wrong with the first tensor (name=(tensor, dtype)) that
-    _all_on did not take."""
+    _int8_fits did not take."""
     for name, (t, dtype) in tensors.items():
         _require(t, name, dtype=dtype)
         if t.get_device() != dev:
@@ -460,11 +478,8 @@ def write_int8(k, v, block_tables, context_lens, query_start_loc, k_cache, v_cac
     [num_blocks, Hkv] of the blocks they touch."""
     lib = _lib or load()
     dev = _current_device()
-    if not (_all_on(dev, torch.bfloat16, k, v) and _all_on(dev, torch.int8, k_cache, v_cache)
-            and _all_on(dev, torch.int32, block_tables, context_lens, query_start_loc)
-            and _all_on(dev, torch.float32, k_scales, v_scales)
-            and _int8_shapes(k, v, k_cache, v_cache, block_tables, context_lens, query_start_loc,
-                             k_scales, v_scales) and k.shape[1] == k_cache.shape[2]):
+    if not (_int8_fits(dev, k, v, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                       k_scales, v_scales) and k.shape[1] == k_cache.shape[2]):
         _int8_batch(dev, k_cache, v_cache, block_tables, context_lens, query_start_loc, k_scales,
                     v_scales, k=k, v=v)
     nb, bs, hkv, d = k_cache.shape
@@ -477,16 +492,6 @@ def write_int8(k, v, block_tables, context_lens, query_start_loc, k_cache, v_cac
                             v_scales.data_ptr(), desc, meta, _stream_on(dev, stream))
     if st != 0:
         _check(st)
-
-
-def _int8_shapes(x, y, k_cache, v_cache, block_tables, context_lens, query_start_loc, k_scales,
-                 v_scales) -> bool:
-    """Whether the shapes of an int8 call's tensors fit (see _int8_batch)."""
-    c, t, S = k_cache.shape, block_tables.shape, context_lens.shape
-    return (len(c) == 4 and v_cache.shape == c and k_scales.shape == v_scales.shape
-            == (c[0], c[2]) and len(x.shape) == 3 and x.shape == y.shape and x.shape[2] == c[3]
-            and len(S) == 1 and len(t) == 2 and t[0] >= S[0] and query_start_loc.dim() == 1
-            and query_start_loc.shape[0] > S[0])
 
 
 # (the current stream's handle without the Stream object around it: 1 us of a
@@ -516,11 +521,8 @@ def attention_int8(out, q, k_cache, v_cache, block_tables, context_lens, query_s
     workspace_size_int8 bytes) is allocated here when not given and needed."""
     lib = _lib or load()
     dev = _current_device()
-    if not (_all_on(dev, torch.bfloat16, out, q) and _all_on(dev, torch.int8, k_cache, v_cache)
-            and _all_on(dev, torch.int32, block_tables, context_lens, query_start_loc)
-            and _all_on(dev, torch.float32, k_scales, v_scales)
-            and _int8_shapes(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
-                             k_scales, v_scales)):
+    if not _int8_fits(dev, out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                      k_scales, v_scales):
         _int8_batch(dev, k_cache, v_cache, block_tables, context_lens, query_start_loc, k_scales,
                     v_scales, out=out, q=q)
     nb, bs, hkv, d = k_cache.shape
@@ -531,14 +533,14 @@ def attention_int8(out, q, k_cache, v_cache, block_tables, context_lens, query_s
     ws_ptr, ws_bytes = 0, 0
     if workspace is None:
         ws_bytes = lib.pkv_attention_int8_workspace_size(desc, meta)
-        if ws_bytes == ctypes.c_size_t(-1).value:
+        if ws_bytes == _NO_SIZE:
             ws_bytes = 0   # (the call itself says what is wrong)
         elif ws_bytes:
             if stream is None:
-                workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+                workspace = q.new_empty(ws_bytes, dtype=_U8)
             else:          # scratch of the stream that uses it
                 with torch.cuda.stream(stream):
-                    workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+                    workspace = q.new_empty(ws_bytes, dtype=_U8)
             ws_ptr = workspace.data_ptr()
     else:
         _refuse(dev, workspace=(workspace, None))
