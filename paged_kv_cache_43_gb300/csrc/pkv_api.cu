@@ -990,12 +990,12 @@ int check_cache_int8(const pkv_cache_desc* c) {
 constexpr int kTeamRangeBlocks = 32;
 
 // The split kernel reads contexts of up to kOneSplitBlocks blocks in one split,
-// however few its CTAs: no partials, no merge launch, no workspace to ask for.
-// Measured one split - the general rule's splits, us on the device (32 / 8 heads
-// of 128): 1 sequence of 100 keys 5.2 - 7.2, of 200 6.9 - 7.9, of 300 (32 / 32)
-// 7.5 - 7.9, 4 of 300 7.7 - 8.5; above, 1 of 500 9.8 - 8.3.  The host's side of a
-// call takes 8 us less in one split.
-constexpr int kOneSplitBlocks = 20;
+// however few its CTAs: no partials, no merge launch, no workspace to ask for,
+// which take 8 us of the host's side of a call (19 - 11).  Measured one split - the
+// general rule's splits, us on the device (32 / 8 heads of 128): 1 sequence of 100
+// keys 5.3 - 7.2, of 200 6.9 - 7.9, of 500 9.8 - 8.2, of 1000 15.4 - 8.9; 4 of 300
+// 7.5 - 8.5.
+constexpr int kOneSplitBlocks = 32;
 
 struct Int8Plan {
   Plan split;              // num_decode, and the split kernel's cut
