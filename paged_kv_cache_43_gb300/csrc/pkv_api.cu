@@ -989,17 +989,24 @@ int check_cache_int8(const pkv_cache_desc* c) {
 // teams of one warp (10 / 5), 16 of 8K to 16K 58 - 62.
 constexpr int kTeamRangeBlocks = 32;
 
-// The split kernel reads contexts of up to kOneSplitBlocks blocks in one split,
-// however few its CTAs: no partials, no merge launch, no workspace to ask for,
-// which take 8 us of the host's side of a call (19 - 11).  Measured one split - the
-// general rule's splits, us on the device (32 / 8 heads of 128): 1 sequence of 100
-// keys 5.3 - 7.2, of 200 6.9 - 7.9, of 500 9.8 - 8.2, of 1000 15.4 - 8.9; 4 of 300
-// 7.5 - 8.5.
-constexpr int kOneSplitBlocks = 32;
+// Up to kDecodeCluster splits of a row are a thread-block cluster, which merges its
+// partials itself: no merge launch, no workspace to ask for (the host's side of a
+// call 19.7 - 10.2 us).  Contexts of up to kOneSplitBlocks take one split, of up to
+// kSmallClusterBlocks at most 8, of up to kClusterBlocks at most 16; longer ones
+// the general rule's splits, a workspace and a merge launch where they are more.
+// Measured, us on the device, workspace - 8 - 16 (32 / 8 heads of 128): 1 sequence
+// of 100 keys 7.2 - 5.9 - 6.5 (one split 5.2), of 500 7.8 - 5.6 - 6.0 (one 9.8), of
+// 1000 8.6 - 6.5 - 7.2, of 2000 11.9 - 8.2 - 7.9, of 4000 13.2 - 10.8 - 9.7, of 8000
+// 15.0 - 16.6 - 13.2, of 16000 19.6 - 26 - 20.4; 4 of 1000 10.2 - 7.9 - 8.3; 8 of 6000
+// 25.6 - 23.3 - 23.6.
+constexpr int kOneSplitBlocks = 8;
+constexpr int kSmallClusterBlocks = 96;
+constexpr int kClusterBlocks = 1024;
 
 struct Int8Plan {
   Plan split;              // num_decode, and the split kernel's cut
   bool teams = false;
+  bool cluster = false;    // the split kernel's CTAs of a row merge among themselves
   int col_groups = 1;      // groups of 8 q heads per kv head
   int team_heads = 1, team_warps = 1;
   int teams_per_range = 1;
@@ -1031,12 +1038,22 @@ int make_int8_decode_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int n
   pkv_cache_desc as_bytes = *c;
   as_bytes.dtype = PKV_FP8_E4M3;
   if (int st = make_plan(&as_bytes, m, num_sms, &p->split)) return st;
-  if (m->kv_split_tokens == 0 && p->split.max_splits > 1 &&
-      p->split.split_blocks * p->split.max_splits <= kOneSplitBlocks) {
-    p->split.split_blocks *= p->split.max_splits;
+  const int split_span = p->split.split_blocks * p->split.max_splits;
+  if (m->kv_split_tokens == 0 && p->split.max_splits > 1 && split_span <= kOneSplitBlocks) {
+    p->split.split_blocks = split_span;
     p->split.max_splits = 1;
-    p->split.ws_o_bytes = p->split.ws_bytes = 0;
   }
+  const int most = split_span <= kSmallClusterBlocks ? kDecodeCluster / 2 : kDecodeCluster;
+  // (splits that the caller asked for go through the workspace, and so do those
+  // beside chunk rows, whose CTAs rarely leave a cluster its SMs at one time: 16 rows
+  // of 1K to 8K keys and 2 x 1024 tokens 156 us, 179 with clusters)
+  const bool may = m->kv_split_tokens == 0 && p->split.num_decode == m->num_seqs;
+  if (may && p->split.max_splits > most && split_span <= kClusterBlocks) {
+    p->split.split_blocks = (split_span + most - 1) / most;
+    p->split.max_splits = (split_span + p->split.split_blocks - 1) / p->split.split_blocks;
+  }
+  p->cluster = may && p->split.max_splits > 1 && p->split.max_splits <= kDecodeCluster;
+  if (p->cluster || p->split.max_splits <= 1) p->split.ws_o_bytes = p->split.ws_bytes = 0;
   p->decode_bytes = p->split.ws_bytes;
   const int nd = p->split.num_decode;
   if (nd == 0) return PKV_OK;
@@ -1267,8 +1284,9 @@ extern "C" int pkv_attention_int8(void* out, const void* q, const void* k_cache,
     d.k_scales = k_scales;
     d.v_scales = v_scales;
     d.scale_log2 = scale_log2;
+    d.cluster = p.cluster;
     PKV_TRY(launch_decode_int8(kmap, vmap, d, cache->head_size, st));
-    PKV_TRY(launch_combine_bf16(d, cache->head_size, st, /*after_decode=*/true));
+    if (!p.cluster) PKV_TRY(launch_combine_bf16(d, cache->head_size, st, /*after_decode=*/true));
     return PKV_OK;
   };
   auto prefill_part = [&](cudaStream_t st) -> int {

@@ -124,6 +124,24 @@ __device__ __forceinline__ float int8_scale(float s) {
   return s < kInt8ScaleFloor ? kInt8ScaleFloor : s;
 }
 
+// ---- thread-block clusters: a barrier over the cluster's threads that have not
+// exited (shared-memory writes before it are visible to the others after it),
+// and loads from another CTA's shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\t"
+      "ld.shared::cluster.f32 %0, [r];\n\t}"
+      : "=f"(v)
+      : "r"(addr), "r"(rank)
+      : "memory");
+  return v;
+}
+
 // Named barrier over `nthreads` threads (a multiple of 32).
 __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

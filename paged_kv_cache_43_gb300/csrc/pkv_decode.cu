@@ -31,8 +31,9 @@
 //  * one-byte caches (e4m3; int8 with block scales, for which pkv_decode_int8.cu
 //    takes the large batches) travel as codes and are widened to fp16 in
 //    registers; int8's K scale multiplies a block's scores and the log of its V
-//    scale joins the exponent.  Int8, 8 kv heads of 128: 1 sequence of 100 keys 5.3
-//    us, of 4000 13; 16 of 300 7.7.
+//    scale joins the exponent.  Int8's splits of a row are a cluster that merges
+//    its partials through shared memory (make_int8_decode_plan has the rule).  8 kv
+//    heads of 128: 1 sequence of 100 keys 5.3 us, of 4000 9.7; 16 of 300 7.7.
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 
@@ -610,6 +611,47 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
   }
   __syncthreads();
 
+  if constexpr (I8) {
+    // A cluster of the row's splits: each CTA's partial stays in its shared
+    // memory, and the CTAs share out the merge, 128 outputs at a time.
+    if (a.cluster != 0 && nsplit > 1) {
+      float* part = merge_area(0);   // (each element is read and written by one thread)
+      for (int idx = threadIdx.x; idx < 8 * D; idx += NW * 32) {
+        float r = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) r += merge_f[w * 8 + idx / D] * merge_area(w)[idx];
+        part[idx] = r;
+      }
+      cluster_sync();   // (splits past the context's end have exited)
+      const uint32_t part_at = smem_u32(part), lse_at = smem_u32(merge_f + NW * 8);
+      auto merge = [&]<int N>() {   // (N loads of each kind in flight)
+        for (int idx = NW * 32 * split + threadIdx.x; idx < 8 * D; idx += NW * 32 * nsplit) {
+          const int c = idx / D, g = gsub * 8 + c;
+          if (g >= G) continue;
+          float lse[N], v[N], M = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            lse[k] = k < nsplit ? ld_cluster(lse_at + 4 * c, k) : -INFINITY;
+            v[k] = k < nsplit ? ld_cluster(part_at + 4 * idx, k) : 0.f;
+            M = fmaxf(M, lse[k]);
+          }
+          float den = 0.f, r = 0.f;
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const float f = lse[k] == -INFINITY ? 0.f : exp2f(lse[k] - M);
+            den += f;
+            r = f == 0.f ? r : fmaf(f, v[k], r);
+          }
+          out[(static_cast<int64_t>(q0) * Hq + kvh * G + g) * D + idx % D] =
+              __float2bfloat16(den == 0.f ? 0.f : r / den);
+        }
+      };
+      if (nsplit <= kDecodeCluster / 2) merge.template operator()<kDecodeCluster / 2>();
+      else merge.template operator()<kDecodeCluster>();
+      cluster_sync();   // the partials stay until all have been read
+      return;
+    }
+  }
   const bool direct = !PREFIX && nsplit == 1 && !a.force_partial;
   for (int idx = threadIdx.x; idx < 8 * D; idx += NW * 32) {
     const int c = idx / D;
@@ -766,6 +808,26 @@ cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap,
             PREFIX ? 1 : a.num_seqs);
   DecodeArgs b = a;
   debug_wait_settings(&b.wait_limit_ns, &b.debug_stall);
+  if constexpr (FMT == kInt8)
+    if (a.cluster != 0) {
+      if (grid.x > 8) {
+        e = cudaFuncSetAttribute(kfn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+      }
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = grid;
+      cfg.blockDim = dim3(kDecodeWarps * 32);
+      cfg.dynamicSmemBytes = smem;
+      cfg.stream = stream;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = grid.x;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      return cudaLaunchKernelEx(&cfg, kfn, kmap, vmap, b);
+    }
   kfn<<<grid, kDecodeWarps * 32, smem, stream>>>(kmap, vmap, b);
   return cudaGetLastError();
 }

@@ -71,10 +71,14 @@ struct DecodeArgs {
   // that its wait runs out.
   uint64_t wait_limit_ns;
   int32_t debug_stall;
-  // Int8 cache: block scales [num_blocks, Hkv] (null otherwise)
+  // Int8 cache: block scales [num_blocks, Hkv] (null otherwise); cluster != 0:
+  // the max_splits (<= kDecodeCluster) CTAs of a row are a cluster that merges
+  // its partials itself
   const float* k_scales;
   const float* v_scales;
+  int32_t cluster;
 };
+constexpr int kDecodeCluster = 16;   // (more than 8: where the GPU allows it, as this one does)
 
 // Varlen causal attention over sequences [seq_begin, seq_begin + num_seqs).
 struct PrefillArgs {
