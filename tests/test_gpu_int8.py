@@ -281,6 +281,25 @@ def test_decode_edge_lengths_and_groups(hq, hkv, d, bound):
     assert pkv.get_error() == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(8, 8, 128), (12, 1, 64), (20, 2, 128)])
+@pytest.mark.parametrize("ctx", [[129], [1000, 3], [1537, 700, 16], [4100], [16384, 1, 5000]])
+def test_decode_few_sequences_merge_their_splits(ctx, hq, hkv, d):
+    """A row's splits (up to 16) merge among themselves; shorter sequences of
+    the batch have fewer, or none."""
+    b = batch(ctx, [1] * len(ctx), hq, hkv, d, seed=hq + len(ctx), step=3000)
+    for window in (0, 777):
+        check_attention(*b, window=window)
+    cache, qs, bt, cl, qsl, scale = b
+    bad = bt.clone()
+    bad[0, 1] = cache.kc.shape[0]              # the other sequences stay right
+    good, ref, tol = attend(*b)
+    out = torch.zeros(qs.shape, dtype=torch.bfloat16, device="cuda")
+    pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], bad.cuda(), cl.cuda(), qsl.cuda(), scale,
+                       *cache.gpu[2:], max_query_len=1, max_context_len=int(cl.max()))
+    assert pkv.get_error() == pkv.ERR_BLOCK_ID
+    assert len(ctx) == 1 or (np.abs(out.float().cpu().numpy() - ref) / tol)[1:].max() <= 1
+
+
 @pytest.mark.parametrize("seqs", [1, 3, 255, 256, 257, 600])
 def test_decode_many_short_sequences_and_empty_ones(seqs):
     """Ranges with many sequences in them; sequences without rows, single keys."""
