@@ -34,6 +34,8 @@
 //    scale joins the exponent.  Int8's splits of a row are a cluster that merges
 //    its partials through shared memory (make_int8_decode_plan has the rule).  8 kv
 //    heads of 128: 1 sequence of 100 keys 5.3 us, of 4000 9.7; 16 of 300 7.7.
+#include <type_traits>
+
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 
@@ -624,7 +626,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
       }
       cluster_sync();   // (splits past the context's end have exited)
       const uint32_t part_at = smem_u32(part), lse_at = smem_u32(merge_f + NW * 8);
-      auto merge = [&]<int N>() {   // (N loads of each kind in flight)
+      auto merge = [&](auto most) {   // (that many loads of each kind in flight)
+        constexpr int N = decltype(most)::value;
         for (int idx = NW * 32 * split + threadIdx.x; idx < 8 * D; idx += NW * 32 * nsplit) {
           const int c = idx / D, g = gsub * 8 + c;
           if (g >= G) continue;
@@ -646,8 +649,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
               __float2bfloat16(den == 0.f ? 0.f : r / den);
         }
       };
-      if (nsplit <= kDecodeCluster / 2) merge.template operator()<kDecodeCluster / 2>();
-      else merge.template operator()<kDecodeCluster>();
+      if (nsplit <= kDecodeCluster / 2) merge(std::integral_constant<int, kDecodeCluster / 2>{});
+      else merge(std::integral_constant<int, kDecodeCluster>{});
       cluster_sync();   // the partials stay until all have been read
       return;
     }
