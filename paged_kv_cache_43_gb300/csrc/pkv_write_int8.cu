@@ -160,11 +160,12 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
     return;
   }
   float* scale_at = (is_v ? a.v_scales : a.k_scales) + static_cast<int64_t>(bid) * hkv + h;
-  float old = 0.f;
+  float stored = 0.f, old = 0.f;
   if (o0 > 0) {
-    old = *scale_at;
-    // (a block that was never begun: its codes count as zero)
-    if (!(old >= kInt8ScaleFloor && old <= FLT_MAX)) old = kInt8ScaleFloor;
+    stored = *scale_at;
+    // (a scale that no write makes, as of a block that was never begun, counts as
+    // the floor, and the floor goes to memory if the new rows ask for no more)
+    old = stored >= kInt8ScaleFloor && stored <= FLT_MAX ? stored : kInt8ScaleFloor;
   }
   // largest magnitude: bf16 patterns without their sign compare like the values
   uint32_t top = 0;
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32)
                        requantise4(c.w, ratio));
     }
   }
-  if (lane == 0 && scale != old) *scale_at = scale;
+  if (lane == 0 && scale != stored) *scale_at = scale;   // (a NaN differs)
   const float inv = __fdiv_rn(1.f, scale);
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
