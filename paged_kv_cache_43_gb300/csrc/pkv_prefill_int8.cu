@@ -466,7 +466,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lo = a.window > 0 ? pos - a.window + 1 : 0;   // first key this row sees
     for (int h = 0; done && h < H; ++h) {
       if (!(h & 1)) {   // this tile's scales to shared memory, the next tile's on their way
-        const float now = int8_scale(scale_next);
+        float now = int8_scale(scale_next);
+        // A scale that is not finite counts as 1 here, where masked keys meet it too;
+        // the rows that see a key of its block become NaN through their sums.
+        const uint32_t odd = __ballot_sync(0xffffffffu, lane < 16 && !(now <= FLT_MAX));
+        if (odd != 0) {
+          if (!(now <= FLT_MAX)) now = 1.f;
+          for (uint32_t left = (odd | odd >> 8) & 0xffu; left != 0; left &= left - 1) {
+            const int p0 = (j0 + (h >> 1)) * kTcKeys + (__ffs(left) - 1) * kBlock;
+            if (p0 <= pos && p0 + kBlock > lo) l = NAN;
+          }
+        }
         scale_next = scale_of(id_next);
         id_next = id_of((h >> 1) + 2);
         const float lv = log2f(__shfl_sync(0xffffffffu, now, 8 + (lane & 7)));
@@ -593,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool ok = done && warp_wait(smem_u32(&sh->o_done[t]), 0, abort, a.err, wlim);
     if (t < ntq) {
       tc::fence_after_sync();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;   // (a NaN stays)
       // every row of the tile is a query row of this sequence: its rows go out
       // through the tile's Q slot (its products have all completed), in the
       // swizzled layout Q arrived in, and one TMA store per 64-column half (a row

@@ -34,3 +34,51 @@ def test_write_replaces_a_stored_scale_that_is_not_one(stored, n, what):
     for scales in cache.gpu[2:]:
         held = scales[[0, 2]]
         assert torch.isfinite(held).all() and (held >= 2.0 ** -60).all()
+
+
+# -------------------------------------------------------------- attention
+
+def poison(cache, which, block, head, value):
+    """The scale of (block, head) of K or V is `value` on the GPU; returns what undoes it."""
+    t = cache.gpu[2 if which == "k" else 3]
+    old = float(t[block, head])
+    t[block, head] = value
+
+    def undo():
+        t[block, head] = old
+    return undo
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("hq,hkv,d,bound", [(8, 2, 128, None), (4, 2, 64, None), (6, 2, 128, 9000),
+                                            (32, 2, 64, 9000), (260, 2, 64, None)])
+def test_a_bad_scale_reaches_no_row_that_does_not_see_its_block(which, value, window, hq, hkv, d,
+                                                                bound):
+    """Chunks whose rows see different blocks: a scale that is NaN makes the rows
+    that see a key of its block NaN (an infinite one does so at least where a
+    score is not negative), and leaves the others as they are."""
+    q, ctx = [64, 100], [64, 333]
+    b = batch(ctx, q, hq, hkv, d, seed=hq + d)
+    cache, qs, bt, cl, qsl, scale = b
+    # (row tiles side by side and, with the loose bound, parts of the keys)
+    kw = dict(window=window, max_context_len=bound)
+    group = hq // hkv
+    pos = np.concatenate([np.arange(c - n, c) for n, c in zip(q, ctx)])
+    seq = np.repeat([0, 1], q)
+    for s, j in ((0, 3), (0, 1), (1, 20), (1, 17), (1, 14), (1, 16)):
+        undo = poison(cache, which, int(bt[s, j]), 1, value)
+        got, ref, tol = attend(*b, **kw)       # (the oracle's copy keeps the sound scale)
+        undo()
+        sees = (seq == s) & (pos >= 16 * j)
+        if window:
+            sees &= pos - window + 1 <= 16 * j + 15
+        mine = np.zeros(got.shape[:2], bool)
+        mine[sees, group:] = True
+        assert mine.any() and not mine.all()
+        if np.isnan(value):
+            assert np.isnan(got[mine]).all()
+        bad = ~(np.abs(got - ref) <= tol)
+        assert not bad[~mine].any(), (s, j, np.argwhere(bad.any(-1) & ~mine)[:4])
+    assert pkv.get_error() == 0
