@@ -332,8 +332,8 @@ int pkv_write_int8(const void *k, const void *v, const int32_t *block_tables,
 
 /* PagedAttention over an INT8 cache: as pkv_attention (lengths, masks, window,
  * errors, rows left alone) with q and out in bf16.  A scale below 2^-60 (zero
- * included) counts as 2^-60, an infinite or NaN one makes the rows that see its
- * block NaN; scales of blocks that no query sees are not read.  A batch's
+ * and negative ones included) counts as 2^-60; one that is +infinity or NaN makes
+ * the rows that see a key of its block NaN, and no others.  A batch's
  * sequences past num_decode_seqs are 65535 at most (PKV_E_SHAPE).
  * The workspace's size comes from pkv_attention_int8_workspace_size (not from
  * pkv_attention_workspace_size); it is scratch of one call, so calls that may

@@ -116,12 +116,13 @@ __device__ __forceinline__ int seq_of_row(const int32_t* qsl, int num_seqs, int 
   return (num_seqs > 0 && __ldg(qsl + lo) <= tok && tok < __ldg(qsl + lo + 1)) ? lo : -1;
 }
 
-// int8 caches: block scales below this (zero included) count as this, so that
-// a block of zeros keeps a scale whose reciprocal and logarithm are finite;
-// NaN stays NaN.
+// int8 caches: block scales below this (zero and negative ones included) count
+// as this, so that a block of zeros keeps a scale whose reciprocal and logarithm
+// are finite; NaN stays NaN, and an infinite scale becomes one (its products with
+// scores below zero would be weights of zero and leave the block out unseen).
 constexpr float kInt8ScaleFloor = 0x1p-60f;
 __device__ __forceinline__ float int8_scale(float s) {
-  return s < kInt8ScaleFloor ? kInt8ScaleFloor : s;
+  return s < kInt8ScaleFloor ? kInt8ScaleFloor : (s < INFINITY ? s : NAN);
 }
 
 // ---- thread-block clusters: a barrier over the cluster's threads that have not

@@ -466,12 +466,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lo = a.window > 0 ? pos - a.window + 1 : 0;   // first key this row sees
     for (int h = 0; done && h < H; ++h) {
       if (!(h & 1)) {   // this tile's scales to shared memory, the next tile's on their way
-        float now = int8_scale(scale_next);
-        // A scale that is not finite counts as 1 here, where masked keys meet it too;
-        // the rows that see a key of its block become NaN through their sums.
-        const uint32_t odd = __ballot_sync(0xffffffffu, lane < 16 && !(now <= FLT_MAX));
+        // A scale that is not finite counts as 1 here (as int8_scale otherwise), where
+        // masked keys meet it too; the rows that see a key of its block become NaN
+        // through their sums.
+        float now = fmaxf(scale_next, kInt8ScaleFloor);
+        const uint32_t odd = __ballot_sync(0xffffffffu, lane < 16 && !(scale_next <= FLT_MAX));
         if (odd != 0) {
-          if (!(now <= FLT_MAX)) now = 1.f;
+          if (!(scale_next <= FLT_MAX)) now = 1.f;
           for (uint32_t left = (odd | odd >> 8) & 0xffu; left != 0; left &= left - 1) {
             const int p0 = (j0 + (h >> 1)) * kTcKeys + (__ffs(left) - 1) * kBlock;
             if (p0 <= pos && p0 + kBlock > lo) l = NAN;

@@ -82,3 +82,31 @@ def test_a_bad_scale_reaches_no_row_that_does_not_see_its_block(which, value, wi
         bad = ~(np.abs(got - ref) <= tol)
         assert not bad[~mine].any(), (s, j, np.argwhere(bad.any(-1) & ~mine)[:4])
     assert pkv.get_error() == 0
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("ctx,chunk,hq,hkv,bound", [
+    ([100, 60], 1, 8, 4, None),            # a CTA for the row
+    ([1200, 600], 1, 8, 4, None),          # splits that merge in a cluster
+    ([1200, 600], 1, 8, 4, 200000),        # teams
+    ([1200, 600], 20, 8, 4, None),         # chunks, parts of the keys
+    ([300, 200], 64, 40, 1, None),         # chunks
+    ([300, 200], 5, 130, 1, None)])        # more q heads than a row tile has rows
+def test_an_infinite_scale_makes_the_rows_that_see_it_nan(which, sign, ctx, chunk, hq, hkv, bound):
+    """Also where every score against the block's codes has the same sign."""
+    b = batch(ctx, [chunk] * 2, hq, hkv, 64, seed=7)
+    cache, qs, bt, cl, qsl, scale = b
+    blk = int(bt[0, 1])
+    cache.kc[blk] = np.abs(cache.kc[blk])       # scores of this block: the query's sign
+    cache.gpu[0][blk] = cache.gpu[0][blk].abs()
+    qs[:] = sign * qs.abs()
+    good, ref, tol = attend(*b, max_context_len=bound)
+    assert (np.abs(good - ref) <= tol).all()
+    undo = poison(cache, which, blk, 0, np.inf)
+    got, _, _ = attend(*b, max_context_len=bound)
+    undo()
+    assert np.isnan(got[:chunk, :hq // hkv]).all()
+    got[:chunk, :hq // hkv] = ref[:chunk, :hq // hkv]
+    assert (np.abs(got - ref) <= tol).all()
+    assert pkv.get_error() == 0
