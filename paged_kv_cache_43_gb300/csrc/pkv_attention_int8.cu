@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kWarps * 32) pkv_attention_int8_kernel(const A
     }
     const int64_t sc = static_cast<int64_t>(bid) * a.num_kv_heads + kvh;
     const float ks = int8_scale(__ldg(a.k_scales + sc)), vs = int8_scale(__ldg(a.v_scales + sc));
+    const float vs_down = vs * (1.f / kTwoSumBias);   // (many V of about 2^127 add up below infinity)
     const int64_t row =
         ((static_cast<int64_t>(bid) * kBlock + p % kBlock) * a.num_kv_heads + kvh) * D + lane * PER;
     float dot = 0.f;
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kWarps * 32) pkv_attention_int8_kernel(const A
     l = l * alpha + w;
 #pragma unroll
     for (int e = 0; e < PER; ++e)
-      acc[e] = fmaf(w * vs, static_cast<float>(static_cast<const int8_t*>(a.v_cache)[row + e]),
+      acc[e] = fmaf(w * vs_down, static_cast<float>(static_cast<const int8_t*>(a.v_cache)[row + e]),
                     acc[e] * alpha);
     m = mn;
   }
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kWarps * 32) pkv_attention_int8_kernel(const A
     float r = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) r += f[w] * sm_o[w][d];
-    out[d] = __float2bfloat16(den == 0.f ? 0.f : r / den);
+    out[d] = __float2bfloat16(den == 0.f ? 0.f : r / den * kTwoSumBias);
   }
 }
 

@@ -125,6 +125,13 @@ __device__ __forceinline__ float int8_scale(float s) {
   return s < kInt8ScaleFloor ? kInt8ScaleFloor : (s < INFINITY ? s : NAN);
 }
 
+// The V scales lv (log2) that one row sees span [-60, 121].  Its exponent reference m
+// follows the largest x + lv, so the terms 2^(x - m) of its denominator lie about
+// 2^-lv: the sums are held times 2^kSumBias, which leaves 2^20 keys their bits at
+// either end.  The terms are formed from x itself: a weight 2^(x + lv - m) goes to
+// zero where lv is far below the largest, although its term may count.
+constexpr float kSumBias = 30.f, kTwoSumBias = 0x1p30f;
+
 // ---- thread-block clusters: a barrier over the cluster's threads that have not
 // exited (shared-memory writes before it are visible to the others after it),
 // and loads from another CTA's shared memory.

@@ -360,8 +360,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
   // Int8: the same step with the block's scales.  The weight that meets the V
   // codes is w = 2^(x + log2 sv - m), m following the largest x + log2 sv: w in
   // fp16 is at most 2^8 and exact to 2^-11 of the numerator's largest terms
-  // whatever the scales' sizes; the denominator adds w / sv, in fp32 and before
-  // the rounding.
+  // whatever the scales' sizes; the denominator adds 2^(x - m), in fp32.
   auto softmax_step_i8 = [&](const float (&sc)[4], int i, int p0, uint32_t& pb0, uint32_t& pb1) {
     const float ks = __shfl_sync(0xffffffffu, my_ks, i);
     const float lv = __shfl_sync(0xffffffffu, my_lv, i);
@@ -383,12 +382,14 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
       }
       const float mn0 = fmaxf(m[0], mx0), mn1 = fmaxf(m[1], mx1);
-      const float alpha0 = mn0 == -INFINITY ? 1.f : ex2(m[0] - mn0);
-      const float alpha1 = mn1 == -INFINITY ? 1.f : ex2(m[1] - mn1);
+      // (in two steps: the sums may be far above 1 where the factor is below 2^-126)
+      const float half0 = mn0 == -INFINITY ? 1.f : ex2(0.5f * (m[0] - mn0));
+      const float half1 = mn1 == -INFINITY ? 1.f : ex2(0.5f * (m[1] - mn1));
+      const float alpha0 = half0 * half0, alpha1 = half1 * half1;
       m[0] = mn0;
       m[1] = mn1;
-      l[0] *= alpha0;
-      l[1] *= alpha1;
+      l[0] = l[0] * half0 * half0;
+      l[1] = l[1] * half1 * half1;
 #pragma unroll
       for (int dt = 0; dt < D / 16; ++dt) {
         o[dt][0] *= alpha0;
@@ -401,9 +402,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
     const float mu1 = m[1] == -INFINITY ? 0.f : m[1];
     const float w0 = ex2(y[0] - mu0), w1 = ex2(y[1] - mu1);
     const float w2 = ex2(y[2] - mu0), w3 = ex2(y[3] - mu1);
-    const float ivs = ex2(-lv);
-    l[0] = fmaf(w0 + w2, ivs, l[0]);
-    l[1] = fmaf(w1 + w3, ivs, l[1]);
+    const float d0 = kSumBias - lv - mu0, d1 = kSumBias - lv - mu1;
+    l[0] += ex2(y[0] + d0) + ex2(y[2] + d0);
+    l[1] += ex2(y[1] + d1) + ex2(y[3] + d1);
     pb0 = movmatrix_trans(pack_f16(w0, w1));
     pb1 = movmatrix_trans(pack_f16(w2, w3));
   };
@@ -598,15 +599,33 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
     for (int w = 0; w < NW; ++w) M = fmaxf(M, merge_area(w)[8 * D + c]);
     float den = 0.f;
     float f[NW];
-    for (int w = 0; w < NW; ++w) {
-      const float* ww = merge_area(w);
-      f[w] = (M == -INFINITY) ? 0.f : exp2f(ww[8 * D + c] - M);
-      den += f[w] * ww[8 * D + 8 + c];
-    }
-    if constexpr (I8) {   // a NaN stays one (the combine makes it of an infinite lse)
-      for (int w = 0; w < NW; ++w) merge_f[w * 8 + c] = den == 0.f ? 0.f : f[w] / den;
-      merge_f[NW * 8 + c] = den == 0.f ? -INFINITY : (den > 0.f ? M + log2f(den) : INFINITY);
+    if constexpr (I8) {
+      // The warps' sums m + log2 l, relative to M, against the largest of them E (m
+      // alone follows the numerators: where their V scales differ, so do the sums).
+      // A NaN stays one (the combine makes it of an infinite lse).
+      if (M == -INFINITY) M = 0.f;   // (no key, or NaN scores only)
+      float E = -INFINITY;
+      for (int w = 0; w < NW; ++w) {
+        const float* ww = merge_area(w);
+        const float l_w = ww[8 * D + 8 + c];
+        f[w] = l_w == 0.f ? -INFINITY : ww[8 * D + c] - M + log2f(l_w);
+        E = fmaxf(E, f[w]);
+      }
+      for (int w = 0; w < NW; ++w) {
+        const bool none = f[w] == -INFINITY;
+        den += none ? 0.f : exp2f(f[w] - E);
+        f[w] = none ? 0.f : exp2f(merge_area(w)[8 * D + c] - M - E);
+      }
+      for (int w = 0; w < NW; ++w)
+        merge_f[w * 8 + c] = f[w] == 0.f ? 0.f : f[w] * (kTwoSumBias / den);
+      merge_f[NW * 8 + c] =
+          den == 0.f ? -INFINITY : (den > 0.f ? M + (E + log2f(den) - kSumBias) : INFINITY);
     } else {
+      for (int w = 0; w < NW; ++w) {
+        const float* ww = merge_area(w);
+        f[w] = (M == -INFINITY) ? 0.f : exp2f(ww[8 * D + c] - M);
+        den += f[w] * ww[8 * D + 8 + c];
+      }
       for (int w = 0; w < NW; ++w) merge_f[w * 8 + c] = den > 0.f ? f[w] * out_scale / den : 0.f;
       merge_f[NW * 8 + c] = den > 0.f ? M + log2f(den) : -INFINITY;
     }

@@ -10,9 +10,11 @@
 // log2 sv[b(p)] - m): the block's V scale rides in the exponent, and m
 // follows the largest x_p + log2 sv, so that w_p, rounded to fp16, is at most
 // 2^8 and exact to 2^-11 relative to the largest term of the numerator,
-// whatever the scales' sizes.  The denominator adds w_p / sv[b(p)] in fp32
-// before that rounding.  Codes are exact in fp16 (|c| <= 127), so K and V are
-// not rounded at all; Q is scaled by a power of two into fp16's range.
+// whatever the scales' sizes.  The denominator adds 2^(x_p - m) in fp32 (not
+// w_p / sv[b(p)], which is zero where w_p is too small a number beside a far larger
+// scale; the kernel waits for HBM, so the second exponential costs nothing).
+// Codes are exact in fp16 (|c| <= 127), so K and V are not rounded at all; Q is
+// scaled by a power of two into fp16's range.
 //
 // Split.  The decode sequences' blocks, one sequence after the other, form
 // one line (with kSeqCost blocks of nothing before each sequence, for what its
@@ -407,7 +409,6 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
         }
         // ---- weights.  The reference m of a column moves only when an
         // exponent exceeds it by more than 8, so most blocks cost one vote.
-        const float ivs = ex2(-lv);
         float y[4];
         y[0] = fmaf(sc[0] + sd[0], col_scale[0] * ks, lv);
         y[1] = fmaf(sc[1] + sd[1], col_scale[1] * ks, lv);
@@ -429,12 +430,14 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
             mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
           }
           const float mn0 = fmaxf(m[0], mx0), mn1 = fmaxf(m[1], mx1);
-          const float alpha0 = mn0 == -INFINITY ? 1.f : ex2(m[0] - mn0);
-          const float alpha1 = mn1 == -INFINITY ? 1.f : ex2(m[1] - mn1);
+          // (in two steps: the sums may be far above 1 where the factor is below 2^-126)
+          const float half0 = mn0 == -INFINITY ? 1.f : ex2(0.5f * (m[0] - mn0));
+          const float half1 = mn1 == -INFINITY ? 1.f : ex2(0.5f * (m[1] - mn1));
+          const float alpha0 = half0 * half0, alpha1 = half1 * half1;
           m[0] = mn0;
           m[1] = mn1;
-          l[0] *= alpha0;
-          l[1] *= alpha1;
+          l[0] = l[0] * half0 * half0;
+          l[1] = l[1] * half1 * half1;
 #pragma unroll
           for (int dt = 0; dt < D / 16; ++dt) {
             o[dt][0] *= alpha0;
@@ -447,8 +450,9 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
         const float mu1 = m[1] == -INFINITY ? 0.f : m[1];
         const float w0 = ex2(y[0] - mu0), w1 = ex2(y[1] - mu1);
         const float w2 = ex2(y[2] - mu0), w3 = ex2(y[3] - mu1);
-        l[0] = fmaf(w0 + w2, ivs, l[0]);
-        l[1] = fmaf(w1 + w3, ivs, l[1]);
+        const float d0 = kSumBias - lv - mu0, d1 = kSumBias - lv - mu1;
+        l[0] += ex2(y[0] + d0) + ex2(y[2] + d0);
+        l[1] += ex2(y[1] + d1) + ex2(y[3] + d1);
         const uint32_t pb0 = movmatrix_trans(pack_f16(w0, w1));   // rows = heads
         const uint32_t pb1 = movmatrix_trans(pack_f16(w2, w3));
         // ---- O^T += V^T . W^T
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
         const int g = gsub * 8 + c0 + c;
         if (g >= G) continue;
         const int hq = kvh * G + g;
-        const float inv = l[c] == 0.f ? 0.f : 1.f / l[c];
+        const float inv = l[c] == 0.f ? 0.f : kTwoSumBias / l[c];
         if (whole) {   // D / 8 consecutive d a lane
           uint32_t w[D / 16];
 #pragma unroll
@@ -496,7 +500,8 @@ __global__ void __launch_bounds__(kThreads, kDecInt8CtasPerSm)
             dst[i] = make_float4(o[2 * i][c] * inv, o[2 * i][2 + c] * inv, o[2 * i + 1][c] * inv,
                                  o[2 * i + 1][2 + c] * inv);
           // (the exponent reference m carries log2 sv; l has it divided out)
-          if (r0 == 0) a.ws_lse[slot * Hq + hq] = l[c] == 0.f ? -INFINITY : m[c] + log2f(l[c]);
+          if (r0 == 0)
+            a.ws_lse[slot * Hq + hq] = l[c] == 0.f ? -INFINITY : m[c] + (log2f(l[c]) - kSumBias);
         }
       }
       if (!alive) {

@@ -7,7 +7,8 @@
 // fp16, a row of Q is scaled by a power of two into its range.  P = 2^(x + log2
 // sv - m): a block's V scale rides in the softmax exponent, and m follows the
 // largest x + log2 sv, so P in fp16 is at most 2^15 whatever the scales are;
-// the row sum divides sv out again (per block, in fp32).  Both scales cost
+// the row sum divides sv out again (per block, in fp32; from the first V scale
+// above kLargeScale on it is formed without it).  Both scales cost
 // nothing per element: they are the factor and the addend of the exponent's one
 // FMA.  Every code is finite, so rows no key may see need no zeroing.
 //
@@ -55,6 +56,10 @@ constexpr int kHalfBlocks = kHalfKeys / kBlock;
 constexpr int kRegsSoftmax = 168;
 constexpr int kRegsOther = 88;
 static_assert(2 * 128 * (kRegsSoftmax + kRegsOther) <= kThreads * 128, "register split");
+// V scales up to this are within 2^64 of the smallest: dividing them out of the weights
+// loses less than 2^-54 of the row sum a key.
+constexpr float kLogLargeScale = 4.f, kLargeScale = kInt8ScaleFloor * 0x1p64f;
+static_assert(kLargeScale == 16.f, "2^kLogLargeScale");
 
 // TMEM columns: S of tile t, half step h at 128t + 64 (h % 2), P over its first
 // 32; O of tile t at 256 + 128t.
@@ -73,8 +78,9 @@ struct Shared {
   uint32_t tmem_base;
   int32_t abort;
   int32_t n_issued[2];           // K / V tiles started, for the drain
-  // (K scale, log2 of the V scale, 1 / V scale, the tile's largest V scale) of a
-  // key tile's blocks, a copy for each softmax warp.
+  // (K scale, log2 of the V scale, 2^kSumBias / V scale, the tile's largest V scale
+  // / 2^kSumBias or, of a marked tile, infinity) of a key tile's blocks, a copy for
+  // each softmax warp.
   alignas(16) float4 sc[8][kTcKeys / kBlock];
 };
 
@@ -462,31 +468,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(q_conv);
     float m_used = -INFINITY, l = 0.f;
+    float limit = kLargeScale;   // V scales above it mark their tile
     bool done = t < ntq;
     const int lo = a.window > 0 ? pos - a.window + 1 : 0;   // first key this row sees
     for (int h = 0; done && h < H; ++h) {
       if (!(h & 1)) {   // this tile's scales to shared memory, the next tile's on their way
-        // A scale that is not finite counts as 1 here (as int8_scale otherwise), where
-        // masked keys meet it too; the rows that see a key of its block become NaN
-        // through their sums.
-        float now = fmaxf(scale_next, kInt8ScaleFloor);
-        const uint32_t odd = __ballot_sync(0xffffffffu, lane < 16 && !(scale_next <= FLT_MAX));
-        if (odd != 0) {
-          if (!(scale_next <= FLT_MAX)) now = 1.f;
-          for (uint32_t left = (odd | odd >> 8) & 0xffu; left != 0; left &= left - 1) {
-            const int p0 = (j0 + (h >> 1)) * kTcKeys + (__ffs(left) - 1) * kBlock;
-            if (p0 <= pos && p0 + kBlock > lo) l = NAN;
-          }
-        }
+        // (as int8_scale, but an infinite or NaN scale stays for now)
+        const float now = scale_next < kInt8ScaleFloor ? kInt8ScaleFloor : scale_next;
         scale_next = scale_of(id_next);
         id_next = id_of((h >> 1) + 2);
         const float lv = log2f(__shfl_sync(0xffffffffu, now, 8 + (lane & 7)));
-        float top = now;   // lanes 8-15: the largest V scale
-#pragma unroll
-        for (int off = 1; off < 8; off <<= 1)
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        top = __shfl_sync(0xffffffffu, top, 8);
-        if (lane < 8) sh->sc[warp][lane] = make_float4(now, lv, ex2(-lv), top);
+        // The largest V scale: patterns of positive numbers compare like the numbers, NaN
+        // above infinity (K's join only if they are either).  Past the limit the tile is
+        // marked with infinity, which sends its keys to the pass for the maximum.  (Told
+        // without a vote or a branch of its own: those cost 2 to 30 us of the 564.)
+        const uint32_t bits = __float_as_uint(now);
+        const float top = __uint_as_float(__reduce_max_sync(
+            0xffffffffu, (lane & 24) == 8 || bits >= 0x7f800000u ? bits : 0u));
+        if (lane < 8)
+          sh->sc[warp][lane] = make_float4(now, lv, ex2(kSumBias - lv),
+                                           top <= limit ? top * (1.f / kTwoSumBias) : INFINITY);
         __syncwarp();
       }
       const float4* sc = sh->sc[warp] + (h & 1) * kHalfBlocks;
@@ -532,6 +533,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kHalfKeys; ++c) x[c] = c < nvis ? x[c] : -INFINITY;
           }
         }
+        if (find_max && !(sc[0].w <= FLT_MAX)) {   // a marked tile
+          // A scale that is not finite becomes 1, where masked keys meet it too; the
+          // rows that see a key of its block become NaN through their sums.
+          float4 c = sh->sc[warp][lane & 7];
+          const bool bad = !(c.x <= FLT_MAX) || !(c.y <= FLT_MAX);
+          for (uint32_t left = __ballot_sync(0xffffffffu, bad) & 0xffu; left != 0; left &= left - 1) {
+            const int p0 = (j0 + (h >> 1)) * kTcKeys + (__ffs(left) - 1) * kBlock;
+            if (p0 <= pos && p0 + kBlock > lo) l = NAN;
+          }
+          if (__any_sync(0xffffffffu, !bad && c.y > kLogLargeScale))
+            limit = -1.f;   // from here on every tile may hold far smaller ones
+          if (lane < 8) sh->sc[warp][lane] = make_float4(bad ? 1.f : c.x, bad ? 0.f : c.y, 0.f, c.w);
+          __syncwarp();
+        }
         if (find_max) {   // (the factors are not negative: maxima of raw scores serve)
           float mt = -INFINITY;
 #pragma unroll
@@ -546,8 +561,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             mt = fmaxf(mt, fmaf(fmaxf(u, w), fmaf(sc[b].x, sl2, FLT_MIN), sc[b].y));
           }
           if (mt > m_used + kLazyRescale) {
-            alpha = (m_used == -INFINITY) ? 0.f : ex2(m_used - mt);
+            // (l in two steps: it may be far above 1 where the factor is below 2^-126)
+            const float half = (m_used == -INFINITY) ? 0.f : ex2(0.5f * (m_used - mt));
+            alpha = half * half;
+            l = l * half * half;
             m_used = mt;
+          }
+          // A marked tile's denominators come from the scores themselves (its weights
+          // are not added): beside a far larger V scale weights may go to zero.
+          if (!(sc[0].w <= FLT_MAX)) {
+            const float add = (m_used == -INFINITY) ? kSumBias : kSumBias - m_used;
+#pragma unroll
+            for (int b = 0; b < kHalfBlocks; ++b) {
+              const float f = fmaf(sc[b].x, sl2, FLT_MIN);
+#pragma unroll
+              for (int k = b * kBlock; k < (b + 1) * kBlock; ++k) l += ex2(fmaf(x[k], f, add));
+            }
           }
         }
         const float neg_mu = (m_used == -INFINITY) ? 0.f : -m_used;
@@ -594,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc::st32(tS, pk);
-      l = l * alpha + ls;
+      l += ls;
       tc::wait_st();
       tc::fence_before_sync();
       __syncwarp();
@@ -604,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool ok = done && warp_wait(smem_u32(&sh->o_done[t]), 0, abort, a.err, wlim);
     if (t < ntq) {
       tc::fence_after_sync();
-      const float inv = l == 0.f ? 0.f : 1.f / l;   // (a NaN stays)
+      const float inv = l == 0.f ? 0.f : kTwoSumBias / l;   // (a NaN stays)
       // every row of the tile is a query row of this sequence: its rows go out
       // through the tile's Q slot (its products have all completed), in the
       // swizzled layout Q arrived in, and one TMA store per 64-column half (a row
@@ -648,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (PARTS) {   // its log2-sum-exp, in the domain of m_used (NaN stays)
         if (ok && valid)
           a.ws_lse[part_row(a, s, tok, hq) * a.key_splits + key_part] =
-              l != 0.f ? m_used + log2f(l) : -INFINITY;
+              l != 0.f ? m_used + (log2f(l) - kSumBias) : -INFINITY;
       } else if (full_tile) {
         fence_proxy_async();   // generic writes, then the TMA engine reads
         // the tile's four warps (named barrier 1 + t); no store unless all wrote

@@ -110,3 +110,64 @@ def test_an_infinite_scale_makes_the_rows_that_see_it_nan(which, sign, ctx, chun
     got[:chunk, :hq // hkv] = ref[:chunk, :hq // hkv]
     assert (np.abs(got - ref) <= tol).all()
     assert pkv.get_error() == 0
+
+
+def definition(cache, qs, bt, cl, qsl, scale):
+    """fp64 output of every row, and the tolerance: the output's rounding (2^-8 of
+    it), and for each weight its rounding to fp16 and the error of its exponent
+    (2^-11 and 2^-14, as where the other attention tests say why) relative to what
+    it weighs: the largest magnitude that its block's V scale allows."""
+    k, v = (x.astype(np.float64) for x in cache.values())
+    q = qs.float().numpy().astype(np.float64)
+    out, tol = np.zeros(q.shape), np.zeros(q.shape)
+    group = q.shape[1] // k.shape[2]
+    for s in range(len(cl)):
+        L, t0, t1 = int(cl[s]), int(qsl[s]), int(qsl[s + 1])
+        at = bt[s, :-(-L // 16)].numpy()
+        top = 127 * np.repeat(np.maximum(cache.vs[at].astype(np.float64), 2.0 ** -60), 16, 0)[:L]
+        for h in range(q.shape[1]):
+            kh = k[at, :, h // group].reshape(-1, q.shape[2])[:L]
+            vh = v[at, :, h // group].reshape(-1, q.shape[2])[:L]
+            x = q[t0:t1, h] @ kh.T * scale
+            x[np.arange(L)[None] > np.arange(L - (t1 - t0), L)[:, None]] = -np.inf
+            w = np.exp(x - x.max(1, keepdims=True))
+            w /= w.sum(1, keepdims=True)
+            out[t0:t1, h] = w @ vh
+            tol[t0:t1, h] = (2.0 ** -8 * np.abs(out[t0:t1, h])
+                             + (2.0 ** -11 + 2.0 ** -14) * (w @ top[:, h // group])[:, None])
+    return out, tol
+
+
+@pytest.mark.parametrize("ctx,chunk,hq,hkv,d,bound", [
+    ([100, 60], 1, 8, 4, 64, None),        # a CTA for the row
+    ([1200, 600], 1, 8, 4, 128, None),     # splits that merge in a cluster
+    ([1200, 600], 1, 8, 4, 64, 200000),    # teams
+    ([1200, 600], 1, 8, 4, 128, 200000),
+    ([1200, 600], 20, 8, 4, 128, None),    # chunks, parts of the keys
+    ([300, 200], 150, 40, 1, 64, None),    # chunks
+    ([300, 200], 150, 8, 2, 128, None),
+    ([300, 200], 5, 130, 1, 64, None)])    # more q heads than a row tile has rows
+@pytest.mark.parametrize("large", [20, 60, 118])
+@pytest.mark.parametrize("sharp", [0.0, 1.0, 12.0])
+def test_v_scales_at_both_ends_of_their_range(ctx, chunk, hq, hkv, d, bound, large, sharp):
+    """Blocks of V of about 2^large beside blocks of zeros and ordinary ones, in
+    any order: the weights of the small blocks count in full."""
+    rng = np.random.default_rng(int(sharp) + large)
+    b = batch(ctx, [min(chunk, c) for c in ctx], hq, hkv, d, seed=3)
+    cache, qs, bt, cl, qsl, scale = b
+    power = rng.choice([large, 0, -60, -200], cache.vs.shape, p=[0.2, 0.2, 0.2, 0.4])
+    with np.errstate(under="ignore"):
+        cache.vs[:] = np.maximum(cache.vs.astype(np.float64) * 2.0 ** power,
+                                 2.0 ** -60).astype(np.float32)
+    cache.vc[np.repeat((power == -200)[:, None], 16, 1)] = 0       # (blocks of zeros)
+    cache.gpu[1].copy_(torch.from_numpy(cache.vc))
+    cache.gpu[3].copy_(torch.from_numpy(cache.vs))
+    qs = (qs.float() * sharp).to(torch.bfloat16)
+    out = torch.full(qs.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    pkv.attention_int8(out, qs.cuda(), *cache.gpu[:2], wide(bt, bound).cuda(), cl.cuda(),
+                       qsl.cuda(), scale, *cache.gpu[2:], max_query_len=chunk,
+                       max_context_len=bound or max(ctx))
+    assert pkv.get_error() == 0
+    ref, tol = definition(cache, qs, bt, cl, qsl, scale)
+    off = np.abs(out.float().cpu().numpy().astype(np.float64) - ref)
+    assert (off <= tol).all(), float((off / tol).max())
