@@ -120,11 +120,13 @@ class DecodeLoop:
 
     def resize(self, num_blocks: int) -> bool:
         """Changes the caches' size between steps: blocks in use move below the
-        new end, then the caches are reallocated.  False when they do not fit."""
+        new end, then the caches are replaced.  False when they do not fit.  The
+        new caches are had first: without memory for them nothing has changed."""
+        new = self._new_caches(max(num_blocks, 0))
         if not self.pool.resize(num_blocks):
             return False
         self._make_copies()
-        old, new = self.buffers(), self._new_caches(num_blocks)
+        old = self.buffers()
         n = min(num_blocks, old[0].shape[0])
         for a, b in zip(old, new):
             b[:n].copy_(a[:n])
