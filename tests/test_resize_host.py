@@ -1,5 +1,6 @@
 """DecodeLoop.resize on CPU, the kernel calls replaced by stand-ins: a resize
-whose new caches cannot be had changes nothing."""
+whose new caches cannot be had changes nothing, and the page copies of one that
+shrinks carry every request's rows along."""
 import numpy as np
 import pytest
 import torch
@@ -81,3 +82,27 @@ def test_a_resize_without_memory_then_steps(monkeypatch, _host_kernels):
         st = loop.step()
         assert int(st.slot_mapping.max()) < 30 * 16
         check_rows(loop)
+
+
+def test_shrinking_moves_blocks_in_use(_host_kernels):
+    """Short requests leave low blocks, long ones hold high ones: the caches are
+    made as small as the blocks in use allow."""
+    loop = loop_of(64, [(60, 3), (100, 3), (40, 40), (70, 40), (33, 40)])
+    moved = 0
+    for step in range(30):
+        loop.step()
+        check_rows(loop)
+        if step in (5, 15):
+            used = {b for r in loop.running for b in loop.pool.block_table(r.rid)}
+            del _host_kernels[:]
+            assert not loop.resize(len(used))          # (the null block needs one, too)
+            assert not _host_kernels
+            n = len(used) + 1
+            high = [b for b in used if b >= n]
+            assert loop.resize(n) and loop.k_cache.shape[0] == n
+            assert sorted(a for a, _ in _host_kernels) == sorted(high)
+            moved += len(high)
+            check_rows(loop)
+            assert loop.resize(64)
+            check_rows(loop)
+    assert moved >= 3
