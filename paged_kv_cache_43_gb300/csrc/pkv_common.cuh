@@ -128,9 +128,12 @@ __device__ __forceinline__ float int8_scale(float s) {
 // The V scales lv (log2) that one row sees span [-60, 121].  Its exponent reference m
 // follows the largest x + lv, so the terms 2^(x - m) of its denominator lie about
 // 2^-lv: the sums are held times 2^kSumBias, which leaves 2^20 keys their bits at
-// either end.  The terms are formed from x itself: a weight 2^(x + lv - m) goes to
-// zero where lv is far below the largest, although its term may count.
+// either end.  A weight 2^(x + lv - m) goes to zero where lv is far below the largest,
+// although its term may count: the terms are formed from x itself, or, while the V
+// scales are within kNearScales of one another, as weight / scale (which loses less
+// than 2^-54 of the sum a key).
 constexpr float kSumBias = 30.f, kTwoSumBias = 0x1p30f;
+constexpr float kNearScales = 0x1p64f;
 
 // ---- thread-block clusters: a barrier over the cluster's threads that have not
 // exited (shared-memory writes before it are visible to the others after it),

@@ -360,7 +360,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
   // Int8: the same step with the block's scales.  The weight that meets the V
   // codes is w = 2^(x + log2 sv - m), m following the largest x + log2 sv: w in
   // fp16 is at most 2^8 and exact to 2^-11 of the numerator's largest terms
-  // whatever the scales' sizes; the denominator adds 2^(x - m), in fp32.
+  // whatever the scales' sizes; the denominator adds w / sv, in fp32 and before
+  // the rounding, or, with a V scale above 16 among the warp's (apart: they may differ
+  // by more than kNearScales), 2^(x - m) itself (always doing so took 2 % longer:
+  // 16 sequences of 8K to 16K keys, 10 q / 5 kv heads, 72.6 - 74.2 us).
+  bool apart = false;
   auto softmax_step_i8 = [&](const float (&sc)[4], int i, int p0, uint32_t& pb0, uint32_t& pb1) {
     const float ks = __shfl_sync(0xffffffffu, my_ks, i);
     const float lv = __shfl_sync(0xffffffffu, my_lv, i);
@@ -402,13 +406,22 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
     const float mu1 = m[1] == -INFINITY ? 0.f : m[1];
     const float w0 = ex2(y[0] - mu0), w1 = ex2(y[1] - mu1);
     const float w2 = ex2(y[2] - mu0), w3 = ex2(y[3] - mu1);
-    const float d0 = kSumBias - lv - mu0, d1 = kSumBias - lv - mu1;
-    l[0] += ex2(y[0] + d0) + ex2(y[2] + d0);
-    l[1] += ex2(y[1] + d1) + ex2(y[3] + d1);
+    if (apart) {   // (warp-uniform)
+      const float d0 = kSumBias - lv - mu0, d1 = kSumBias - lv - mu1;
+      l[0] += ex2(y[0] + d0) + ex2(y[2] + d0);
+      l[1] += ex2(y[1] + d1) + ex2(y[3] + d1);
+    } else {
+      const float ivs = ex2(kSumBias - lv);
+      l[0] = fmaf(w0 + w2, ivs, l[0]);
+      l[1] = fmaf(w1 + w3, ivs, l[1]);
+    }
     pb0 = movmatrix_trans(pack_f16(w0, w1));
     pb1 = movmatrix_trans(pack_f16(w2, w3));
   };
-  if constexpr (I8) my_lv = log2f(my_lv == 0.f ? 1.f : my_lv);   // (0: no block)
+  if constexpr (I8) {
+    apart = __any_sync(0xffffffffu, my_lv > kInt8ScaleFloor * kNearScales);
+    my_lv = log2f(my_lv == 0.f ? 1.f : my_lv);   // (0: no block)
+  }
 
   // FP8: this lane's fragment offsets inside a block's code tiles (the same
   // for every block): K rows r0, r0 + 8 at chunks (D/64) t + c; V rows 2t,
@@ -600,26 +613,18 @@ __global__ void __launch_bounds__(kDecodeWarps * 32)
     float den = 0.f;
     float f[NW];
     if constexpr (I8) {
-      // The warps' sums m + log2 l, relative to M, against the largest of them E (m
-      // alone follows the numerators: where their V scales differ, so do the sums).
-      // A NaN stays one (the combine makes it of an infinite lse).
-      if (M == -INFINITY) M = 0.f;   // (no key, or NaN scores only)
-      float E = -INFINITY;
+      // (in two steps: a sum may be far above 1 where its factor is below 2^-126.  A
+      // NaN stays one; the combine makes it of an infinite lse.)
       for (int w = 0; w < NW; ++w) {
         const float* ww = merge_area(w);
-        const float l_w = ww[8 * D + 8 + c];
-        f[w] = l_w == 0.f ? -INFINITY : ww[8 * D + c] - M + log2f(l_w);
-        E = fmaxf(E, f[w]);
+        const float half = M == -INFINITY ? 0.f : exp2f(0.5f * (ww[8 * D + c] - M));
+        f[w] = half * half;
+        den += ww[8 * D + 8 + c] * half * half;
       }
-      for (int w = 0; w < NW; ++w) {
-        const bool none = f[w] == -INFINITY;
-        den += none ? 0.f : exp2f(f[w] - E);
-        f[w] = none ? 0.f : exp2f(merge_area(w)[8 * D + c] - M - E);
-      }
-      for (int w = 0; w < NW; ++w)
-        merge_f[w * 8 + c] = f[w] == 0.f ? 0.f : f[w] * (kTwoSumBias / den);
+      const float inv = kTwoSumBias / den;
+      for (int w = 0; w < NW; ++w) merge_f[w * 8 + c] = den == 0.f ? 0.f : f[w] * inv;
       merge_f[NW * 8 + c] =
-          den == 0.f ? -INFINITY : (den > 0.f ? M + (E + log2f(den) - kSumBias) : INFINITY);
+          den == 0.f ? -INFINITY : (den > 0.f ? M + (log2f(den) - kSumBias) : INFINITY);
     } else {
       for (int w = 0; w < NW; ++w) {
         const float* ww = merge_area(w);

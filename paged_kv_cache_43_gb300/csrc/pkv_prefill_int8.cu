@@ -7,8 +7,8 @@
 // fp16, a row of Q is scaled by a power of two into its range.  P = 2^(x + log2
 // sv - m): a block's V scale rides in the softmax exponent, and m follows the
 // largest x + log2 sv, so P in fp16 is at most 2^15 whatever the scales are;
-// the row sum divides sv out again (per block, in fp32; from the first V scale
-// above kLargeScale on it is formed without it).  Both scales cost
+// the row sum divides sv out again (per block, in fp32; where V scales
+// differ by 2^64 and more it is formed without it).  Both scales cost
 // nothing per element: they are the factor and the addend of the exponent's one
 // FMA.  Every code is finite, so rows no key may see need no zeroing.
 //
@@ -56,10 +56,6 @@ constexpr int kHalfBlocks = kHalfKeys / kBlock;
 constexpr int kRegsSoftmax = 168;
 constexpr int kRegsOther = 88;
 static_assert(2 * 128 * (kRegsSoftmax + kRegsOther) <= kThreads * 128, "register split");
-// V scales up to this are within 2^64 of the smallest: dividing them out of the weights
-// loses less than 2^-54 of the row sum a key.
-constexpr float kLogLargeScale = 4.f, kLargeScale = kInt8ScaleFloor * 0x1p64f;
-static_assert(kLargeScale == 16.f, "2^kLogLargeScale");
 
 // TMEM columns: S of tile t, half step h at 128t + 64 (h % 2), P over its first
 // 32; O of tile t at 256 + 128t.
@@ -468,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(q_conv);
     float m_used = -INFINITY, l = 0.f;
-    float limit = kLargeScale;   // V scales above it mark their tile
+    float low = kInt8ScaleFloor;   // a V scale outside [low, low * kNearScales] marks its tile
     bool done = t < ntq;
     const int lo = a.window > 0 ? pos - a.window + 1 : 0;   // first key this row sees
     for (int h = 0; done && h < H; ++h) {
@@ -478,16 +474,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         scale_next = scale_of(id_next);
         id_next = id_of((h >> 1) + 2);
         const float lv = log2f(__shfl_sync(0xffffffffu, now, 8 + (lane & 7)));
-        // The largest V scale: patterns of positive numbers compare like the numbers, NaN
-        // above infinity (K's join only if they are either).  Past the limit the tile is
-        // marked with infinity, which sends its keys to the pass for the maximum.  (Told
-        // without a vote or a branch of its own: those cost 2 to 30 us of the 564.)
-        const uint32_t bits = __float_as_uint(now);
-        const float top = __uint_as_float(__reduce_max_sync(
-            0xffffffffu, (lane & 24) == 8 || bits >= 0x7f800000u ? bits : 0u));
+        // The largest V scale: patterns of positive numbers compare like the numbers.  A V
+        // scale out of range and a K scale that is not finite mark the tile with
+        // infinity, which sends its keys to the pass for the maximum.  (Told without a
+        // vote or a branch of its own: those cost 2 to 30 us of the 564.)
+        const bool is_v = (lane & 24) == 8;
+        const bool fine = is_v ? now >= low && now <= low * kNearScales : now <= FLT_MAX;
+        const uint32_t bits = !fine ? 0x7f800000u : (is_v ? __float_as_uint(now) : 0u);
+        const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, bits));
         if (lane < 8)
-          sh->sc[warp][lane] = make_float4(now, lv, ex2(kSumBias - lv),
-                                           top <= limit ? top * (1.f / kTwoSumBias) : INFINITY);
+          sh->sc[warp][lane] =
+              make_float4(now, lv, ex2(kSumBias - lv), top * (1.f / kTwoSumBias));
         __syncwarp();
       }
       const float4* sc = sh->sc[warp] + (h & 1) * kHalfBlocks;
@@ -542,8 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int p0 = (j0 + (h >> 1)) * kTcKeys + (__ffs(left) - 1) * kBlock;
             if (p0 <= pos && p0 + kBlock > lo) l = NAN;
           }
-          if (__any_sync(0xffffffffu, !bad && c.y > kLogLargeScale))
-            limit = -1.f;   // from here on every tile may hold far smaller ones
+          // a V scale above the range moves it, to 2^16 above that scale
+          const float up = bad ? 0.f : ex2(c.y + 16.f - 64.f);
+          const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(up)));
+          if (most > low * 0x1p16f) low = most;
           if (lane < 8) sh->sc[warp][lane] = make_float4(bad ? 1.f : c.x, bad ? 0.f : c.y, 0.f, c.w);
           __syncwarp();
         }
@@ -568,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             m_used = mt;
           }
           // A marked tile's denominators come from the scores themselves (its weights
-          // are not added): beside a far larger V scale weights may go to zero.
+          // are not added): beside a far larger V scale weights go to zero.
           if (!(sc[0].w <= FLT_MAX)) {
             const float add = (m_used == -INFINITY) ? kSumBias : kSumBias - m_used;
 #pragma unroll
