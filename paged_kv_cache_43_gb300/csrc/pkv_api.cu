@@ -999,6 +999,11 @@ constexpr int kTeamRangeBlocks = 32;
 // 1000 8.6 - 6.5 - 7.2, of 2000 11.9 - 8.2 - 7.9, of 4000 13.2 - 10.8 - 9.7, of 8000
 // 15.0 - 16.6 - 13.2, of 16000 19.6 - 26 - 20.4; 4 of 1000 10.2 - 7.9 - 8.3; 8 of 6000
 // 25.6 - 23.3 - 23.6.
+// Only where the GPU holds all the launch's CTAs at a time: past that a cluster waits
+// for room for all of it.  Workspace - clusters: 32 sequences of 1K to 3K keys, 32 / 8
+// heads of 128 (768 CTAs) 37.5 - 47, of 64 27.3 - 32.6; 16 of 8K to 16K, 10 / 5 (1280 CTAs)
+// 58 - 73; below 32 of 1K to 3K, 10 / 5, 30.0 - 27.7.
+constexpr int kDecodeCtasPerSm = 4;
 constexpr int kOneSplitBlocks = 8;
 constexpr int kSmallClusterBlocks = 96;
 constexpr int kClusterBlocks = 1024;
@@ -1048,11 +1053,19 @@ int make_int8_decode_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int n
   // beside chunk rows, whose CTAs rarely leave a cluster its SMs at one time: 16 rows
   // of 1K to 8K keys and 2 x 1024 tokens 156 us, 179 with clusters)
   const bool may = m->kv_split_tokens == 0 && p->split.num_decode == m->num_seqs;
-  if (may && p->split.max_splits > most && split_span <= kClusterBlocks) {
-    p->split.split_blocks = (split_span + most - 1) / most;
-    p->split.max_splits = (split_span + p->split.split_blocks - 1) / p->split.split_blocks;
+  int blocks_each = p->split.split_blocks, splits = p->split.max_splits;
+  if (splits > most && split_span <= kClusterBlocks) {
+    blocks_each = (split_span + most - 1) / most;
+    splits = (split_span + blocks_each - 1) / blocks_each;
   }
-  p->cluster = may && p->split.max_splits > 1 && p->split.max_splits <= kDecodeCluster;
+  const int64_t rows = static_cast<int64_t>(p->split.num_decode) * c->num_kv_heads *
+                       ((m->num_q_heads / c->num_kv_heads + 7) / 8);
+  p->cluster = may && splits > 1 && splits <= kDecodeCluster &&
+               rows * splits <= static_cast<int64_t>(kDecodeCtasPerSm) * num_sms;
+  if (p->cluster) {
+    p->split.split_blocks = blocks_each;
+    p->split.max_splits = splits;
+  }
   if (p->cluster || p->split.max_splits <= 1) p->split.ws_o_bytes = p->split.ws_bytes = 0;
   p->decode_bytes = p->split.ws_bytes;
   const int nd = p->split.num_decode;

@@ -1,8 +1,8 @@
 """Int8 decode by the kernel that a batch takes, told from the workspace it asks
 for: an all-decode batch of contexts up to 16384 keys takes clusters of its rows'
-splits (no workspace), or, where the blocks by max_context_len are enough for
-every team, the team kernel (partials in a workspace).  Windows, NaN, graph
-captures and waits that run out reach both."""
+splits (no workspace) if the GPU holds them all at a time, or, where the blocks by
+max_context_len are enough for every team, the team kernel (partials in a
+workspace).  Windows, NaN, graph captures and waits that run out reach both."""
 import numpy as np
 import pytest
 import torch
@@ -75,6 +75,20 @@ def test_no_window_on_the_team_kernel_of_many_ragged_sequences():
         b = ready(ctx.tolist(), hq, hkv, d, seed=hq)
         assert workspace(b, bound=6000) > 0
         check_attention(*b, max_context_len=6000)
+
+
+@pytest.mark.parametrize("seqs,lo,hi,hq,hkv,clusters", [
+    (16, 8000, 16000, 10, 5, False), (7, 8000, 16000, 10, 5, True), (32, 1000, 3000, 32, 8, False),
+    (8, 1000, 3000, 32, 8, True), (8, 1000, 3000, 130, 1, True)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_clusters_only_where_the_gpu_holds_them_all(seqs, lo, hi, hq, hkv, clusters, d):
+    """Middle batches with splits that would not all be resident as clusters merge
+    through a workspace."""
+    ctx = np.random.default_rng(seqs).integers(lo, hi + 1, seqs).tolist()
+    b = ready(ctx, hq, hkv, d, seed=seqs)
+    assert (workspace(b) == 0) == clusters
+    check_attention(*b)
+    check_attention(*b, window=700)
 
 
 # -------------------------------------------------------------------- NaN
