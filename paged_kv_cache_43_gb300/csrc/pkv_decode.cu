@@ -33,7 +33,8 @@
 //    registers; int8's K scale multiplies a block's scores and the log of its V
 //    scale joins the exponent.  Int8's splits of a row are a cluster that merges
 //    its partials through shared memory (make_int8_decode_plan has the rule).  8 kv
-//    heads of 128: 1 sequence of 100 keys 5.3 us, of 4000 9.7; 16 of 300 7.7.
+//    heads of 128: 1 sequence of 100 keys 5.1 us, of 4000 9.5; 16 of 300 7.6; of 64:
+//    1 of 4000 7.6.
 #include <type_traits>
 
 #include "pkv_common.cuh"

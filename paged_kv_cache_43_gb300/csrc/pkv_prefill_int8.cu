@@ -30,7 +30,7 @@
 // issuing a half step's products of one tile 0.5: with fewer warps for them (one
 // to start all, two to widen all, one to issue all) those bound the step.
 // Measured, 4 x 2048 tokens over 2K to 8K keys (32 q / 8 kv heads, head_size 128):
-// 561 us, 1085 TFLOP/s, 0.57 of the measured bf16 peak (the first form, products of
+// 564 us, 1080 TFLOP/s, 0.56 of the measured bf16 peak (the first form, products of
 // 128 keys as in pkv_prefill_tc.cu: 737).  A step of 128 keys takes 2.1 us, of
 // which the tensor core's reads of shared memory 1.2; an SM is idle or filling
 // for 11 us of each CTA (launch and work choice 2.7, the first K landing, widened
