@@ -56,9 +56,9 @@ def poison(cache, which, block, head, value):
                                             (32, 2, 64, 9000), (260, 2, 64, None)])
 def test_a_bad_scale_reaches_no_row_that_does_not_see_its_block(which, value, window, hq, hkv, d,
                                                                 bound):
-    """Chunks whose rows see different blocks: a scale that is NaN makes the rows
-    that see a key of its block NaN (an infinite one does so at least where a
-    score is not negative), and leaves the others as they are."""
+    """Chunks whose rows see different blocks: a scale that is NaN or infinite
+    makes the rows that see a key of its block NaN, and leaves the others as they
+    are."""
     q, ctx = [64, 100], [64, 333]
     b = batch(ctx, q, hq, hkv, d, seed=hq + d)
     cache, qs, bt, cl, qsl, scale = b
@@ -77,8 +77,7 @@ def test_a_bad_scale_reaches_no_row_that_does_not_see_its_block(which, value, wi
         mine = np.zeros(got.shape[:2], bool)
         mine[sees, group:] = True
         assert mine.any() and not mine.all()
-        if np.isnan(value):
-            assert np.isnan(got[mine]).all()
+        assert np.isnan(got[mine]).all()
         bad = ~(np.abs(got - ref) <= tol)
         assert not bad[~mine].any(), (s, j, np.argwhere(bad.any(-1) & ~mine)[:4])
     assert pkv.get_error() == 0
