@@ -77,6 +77,10 @@ extern "C" {
 #define PKV_ERR_TIMEOUT (1 << 5)     /* an on-chip wait gave up (bounded spin)   */
 #define PKV_ERR_NONFINITE (1 << 6)   /* pkv_write_int8: an infinity or NaN in k  */
                                      /* or v                                     */
+#define PKV_ERR_POSITION (1 << 7)    /* pkv_rope*: a position outside            */
+                                     /* [0, max_position)                        */
+#define PKV_ERR_ACCEPTED (1 << 8)    /* pkv_accept_drafts: a count or path that  */
+                                     /* does not fit the drafts                  */
 
 typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_FP8_E4M3 = 2, PKV_INT8 = 3 } pkv_dtype;
 
@@ -366,6 +370,126 @@ int pkv_attention_int8(void *out, const void *q, const void *k_cache, const void
  * was captured with. */
 int pkv_copy_blocks(void *const *buffers, const int64_t *page_bytes, int32_t num_buffers,
                     int32_t num_blocks, const int32_t *pairs, int32_t num_pairs, void *stream);
+
+/* ---- Steps with drafted tokens (speculative decoding); no counterpart in the
+ * pages.  A step writes a sequence's drafted tokens behind its keys
+ * (pkv_rope_write: their positions come from their depth in the tree, their
+ * slots from the pool), attends from all of them at once (pkv_attention_tree)
+ * and, once the model's outputs say which path is right, keeps that path's rows
+ * (pkv_accept_drafts).
+ *
+ * The pass between the QKV projection and attention, for any step. */
+typedef struct {
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_size;             /* 64 or 128                                     */
+  int32_t dtype;                 /* PKV_BF16 or PKV_F32: q, k, v, q_out, weights  */
+  int32_t rot_dim;               /* rotated elements of a head, even, 0..head_size */
+  int32_t max_position;          /* rows of cos_sin                               */
+  int32_t interleaved;           /* 0: pairs (i, i + rot_dim / 2); 1: (2i, 2i + 1) */
+  int64_t q_stride;              /* elements from a token's rows to the next      */
+  int64_t k_stride;              /* token's (slices of one projection's output    */
+  int64_t v_stride;              /* as they are): at least heads * head_size, a   */
+  int64_t q_out_stride;          /* multiple of 16 bytes                          */
+  int64_t k_out_stride;          /* (pkv_rope only)                               */
+  float eps;
+} pkv_rope_desc;
+
+/* For every token t with slot = slot_mapping[t] >= 0: each query head's and key
+ * head's row x is normalised where its weight is given, y = x * w / sqrt(mean(x^2)
+ * + eps), the first rot_dim elements of y are rotated by the angle at row
+ * positions[t] of cos_sin, (a, b) -> (a cos - b sin, b cos + a sin) for each
+ * pair, and the result goes to q_out, or as pkv_write does to row `slot` of
+ * k_cache; v goes to v_cache unchanged.  fp32 arithmetic, rounded once.
+ *   q_out, q       [num_tokens, num_q_heads, head_size], token strides as described;
+ *                  q_out may be q itself (same stride), else overlaps no input
+ *   k, v           [num_tokens, num_kv_heads, head_size], likewise
+ *   positions      int64 [num_tokens]
+ *   cos_sin        fp32 [max_position, rot_dim]: rot_dim / 2 cosines, then as many
+ *                  sines (may be NULL when rot_dim is 0)
+ *   q_weight, k_weight  [head_size], rope->dtype, or NULL: no norm
+ *   slot_mapping   int64 [num_tokens]; two tokens with the same slot: either row
+ * Skipped whole, their rows of q_out left as they are: tokens with a slot < 0,
+ * with a slot past the cache (PKV_ERR_SLOT) or with a position outside
+ * [0, max_position) (PKV_ERR_POSITION).  cache->dtype must be rope->dtype. */
+int pkv_rope_write(void *q_out, const void *q, const void *k, const void *v,
+                   const int64_t *positions, const float *cos_sin, const void *q_weight,
+                   const void *k_weight, const int64_t *slot_mapping, void *k_cache,
+                   void *v_cache, const pkv_rope_desc *rope, const pkv_cache_desc *cache,
+                   void *stream);
+/* The same into e4m3 caches: codes of value / k_scale[h] and v / v_scale[h] as
+ * pkv_write_fp8 makes them, of the fp32 value (rope->dtype PKV_BF16). */
+int pkv_rope_write_fp8(void *q_out, const void *q, const void *k, const void *v,
+                       const int64_t *positions, const float *cos_sin, const void *q_weight,
+                       const void *k_weight, const int64_t *slot_mapping, void *k_cache,
+                       void *v_cache, const float *k_scale, const float *v_scale,
+                       const pkv_rope_desc *rope, const pkv_cache_desc *cache, void *stream);
+/* The rows alone, k's to k_out [num_tokens, num_kv_heads, head_size] (which may be
+ * k itself, same stride): for an int8 cache, whose write (pkv_write_int8) makes
+ * scales of whole blocks.  Every token with a position in range is computed. */
+int pkv_rope(void *q_out, void *k_out, const void *q, const void *k, const int64_t *positions,
+             const float *cos_sin, const void *q_weight, const void *k_weight,
+             const pkv_rope_desc *rope, void *stream);
+
+/* Attention of a tree of drafted tokens: as pkv_attention (arguments, layouts,
+ * errors, rows left alone), but sequence s with L keys and n query rows sees,
+ * from row i, the keys 0 .. L - n - 1 and those keys L - n + j, j < n, whose bit
+ * j of row i's mask is set (its ancestors and itself; any set of bits is
+ * allowed).  A row that sees no key is zero.  What a key's K and V hold reaches
+ * only the rows that see it, NaN and infinities too.
+ *   tree_mask  int64 [num_tokens, ceil(max_query_len / 64)]: bit j % 64 of word
+ *              j / 64; bits from n on are ignored
+ * Every sequence is taken alike (num_decode_seqs is ignored); sliding_window
+ * must be 0 (PKV_E_META).  A sequence longer than max_query_len or
+ * max_context_len: its bit of pkv_attention, its first max_query_len rows zero.
+ * num_seqs is 65535 at most, and so are num_kv_heads x the tiles of 32
+ * (row, head) pairs that max_query_len rows make (PKV_E_SHAPE).  Int8 caches are
+ * not taken: keeping some of a block's drafted rows would leave it with a scale
+ * that its dropped rows made.  Workspace: scratch of one call, size from the
+ * function below; calls that may overlap, captured graphs included, need one
+ * each. */
+size_t pkv_attention_tree_workspace_size(const pkv_cache_desc *cache, const pkv_attn_meta *meta);
+int pkv_attention_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
+                       const int32_t *block_tables, const int32_t *context_lens,
+                       const int32_t *query_start_loc, const int64_t *tree_mask, float scale,
+                       const pkv_cache_desc *cache, const pkv_attn_meta *meta, void *workspace,
+                       size_t workspace_bytes, void *stream);
+/* The same over e4m3 caches, with the descales of pkv_attention_fp8. */
+int pkv_attention_tree_fp8(void *out, const void *q, const void *k_cache, const void *v_cache,
+                           const int32_t *block_tables, const int32_t *context_lens,
+                           const int32_t *query_start_loc, const int64_t *tree_mask, float scale,
+                           const float *k_descale, const float *v_descale,
+                           const pkv_cache_desc *cache, const pkv_attn_meta *meta, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* Keeps an accepted path of each sequence's drafts: of the n = query_start_loc[s + 1] -
+ * query_start_loc[s] drafted rows at the end of its L = context_lens[s] keys, row
+ * L - n + accepted[s][j] moves to L - n + j for j < num_accepted[s], in every buffer
+ * (as if all were read before the first is written).  Rows behind them are left as
+ * they are.  Everything is read on the device: no host synchronisation between the
+ * model's choice and the next step.
+ *   buffers, row_bytes  HOST arrays [num_buffers]; buffer i is [num_blocks, 16,
+ *                       row_bytes[i]]: a layer's K or V cache (not of an int8 cache,
+ *                       whose scales belong to whole blocks); 4-byte aligned, a
+ *                       multiple of 4 bytes a row, 2^26 at most (16-byte alignment of
+ *                       both is the fast case).  The buffers do not overlap
+ *   accepted            int32 [num_seqs, max_accepted]: rising drafts, 0 <= accepted[s][0]
+ *                       < accepted[s][1] < ... < n; entries from num_accepted[s] on
+ *                       are not read
+ *   num_accepted        int32 [num_seqs], 0 .. min(n, max_accepted)
+ *   new_context_lens    int32 [num_seqs] or NULL: becomes L - n + num_accepted[s]; it
+ *                       must not overlap context_lens (PKV_E_META)
+ * Sequences with bad lengths (PKV_ERR_QUERY_LEN, PKV_ERR_CONTEXT_LEN) or a bad path
+ * (PKV_ERR_ACCEPTED) are left alone, their new length is L; a row whose block id is
+ * bad is not moved (PKV_ERR_BLOCK_ID).  Drafted rows of two sequences in the same
+ * block: unspecified. */
+int pkv_accept_drafts(void *const *buffers, const int64_t *row_bytes, int32_t num_buffers,
+                      int32_t num_blocks, const int32_t *block_tables,
+                      int32_t block_table_stride, const int32_t *context_lens,
+                      const int32_t *query_start_loc, int32_t num_seqs, const int32_t *accepted,
+                      const int32_t *num_accepted, int32_t max_accepted,
+                      int32_t *new_context_lens, void *stream);
 
 /* Reads (and, if clear != 0, resets) the current device's error word: the OR
  * of PKV_ERR_* bits raised by kernels since the last clear.  SYNCHRONISES the

@@ -1477,6 +1477,328 @@ extern "C" int pkv_copy_blocks(void* const* buffers, const int64_t* page_bytes,
   return a.num_pairs > 0 ? flush() : PKV_OK;
 }
 
+// ------------------------------------- steps with drafted tokens: rotation and write
+
+namespace pkv {
+namespace {
+
+int check_rope(const pkv_rope_desc* d) {
+  if (d == nullptr) return PKV_E_NULL;
+  if (d->dtype != PKV_BF16 && d->dtype != PKV_F32) return PKV_E_DTYPE;
+  if (d->head_size != 64 && d->head_size != 128) return PKV_E_SHAPE;
+  if (d->num_tokens < 0 || d->num_q_heads < 1 || d->num_kv_heads < 1 ||
+      static_cast<int64_t>(d->num_q_heads) + 2 * static_cast<int64_t>(d->num_kv_heads) > 65535 ||
+      d->rot_dim < 0 || d->rot_dim > d->head_size || d->rot_dim % 2 != 0 || d->max_position < 0)
+    return PKV_E_SHAPE;
+  return PKV_OK;
+}
+
+// Rows of `heads` heads, `stride` elements from one token to the next: rows apart, each
+// begins on 16 bytes.
+int check_rows(const void* p, int64_t stride, int heads, const pkv_rope_desc& d) {
+  if (p == nullptr) return PKV_E_NULL;
+  const int64_t e = d.dtype == PKV_F32 ? 4 : 2;
+  if (stride < static_cast<int64_t>(heads) * d.head_size || stride > INT64_MAX / 16) return PKV_E_SHAPE;
+  return aligned16(p) && stride * e % 16 == 0 ? PKV_OK : PKV_E_ALIGN;
+}
+
+// What the three calls share; v, slots and the caches are null for rows alone.
+int rope_impl(void* q_out, void* k_out, const void* q, const void* k, const void* v,
+              const int64_t* positions, const float* cos_sin, const void* q_weight,
+              const void* k_weight, const int64_t* slot_mapping, void* k_cache, void* v_cache,
+              const float* k_scale, const float* v_scale, const pkv_rope_desc* rope,
+              const pkv_cache_desc* cache, void* stream) {
+  if (int st = check_rope(rope)) return st;
+  const pkv_rope_desc& d = *rope;
+  if (cache != nullptr && (cache->num_kv_heads != d.num_kv_heads || cache->head_size != d.head_size))
+    return PKV_E_SHAPE;
+  if (d.num_tokens == 0) return PKV_OK;
+  if (!positions || (!cos_sin && d.rot_dim > 0)) return PKV_E_NULL;
+  if (int st = check_rows(q, d.q_stride, d.num_q_heads, d)) return st;
+  if (int st = check_rows(k, d.k_stride, d.num_kv_heads, d)) return st;
+  if (int st = check_rows(q_out, d.q_out_stride, d.num_q_heads, d)) return st;
+  if (cache != nullptr) {
+    if (int st = check_rows(v, d.v_stride, d.num_kv_heads, d)) return st;
+    if (!slot_mapping || !k_cache || !v_cache) return PKV_E_NULL;
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_E_ALIGN;
+  } else if (int st = check_rows(k_out, d.k_out_stride, d.num_kv_heads, d)) {
+    return st;
+  }
+  if ((reinterpret_cast<uintptr_t>(positions) & 7u) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) ||
+      !aligned4(cos_sin) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned4(k_scale) ||
+      !aligned4(v_scale))
+    return PKV_E_ALIGN;
+  RopeArgs a{};
+  int sms;
+  if (int st = device_state(&a.err, &sms)) return st;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.slot_mapping = slot_mapping;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  if (cache != nullptr) a.num_slots = static_cast<int64_t>(cache->num_blocks) * cache->block_size;
+  a.q_stride = d.q_stride;
+  a.k_stride = d.k_stride;
+  a.v_stride = d.v_stride;
+  a.q_out_stride = d.q_out_stride;
+  a.k_out_stride = d.k_out_stride;
+  a.num_tokens = d.num_tokens;
+  a.num_q_heads = d.num_q_heads;
+  a.num_kv_heads = d.num_kv_heads;
+  a.max_position = d.max_position;
+  a.rot_dim = d.rot_dim;
+  a.interleaved = d.interleaved != 0;
+  a.eps = d.eps;
+  PKV_TRY(launch_rope(a, d.head_size, d.dtype == PKV_F32, k_scale != nullptr, as_stream(stream)));
+  return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" int pkv_rope_write(void* q_out, const void* q, const void* k, const void* v,
+                              const int64_t* positions, const float* cos_sin,
+                              const void* q_weight, const void* k_weight,
+                              const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                              const pkv_rope_desc* rope, const pkv_cache_desc* cache,
+                              void* stream) {
+  if (int st = check_cache(cache)) return st;
+  if (rope == nullptr) return PKV_E_NULL;
+  if (cache->dtype != rope->dtype) return PKV_E_DTYPE;   // (e4m3: pkv_rope_write_fp8)
+  return rope_impl(q_out, nullptr, q, k, v, positions, cos_sin, q_weight, k_weight, slot_mapping,
+                   k_cache, v_cache, nullptr, nullptr, rope, cache, stream);
+}
+
+extern "C" int pkv_rope_write_fp8(void* q_out, const void* q, const void* k, const void* v,
+                                  const int64_t* positions, const float* cos_sin,
+                                  const void* q_weight, const void* k_weight,
+                                  const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                                  const float* k_scale, const float* v_scale,
+                                  const pkv_rope_desc* rope, const pkv_cache_desc* cache,
+                                  void* stream) {
+  if (int st = check_cache(cache)) return st;
+  if (rope == nullptr || !k_scale || !v_scale) return PKV_E_NULL;
+  if (cache->dtype != PKV_FP8_E4M3 || rope->dtype != PKV_BF16) return PKV_E_DTYPE;
+  return rope_impl(q_out, nullptr, q, k, v, positions, cos_sin, q_weight, k_weight, slot_mapping,
+                   k_cache, v_cache, k_scale, v_scale, rope, cache, stream);
+}
+
+extern "C" int pkv_rope(void* q_out, void* k_out, const void* q, const void* k,
+                        const int64_t* positions, const float* cos_sin, const void* q_weight,
+                        const void* k_weight, const pkv_rope_desc* rope, void* stream) {
+  return rope_impl(q_out, k_out, q, k, nullptr, positions, cos_sin, q_weight, k_weight, nullptr,
+                   nullptr, nullptr, nullptr, nullptr, rope, nullptr, stream);
+}
+
+// ------------------------------------- attention of a tree of drafted tokens
+
+namespace pkv {
+namespace {
+
+struct TreePlan {
+  int split_blocks = 0;
+  int max_splits = 0;
+  size_t ws_o_bytes = 0;
+  size_t ws_bytes = 0;
+};
+
+// Tiles of 32 (row, q head) pairs of one kv head, for the longest sequence.
+int64_t tree_tiles(const pkv_cache_desc& c, const pkv_attn_meta& m) {
+  return (static_cast<int64_t>(m.max_query_len) * (m.num_q_heads / c.num_kv_heads) + 31) / 32;
+}
+
+int check_tree(const pkv_cache_desc* c, const pkv_attn_meta* m) {
+  if (int st = check_cache(c)) return st;
+  if (int st = check_meta(c, m)) return st;
+  if (m->sliding_window != 0) return PKV_E_META;
+  if (m->num_seqs > 65535 || tree_tiles(*c, *m) * c->num_kv_heads > 65535)   // (the grid)
+    return PKV_E_SHAPE;
+  return PKV_OK;
+}
+
+void make_tree_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms, TreePlan* p) {
+  const int64_t tiles = tree_tiles(*c, *m);
+  *p = TreePlan{};
+  const int64_t blocks = std::max<int64_t>((static_cast<int64_t>(m->max_context_len) + kBlock - 1) / kBlock, 1);
+  const int64_t units = std::max<int64_t>(m->num_seqs * tiles * c->num_kv_heads, 1);
+  int64_t sb = m->kv_split_tokens / kBlock;
+  if (sb == 0) {
+    sb = 64;
+    while (sb > 4 && units * ((blocks + sb - 1) / sb) < 2 * num_sms) sb /= 2;
+  }
+  p->split_blocks = static_cast<int>(sb);
+  p->max_splits = static_cast<int>((blocks + sb - 1) / sb);
+  if (p->max_splits > 1) {
+    const size_t n = static_cast<size_t>(m->num_tokens) * m->num_q_heads * p->max_splits;
+    p->ws_o_bytes = round_up(n * c->head_size * sizeof(float), 256);
+    p->ws_bytes = p->ws_o_bytes + round_up(n * sizeof(float), 256);
+  }
+}
+
+int tree_impl(void* out, const void* q, const void* k_cache, const void* v_cache,
+              const int32_t* block_tables, const int32_t* context_lens,
+              const int32_t* query_start_loc, const int64_t* tree_mask, float scale,
+              const float* k_descale, const float* v_descale, const pkv_cache_desc* cache,
+              const pkv_attn_meta* meta, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int st = check_tree(cache, meta)) return st;
+  if (meta->num_seqs == 0 || meta->num_tokens == 0 || meta->max_query_len == 0) return PKV_OK;
+  if (cache->num_blocks == 0) return PKV_E_SHAPE;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start_loc ||
+      !tree_mask)
+    return PKV_E_NULL;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(query_start_loc) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+    return PKV_E_ALIGN;
+  int32_t* err;
+  int sms;
+  if (int st = device_state(&err, &sms)) return st;
+  TreePlan p;
+  make_tree_plan(cache, meta, sms, &p);
+  if (p.ws_bytes > 0) {
+    if (workspace == nullptr || workspace_bytes < p.ws_bytes) return PKV_E_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PKV_E_ALIGN;
+  }
+  TreeArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start_loc = query_start_loc;
+  a.tree_mask = reinterpret_cast<const uint64_t*>(tree_mask);
+  a.k_descale = k_descale;
+  a.v_descale = v_descale;
+  if (p.ws_bytes > 0) {
+    a.ws_o = static_cast<float*>(workspace);
+    a.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ws_o_bytes);
+  }
+  a.err = err;
+  a.bt_stride = meta->block_table_stride;
+  a.num_seqs = meta->num_seqs;
+  a.num_tokens = meta->num_tokens;
+  a.num_q_heads = meta->num_q_heads;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.group = meta->num_q_heads / cache->num_kv_heads;
+  a.num_blocks = cache->num_blocks;
+  a.max_query_len = meta->max_query_len;
+  a.max_context_len = meta->max_context_len;
+  a.mask_words = (meta->max_query_len + 63) / 64;
+  a.split_blocks = p.split_blocks;
+  a.max_splits = p.max_splits;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  const cudaStream_t st = as_stream(stream);
+  PKV_TRY(launch_tree(a, cache->dtype, cache->head_size, st));
+  if (p.max_splits > 1) PKV_TRY(launch_tree_merge(a, cache->dtype == PKV_F32, cache->head_size, st));
+  return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" size_t pkv_attention_tree_workspace_size(const pkv_cache_desc* cache,
+                                                    const pkv_attn_meta* meta) {
+  int32_t* err;
+  int sms;
+  if (check_tree(cache, meta) != PKV_OK || device_state(&err, &sms) != PKV_OK)
+    return static_cast<size_t>(-1);
+  TreePlan p;
+  make_tree_plan(cache, meta, sms, &p);
+  return p.ws_bytes;
+}
+
+extern "C" int pkv_attention_tree(void* out, const void* q, const void* k_cache,
+                                  const void* v_cache, const int32_t* block_tables,
+                                  const int32_t* context_lens, const int32_t* query_start_loc,
+                                  const int64_t* tree_mask, float scale,
+                                  const pkv_cache_desc* cache, const pkv_attn_meta* meta,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  if (cache != nullptr && cache->dtype == PKV_FP8_E4M3) return PKV_E_DTYPE;  // pkv_attention_tree_fp8
+  return tree_impl(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                   tree_mask, scale, nullptr, nullptr, cache, meta, workspace, workspace_bytes,
+                   stream);
+}
+
+extern "C" int pkv_attention_tree_fp8(void* out, const void* q, const void* k_cache,
+                                      const void* v_cache, const int32_t* block_tables,
+                                      const int32_t* context_lens,
+                                      const int32_t* query_start_loc, const int64_t* tree_mask,
+                                      float scale, const float* k_descale,
+                                      const float* v_descale, const pkv_cache_desc* cache,
+                                      const pkv_attn_meta* meta, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  if (cache == nullptr) return PKV_E_NULL;
+  if (cache->dtype != PKV_FP8_E4M3) return PKV_E_DTYPE;
+  if (meta != nullptr && meta->num_seqs > 0 && meta->num_tokens > 0) {
+    if (!k_descale || !v_descale) return PKV_E_NULL;
+    if (!aligned4(k_descale) || !aligned4(v_descale)) return PKV_E_ALIGN;
+  }
+  return tree_impl(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                   tree_mask, scale, k_descale, v_descale, cache, meta, workspace,
+                   workspace_bytes, stream);
+}
+
+// ------------------------------------- the rows of accepted drafts
+
+extern "C" int pkv_accept_drafts(void* const* buffers, const int64_t* row_bytes,
+                                 int32_t num_buffers, int32_t num_blocks,
+                                 const int32_t* block_tables, int32_t block_table_stride,
+                                 const int32_t* context_lens, const int32_t* query_start_loc,
+                                 int32_t num_seqs, const int32_t* accepted,
+                                 const int32_t* num_accepted, int32_t max_accepted,
+                                 int32_t* new_context_lens, void* stream) {
+  if (num_buffers < 0 || num_blocks < 0 || num_seqs < 0 || max_accepted < 0) return PKV_E_SHAPE;
+  if (block_table_stride < 1) return PKV_E_META;
+  if (static_cast<int64_t>(num_blocks) * kBlock > INT32_MAX) return PKV_E_SHAPE;
+  if (num_seqs == 0) return PKV_OK;
+  if (!block_tables || !context_lens || !query_start_loc || !num_accepted ||
+      (!accepted && max_accepted > 0) || (num_buffers > 0 && (!buffers || !row_bytes)))
+    return PKV_E_NULL;
+  for (int i = 0; i < num_buffers; ++i) {
+    if (!buffers[i]) return PKV_E_NULL;
+    if (row_bytes[i] < 1 || row_bytes[i] > (int64_t{1} << 26)) return PKV_E_SHAPE;
+    if (!aligned4(buffers[i]) || row_bytes[i] % 4 != 0) return PKV_E_ALIGN;
+  }
+  if (!aligned4(block_tables) || !aligned4(context_lens) || !aligned4(query_start_loc) ||
+      !aligned4(accepted) || !aligned4(num_accepted) || !aligned4(new_context_lens))
+    return PKV_E_ALIGN;
+  // (every CTA of a sequence reads its length, so its new one goes elsewhere)
+  if (new_context_lens != nullptr && new_context_lens < context_lens + num_seqs &&
+      context_lens < new_context_lens + num_seqs)
+    return PKV_E_META;
+  AcceptArgs a{};
+  int sms;
+  if (int st = device_state(&a.err, &sms)) return st;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start_loc = query_start_loc;
+  a.accepted = accepted;
+  a.num_accepted = num_accepted;
+  a.new_lens = new_context_lens;
+  a.bt_stride = block_table_stride;
+  a.num_blocks = num_blocks;
+  a.num_seqs = num_seqs;
+  a.max_accepted = max_accepted;
+  // (without buffers, one launch for the new lengths)
+  for (int b0 = 0; b0 == 0 || b0 < num_buffers; b0 += kAcceptBuffers) {
+    a.num_buffers = std::min(kAcceptBuffers, num_buffers - b0);
+    for (int i = 0; i < a.num_buffers; ++i) a.buffers[i] = {buffers[b0 + i], row_bytes[b0 + i]};
+    a.report = b0 == 0;
+    PKV_TRY(launch_accept(a, as_stream(stream)));
+  }
+  return PKV_OK;
+}
+
 extern "C" int pkv_get_error(int32_t* error_bits, int clear) {
   if (error_bits == nullptr) return PKV_E_NULL;
   int32_t* err;

@@ -273,6 +273,92 @@ struct CopyArgs {
   int32_t num_pairs;
 };
 
+// ---- norms, rotation and write in one pass
+struct RopeArgs {
+  void* q_out;                   // [T, Hq, D] rows, q_out_stride elements apart (as all below)
+  void* k_out;                   // rows only (no slot_mapping), else null
+  const void* q;
+  const void* k;
+  const void* v;                 // null: rows only
+  const int64_t* positions;
+  const float* cos_sin;          // [max_position, rot_dim]: cosines, then sines
+  const void* q_weight;          // [D], null: no norm
+  const void* k_weight;
+  const int64_t* slot_mapping;   // null: rows only
+  void* k_cache;
+  void* v_cache;
+  const float* k_scale;          // e4m3: per kv head (null otherwise)
+  const float* v_scale;
+  int32_t* err;
+  int64_t num_slots;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t max_position;
+  int32_t rot_dim;
+  int32_t interleaved;
+  int32_t groups_per_token;      // set by the launch
+  float eps;
+};
+cudaError_t launch_rope(const RopeArgs& a, int head_size, bool f32, bool fp8, cudaStream_t stream);
+
+// ---- attention of a tree of drafted tokens
+struct TreeArgs {
+  void* out;                     // [T, Hq, D]
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start_loc;
+  const uint64_t* tree_mask;     // [T, mask_words]
+  const float* k_descale;        // e4m3: [num_seqs, Hkv] (null otherwise)
+  const float* v_descale;
+  float* ws_o;                   // [T, Hq, max_splits, D] fp32 (max_splits > 1 only)
+  float* ws_lse;                 // [T, Hq, max_splits], log2 domain
+  int32_t* err;
+  int64_t bt_stride;
+  int32_t num_seqs;
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t group;
+  int32_t num_blocks;
+  int32_t max_query_len;
+  int32_t max_context_len;
+  int32_t mask_words;
+  int32_t split_blocks;          // cache blocks per split (a multiple of 4)
+  int32_t max_splits;
+  float scale_log2;
+};
+cudaError_t launch_tree(const TreeArgs& a, int dtype, int head_size, cudaStream_t stream);
+cudaError_t launch_tree_merge(const TreeArgs& a, bool f32, int head_size, cudaStream_t stream);
+
+// ---- the rows of accepted drafts
+constexpr int kAcceptBuffers = 64;
+struct AcceptBuffer {
+  void* base;                    // [num_blocks, 16, row_bytes]
+  int64_t row_bytes;
+};
+struct AcceptArgs {
+  AcceptBuffer buffers[kAcceptBuffers];
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start_loc;
+  const int32_t* accepted;       // [num_seqs, max_accepted]
+  const int32_t* num_accepted;   // [num_seqs]
+  int32_t* new_lens;             // [num_seqs] or null
+  int32_t* err;
+  int64_t bt_stride;
+  int32_t num_buffers;
+  int32_t num_blocks;
+  int32_t num_seqs;
+  int32_t max_accepted;
+  int32_t report;                // this launch raises errors and writes new_lens
+};
+cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream);
+
 cudaError_t launch_write(const WriteArgs& a, cudaStream_t stream, int num_sms);
 cudaError_t launch_write_int8(const WriteInt8Args& a, cudaStream_t stream);
 cudaError_t launch_attention_int8(const AttnInt8Args& a, int head_size, cudaStream_t stream);

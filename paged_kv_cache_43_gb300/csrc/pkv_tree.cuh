@@ -1,0 +1,65 @@
+// pkv_tree.cuh -- what the tree-attention kernels share: a sequence's checks, the
+// bits of a query row's mask, where a partial goes.
+#pragma once
+
+#include "pkv_common.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+struct TreeSeq {
+  int q0, n, L;      // first query row, drafted rows, keys with them
+  int first;         // the first drafted key: keys before it are seen by every row
+  int32_t err;       // what is wrong (PKV_ERR_* bits, 0: nothing)
+  bool skip;         // nothing to do, nothing to write
+};
+
+// n > 0 and err != 0 without skip: the sequence's rows are zeroed.
+__device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int s) {
+  TreeSeq q;
+  q.L = __ldg(a.context_lens + s);
+  q.q0 = __ldg(a.query_start_loc + s);
+  q.n = __ldg(a.query_start_loc + s + 1) - q.q0;
+  q.first = q.L - q.n;
+  q.err = 0;
+  q.skip = q.n == 0;
+  if (q.n < 0 || q.q0 < 0 || static_cast<int64_t>(q.q0) + q.n > a.num_tokens) {
+    q.err = PKV_ERR_QUERY_LEN;
+    q.skip = true;
+  } else if (q.n > 0) {
+    if (q.L < 1 || static_cast<int64_t>(q.L) > a.bt_stride * kBlock || q.L > a.max_context_len)
+      q.err = PKV_ERR_CONTEXT_LEN;
+    else if (q.n > q.L || q.n > a.max_query_len) q.err = PKV_ERR_QUERY_LEN;
+  }
+  return q;
+}
+
+// Bits of the keys [key0, key0 + 64) that the row whose mask words are `mask` sees: every
+// key before the sequence's first draft, and the drafts whose bits are set.
+__device__ __forceinline__ uint64_t tree_bits(const uint64_t* mask, const TreeSeq& q, int key0) {
+  const int j0 = key0 - q.first;             // draft of the first key
+  if (j0 <= -64) return ~0ull;
+  if (j0 >= q.n) return 0ull;
+  uint64_t bits;
+  if (j0 < 0) {
+    bits = ((1ull << -j0) - 1) | (__ldg(mask) << -j0);
+  } else {
+    const int w = j0 >> 6, sh = j0 & 63;
+    bits = __ldg(mask + w) >> sh;
+    if (sh != 0 && (w + 1) * 64 < q.n) bits |= __ldg(mask + w + 1) << (64 - sh);
+  }
+  const int left = q.n - j0;                 // keys of the sequence from key0 on
+  return left < 64 ? bits & ((1ull << left) - 1) : bits;
+}
+
+// The row of the split partials of query row t, head hq.
+__device__ __forceinline__ int64_t tree_partial(const TreeArgs& a, int64_t t, int hq, int split) {
+  return (t * a.num_q_heads + hq) * a.max_splits + split;
+}
+
+// Splits that a sequence's keys are cut into.
+__device__ __forceinline__ int tree_splits(const TreeArgs& a, int L) {
+  return ((L + kBlock - 1) / kBlock + a.split_blocks - 1) / a.split_blocks;
+}
+
+}  // namespace pkv

@@ -28,12 +28,17 @@ ERR_QUERY_LEN = 1 << 3
 ERR_DECODE_QLEN = 1 << 4
 ERR_TIMEOUT = 1 << 5
 ERR_NONFINITE = 1 << 6
+ERR_POSITION = 1 << 7
+ERR_ACCEPTED = 1 << 8
 EXPORTED = ("pkv_write", "pkv_write_fp8", "pkv_attention_workspace_size", "pkv_attention",
             "pkv_attention_fp8", "pkv_attention_static_scratch",
             "pkv_attention_cascade_workspace_size", "pkv_attention_cascade",
             "pkv_attention_cascade_fp8", "pkv_use_cascade",
             "pkv_write_int8", "pkv_attention_int8_workspace_size", "pkv_attention_int8",
             "pkv_copy_blocks",
+            "pkv_rope_write", "pkv_rope_write_fp8", "pkv_rope",
+            "pkv_attention_tree_workspace_size", "pkv_attention_tree", "pkv_attention_tree_fp8",
+            "pkv_accept_drafts",
             "pkv_get_error", "pkv_status_string", "pkv_last_cuda_error",
             "pkv_last_cuda_error_string", "pkv_debug_wait_test")
 STATIC_SCRATCH_BYTES = 64 << 20
@@ -55,6 +60,16 @@ class AttnMeta(ctypes.Structure):
                 ("max_query_len", ctypes.c_int32), ("max_context_len", ctypes.c_int32),
                 ("num_decode_seqs", ctypes.c_int32), ("sliding_window", ctypes.c_int32),
                 ("kv_split_tokens", ctypes.c_int32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_size", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("max_position", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("k_out_stride", ctypes.c_int64), ("eps", ctypes.c_float)]
 
 
 def library_path() -> str:
@@ -119,6 +134,29 @@ def load(path: str | None = None):
                                            vp, ctypes.c_size_t, vp]
         lib.pkv_copy_blocks.restype = ctypes.c_int
         lib.pkv_copy_blocks.argtypes = [vp, vp, i32, i32, vp, i32, vp]
+        lib.pkv_rope_write.restype = ctypes.c_int
+        lib.pkv_rope_write.argtypes = [vp] * 11 + [ctypes.POINTER(RopeDesc),
+                                                   ctypes.POINTER(CacheDesc), vp]
+        lib.pkv_rope_write_fp8.restype = ctypes.c_int
+        lib.pkv_rope_write_fp8.argtypes = [vp] * 13 + [ctypes.POINTER(RopeDesc),
+                                                       ctypes.POINTER(CacheDesc), vp]
+        lib.pkv_rope.restype = ctypes.c_int
+        lib.pkv_rope.argtypes = [vp] * 8 + [ctypes.POINTER(RopeDesc), vp]
+        lib.pkv_attention_tree_workspace_size.restype = ctypes.c_size_t
+        lib.pkv_attention_tree_workspace_size.argtypes = [ctypes.POINTER(CacheDesc),
+                                                          ctypes.POINTER(AttnMeta)]
+        lib.pkv_attention_tree.restype = ctypes.c_int
+        lib.pkv_attention_tree.argtypes = [vp] * 8 + [ctypes.c_float, ctypes.POINTER(CacheDesc),
+                                                      ctypes.POINTER(AttnMeta), vp,
+                                                      ctypes.c_size_t, vp]
+        lib.pkv_attention_tree_fp8.restype = ctypes.c_int
+        lib.pkv_attention_tree_fp8.argtypes = [vp] * 8 + [ctypes.c_float, vp, vp,
+                                                          ctypes.POINTER(CacheDesc),
+                                                          ctypes.POINTER(AttnMeta), vp,
+                                                          ctypes.c_size_t, vp]
+        lib.pkv_accept_drafts.restype = ctypes.c_int
+        lib.pkv_accept_drafts.argtypes = [vp, vp, i32, i32, vp, i32, vp, vp, i32, vp, vp, i32, vp,
+                                          vp]
         lib.pkv_get_error.restype = ctypes.c_int
         lib.pkv_get_error.argtypes = [ctypes.POINTER(ctypes.c_int32), ctypes.c_int]
         lib.pkv_status_string.restype = ctypes.c_char_p
@@ -580,6 +618,284 @@ def copy_blocks(buffers, pairs, stream=None) -> None:
     page = array.array("q", [t.nbytes // nb for t in buffers] if nb else [0] * len(buffers))
     st = lib.pkv_copy_blocks(ptrs.buffer_info()[0], page.buffer_info()[0], len(buffers), nb,
                              pairs.ctypes.data, pairs.shape[0], _stream_on(dev, stream))
+    if st != 0:
+        _check(st)
+
+
+# ---------------------------------------- steps with drafted tokens
+#
+# (Checked in one expression first, one by one only to say what is wrong: as the
+# int8 calls.)
+
+_I64 = torch.int64
+_FP8 = frozenset(FP8_DTYPES)
+
+
+def _rows_ok(t, dtype, heads, d, tokens, dev) -> bool:
+    """Rows [tokens, heads, d] whose heads lie densely; tokens any stride apart."""
+    return (t.dtype is dtype and t.get_device() == dev and t.shape == (tokens, heads, d)
+            and (t.is_contiguous() or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == d))))
+
+
+def _rope_call(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, dev, **rows):
+    """Checks what the rope calls share; the descriptor.  `rows`: the further tensors of
+    rows by name, with their heads' number."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise PkvError("q and k must be [num_tokens, heads, head_size]")
+    (tokens, hq, d), hkv, dt = q.shape, k.shape[1], q.dtype
+    if dt is not _BF16 and dt is not _F32:
+        raise PkvError(f"unsupported dtype {dt}")
+    if not _rows_ok(q, dt, hq, d, tokens, dev) or not _rows_ok(k, dt, hkv, d, tokens, dev):
+        rows = dict(q=(q, hq), k=(k, hkv), **rows)
+    for n, (t, h) in rows.items():
+        if not _rows_ok(t, dt, h, d, tokens, dev):
+            if t.get_device() != dev:
+                raise PkvError(f"{n} must be on the current CUDA device ({dev})")
+            raise PkvError(f"{n} must be {dt} [{tokens}, {h}, {d}] with dense heads")
+    if not (positions.dtype is _I64 and cos_sin.dtype is _F32
+            and positions.get_device() == dev == cos_sin.get_device()
+            and positions.is_contiguous() and cos_sin.is_contiguous()
+            and positions.shape == (tokens,) and cos_sin.dim() == 2):
+        _refuse(dev, positions=(positions, _I64), cos_sin=(cos_sin, _F32))
+        raise PkvError("positions must be [num_tokens], cos_sin [max_position, rot_dim]")
+    for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and not (w.dtype is dt and w.shape == (d,) and w.get_device() == dev
+                                  and w.is_contiguous()):
+            _refuse(dev, **{n: (w, dt)})
+            raise PkvError(f"{n} must be [{d}]")
+    strides = [t.stride(0) if tokens > 1 else t.shape[1] * d
+               for t in (q, k, *(r[0] for n, r in rows.items() if n not in ("q", "k")))]
+    return strides, RopeDesc(tokens, hq, hkv, d, PKV_BF16 if dt is _BF16 else PKV_F32,
+                             cos_sin.shape[1], cos_sin.shape[0], bool(interleaved), 0, 0, 0, 0, 0,
+                             eps)
+
+
+def _rope_write(call, q_out, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, scales,
+                fp8, q_weight, k_weight, eps, interleaved, stream) -> None:
+    dev = _current_device()
+    hq, hkv = q.shape[1] if q.dim() == 3 else 0, k.shape[1] if k.dim() == 3 else 0
+    strides, desc = _rope_call(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved,
+                               dev, v=(v, hkv), q_out=(q_out, hq))
+    desc.q_stride, desc.k_stride, desc.v_stride, desc.q_out_stride = strides
+    kd = k_cache.dtype
+    if not ((kd in _FP8 if fp8 else kd is q.dtype) and v_cache.dtype is kd
+            and slot_mapping.dtype is _I64
+            and k_cache.get_device() == dev == v_cache.get_device() == slot_mapping.get_device()
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and slot_mapping.is_contiguous() and k_cache.dim() == 4
+            and v_cache.shape == k_cache.shape and k_cache.shape[2:] == k.shape[1:]
+            and slot_mapping.shape == positions.shape):
+        if fp8 and (kd not in _FP8 or v_cache.dtype not in _FP8):
+            raise PkvError("the caches must hold e4m3 codes (uint8 or float8_e4m3fn)")
+        _refuse(dev, slot_mapping=(slot_mapping, _I64),
+                k_cache=(k_cache, None if fp8 else q.dtype),
+                v_cache=(v_cache, None if fp8 else q.dtype))
+        raise PkvError("k_cache and v_cache must both be [num_blocks, 16, num_kv_heads, "
+                       "head_size], slot_mapping [num_tokens]")
+    for n, t in zip(("k_scale", "v_scale"), scales):
+        if not (t.dtype is _F32 and t.shape == (hkv,) and t.get_device() == dev
+                and t.is_contiguous()):
+            _refuse(dev, **{n: (t, _F32)})
+            raise PkvError(f"{n} must have num_kv_heads entries")
+    nb, bs, _, d = k_cache.shape
+    cache = CacheDesc(nb, bs, hkv, d, PKV_FP8_E4M3 if fp8 else desc.dtype)
+    st = call(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(),
+              cos_sin.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(),
+              0 if k_weight is None else k_weight.data_ptr(), slot_mapping.data_ptr(),
+              k_cache.data_ptr(), v_cache.data_ptr(), *[t.data_ptr() for t in scales], desc, cache,
+              _stream_on(dev, stream))
+    if st != 0:
+        _check(st)
+
+
+def rope_write(q_out, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, *,
+               q_weight=None, k_weight=None, eps=1e-6, interleaved=False, stream=None) -> None:
+    """pkv_rope_write: norms of the query and key heads (where weights [D] are given),
+    rotation by cos_sin (fp32 [max_position, rot_dim]) at positions (int64 [T]), q [T, Hq,
+    D] to q_out, k and v [T, Hkv, D] to the caches at slot_mapping [T], in one pass.  q, k,
+    v and q_out may be slices of a larger row (tokens any stride apart); q_out may be q."""
+    _rope_write((_lib or load()).pkv_rope_write, q_out, q, k, v, positions, cos_sin, slot_mapping,
+                k_cache, v_cache, (), False, q_weight, k_weight, eps, interleaved, stream)
+
+
+def rope_write_fp8(q_out, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale,
+                   v_scale, *, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                   stream=None) -> None:
+    """pkv_rope_write_fp8: rope_write of bf16 rows into e4m3 caches with the scales of
+    write_fp8 (fp32 [Hkv])."""
+    _rope_write((_lib or load()).pkv_rope_write_fp8, q_out, q, k, v, positions, cos_sin,
+                slot_mapping, k_cache, v_cache, (k_scale, v_scale), True, q_weight, k_weight, eps,
+                interleaved, stream)
+
+
+def rope(q_out, k_out, q, k, positions, cos_sin, *, q_weight=None, k_weight=None, eps=1e-6,
+         interleaved=False, stream=None) -> None:
+    """pkv_rope: rope_write's q and k rows alone, k to k_out [T, Hkv, D] (which may be k), as
+    write_int8 wants them."""
+    lib = _lib or load()
+    dev = _current_device()
+    hq, hkv = q.shape[1] if q.dim() == 3 else 0, k.shape[1] if k.dim() == 3 else 0
+    strides, desc = _rope_call(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved,
+                               dev, q_out=(q_out, hq), k_out=(k_out, hkv))
+    desc.q_stride, desc.k_stride, desc.q_out_stride, desc.k_out_stride = strides
+    st = lib.pkv_rope(q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
+                      positions.data_ptr(), cos_sin.data_ptr(),
+                      0 if q_weight is None else q_weight.data_ptr(),
+                      0 if k_weight is None else k_weight.data_ptr(), desc,
+                      _stream_on(dev, stream))
+    if st != 0:
+        _check(st)
+
+
+def workspace_size_tree(k_cache, meta: AttnMeta) -> int:
+    desc = cache_desc(k_cache)
+    n = load().pkv_attention_tree_workspace_size(desc, meta)
+    if n == _NO_SIZE:
+        raise PkvError("invalid attention description")
+    return int(n)
+
+
+def _attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                    tree_mask, scale, descales, fp8, max_query_len, max_context_len,
+                    kv_split_tokens, workspace, stream) -> None:
+    lib = _lib or load()
+    dev = _current_device()
+    kd, c, r, n = k_cache.dtype, k_cache.shape, q.shape, context_lens.shape
+    if not ((kd in _FP8 and q.dtype is _BF16 if fp8 else
+             (kd is _BF16 or kd is _F32) and q.dtype is kd)
+            and v_cache.dtype is kd and out.dtype is q.dtype and block_tables.dtype is _I32
+            and context_lens.dtype is _I32 and query_start_loc.dtype is _I32
+            and tree_mask.dtype is _I64
+            and (dev == q.get_device() == out.get_device() == k_cache.get_device()
+                 == v_cache.get_device() == block_tables.get_device()
+                 == context_lens.get_device() == query_start_loc.get_device()
+                 == tree_mask.get_device())
+            and q.is_contiguous() and out.is_contiguous() and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and block_tables.is_contiguous()
+            and context_lens.is_contiguous() and query_start_loc.is_contiguous()
+            and tree_mask.is_contiguous()
+            and len(c) == 4 and len(r) == 3 and len(n) == 1 and block_tables.dim() == 2
+            and query_start_loc.dim() == 1 and v_cache.shape == c and out.shape == r
+            and r[2] == c[3] and block_tables.shape[0] >= n[0] and query_start_loc.shape[0] > n[0]
+            and tree_mask.shape == (r[0], (max_query_len + 63) // 64)):
+        if fp8 and (kd not in _FP8 or v_cache.dtype not in _FP8):
+            raise PkvError("the caches must hold e4m3 codes (uint8 or float8_e4m3fn)")
+        if not fp8 and kd not in (_BF16, _F32):
+            raise PkvError(f"unsupported cache dtype {kd} (bf16 or fp32; e4m3: "
+                           "attention_tree_fp8; int8 is not taken)")
+        row = _BF16 if fp8 else kd
+        _refuse(dev, out=(out, row), q=(q, row), k_cache=(k_cache, kd), v_cache=(v_cache, kd),
+                block_tables=(block_tables, _I32), context_lens=(context_lens, _I32),
+                query_start_loc=(query_start_loc, _I32), tree_mask=(tree_mask, _I64))
+        if len(c) != 4 or v_cache.shape != c:
+            raise PkvError("k_cache and v_cache must both be [num_blocks, 16, num_kv_heads, "
+                           "head_size]")
+        if len(r) != 3 or out.shape != r or r[2] != c[3]:
+            raise PkvError("out and q must both be [num_tokens, heads, head_size]")
+        if tree_mask.dim() != 2 or tree_mask.shape != (r[0], (max_query_len + 63) // 64):
+            raise PkvError("tree_mask must be [num_tokens, ceil(max_query_len / 64)]")
+        raise PkvError("block_tables [num_seqs, stride], context_lens [num_seqs] and "
+                       "query_start_loc [num_seqs + 1] must fit together")
+    for name, t in zip(("k_descale", "v_descale"), descales):
+        if not (t.dtype is _F32 and t.shape == (n[0], c[2]) and t.get_device() == dev
+                and t.is_contiguous()):
+            _refuse(dev, **{name: (t, _F32)})
+            raise PkvError(f"{name} must be [num_seqs, num_kv_heads]")
+    desc = CacheDesc(*c, PKV_FP8_E4M3 if fp8 else (PKV_BF16 if kd is _BF16 else PKV_F32))
+    meta = AttnMeta(n[0], r[0], r[1], block_tables.shape[1], max_query_len, max_context_len, -1, 0,
+                    kv_split_tokens)
+    ws_ptr, ws_bytes = 0, 0
+    if workspace is None:
+        ws_bytes = lib.pkv_attention_tree_workspace_size(desc, meta)
+        if ws_bytes == _NO_SIZE:
+            ws_bytes = 0   # (the call itself says what is wrong)
+        elif ws_bytes:
+            if stream is None:
+                workspace = q.new_empty(ws_bytes, dtype=_U8)
+            else:          # scratch of the stream that uses it
+                with torch.cuda.stream(stream):
+                    workspace = q.new_empty(ws_bytes, dtype=_U8)
+            ws_ptr = workspace.data_ptr()
+    else:
+        _refuse(dev, workspace=(workspace, None))
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    rest = (desc, meta, ws_ptr, ws_bytes, _stream_on(dev, stream))
+    call = lib.pkv_attention_tree_fp8 if fp8 else lib.pkv_attention_tree
+    st = call(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+              block_tables.data_ptr(), context_lens.data_ptr(), query_start_loc.data_ptr(),
+              tree_mask.data_ptr(), scale, *[t.data_ptr() for t in descales], *rest)
+    if st != 0:
+        _check(st)
+
+
+def attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                   tree_mask, scale, *, max_query_len, max_context_len, kv_split_tokens=0,
+                   workspace=None, stream=None) -> None:
+    """pkv_attention_tree into ``out`` [T, Hq, D]: a sequence's query rows are its drafted
+    tokens, its last keys theirs; tree_mask (int64 [T, ceil(max_query_len / 64)]) has bit j
+    of row i set where draft i sees draft j.  ``workspace`` (uint8 CUDA tensor of
+    workspace_size_tree bytes) is allocated here when not given and needed."""
+    _attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                    tree_mask, scale, (), False, max_query_len, max_context_len, kv_split_tokens,
+                    workspace, stream)
+
+
+def attention_tree_fp8(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                       tree_mask, scale, k_descale, v_descale, *, max_query_len, max_context_len,
+                       kv_split_tokens=0, workspace=None, stream=None) -> None:
+    """pkv_attention_tree_fp8: attention_tree over e4m3 caches with the descales of
+    attention_fp8 (fp32 [num_seqs, Hkv])."""
+    _attention_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                    tree_mask, scale, (k_descale, v_descale), True, max_query_len,
+                    max_context_len, kv_split_tokens, workspace, stream)
+
+
+def accept_drafts(buffers, block_tables, context_lens, query_start_loc, accepted, num_accepted, *,
+                  new_context_lens=None, stream=None) -> None:
+    """pkv_accept_drafts: in every buffer (CUDA tensors [num_blocks, 16, ...]: the K and V
+    caches of all layers, not int8 ones), moves the rows of each sequence's accepted drafts
+    (int32 [num_seqs, max_accepted], rising; num_accepted [num_seqs] of them) right behind
+    the keys before its drafts; their number with these goes to ``new_context_lens``."""
+    lib = _lib or load()
+    dev = _current_device()
+    n = context_lens.shape
+    lens = context_lens if new_context_lens is None else new_context_lens
+    if not (block_tables.dtype is _I32 and context_lens.dtype is _I32
+            and query_start_loc.dtype is _I32 and accepted.dtype is _I32
+            and num_accepted.dtype is _I32 and lens.dtype is _I32
+            and (dev == block_tables.get_device() == context_lens.get_device()
+                 == query_start_loc.get_device() == accepted.get_device()
+                 == num_accepted.get_device() == lens.get_device())
+            and block_tables.is_contiguous() and context_lens.is_contiguous()
+            and query_start_loc.is_contiguous() and accepted.is_contiguous()
+            and num_accepted.is_contiguous() and lens.is_contiguous()
+            and len(n) == 1 and block_tables.dim() == 2 and query_start_loc.dim() == 1
+            and accepted.dim() == 2 and block_tables.shape[0] >= n[0]
+            and query_start_loc.shape[0] > n[0] and accepted.shape[0] == n[0]
+            and num_accepted.shape == n == lens.shape):
+        _refuse(dev, block_tables=(block_tables, _I32), context_lens=(context_lens, _I32),
+                query_start_loc=(query_start_loc, _I32), accepted=(accepted, _I32),
+                num_accepted=(num_accepted, _I32), new_context_lens=(lens, _I32))
+        raise PkvError("block_tables [num_seqs, stride], context_lens, num_accepted and "
+                       "new_context_lens [num_seqs], accepted [num_seqs, most] and "
+                       "query_start_loc [num_seqs + 1] must fit together")
+    head = buffers[0].shape[:2] if len(buffers) else (0, 16)
+    nb = head[0]
+    for t in buffers:
+        if (t.get_device() != dev or not t.is_contiguous() or t.dtype is _I8 or t.dim() < 3
+                or t.shape[:2] != head or head[1] != 16):
+            _refuse(dev, buffers=(t, None))
+            raise PkvError("buffers must all be [num_blocks, 16, ...] of the same number of "
+                           "blocks, and not of an int8 cache")
+    ptrs = array.array("Q", [t.data_ptr() for t in buffers])
+    rows = array.array("q", [t.nbytes // (16 * nb) for t in buffers] if nb else
+                       [4] * len(buffers))
+    st = lib.pkv_accept_drafts(ptrs.buffer_info()[0], rows.buffer_info()[0], len(buffers), nb,
+                               block_tables.data_ptr(), block_tables.shape[1],
+                               context_lens.data_ptr(), query_start_loc.data_ptr(), n[0],
+                               accepted.data_ptr(), num_accepted.data_ptr(), accepted.shape[1],
+                               0 if new_context_lens is None else lens.data_ptr(),
+                               _stream_on(dev, stream))
     if st != 0:
         _check(st)
 

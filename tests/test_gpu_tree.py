@@ -1,0 +1,275 @@
+"""pkv_attention_tree and pkv_attention_tree_fp8 against a plain 64-bit implementation, with
+the bounds of tests/drafts.py."""
+import numpy as np
+import pytest
+import torch
+
+from drafts import Batch, drafted, mask_words
+from paged_kv_cache_43_gb300 import build, pkv
+
+pytestmark = pytest.mark.gpu
+BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+    pkv.load()
+    pkv.get_error(clear=True)
+    yield
+    assert pkv.get_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (6, 2), (8, 1), (5, 1), (32, 2)])
+def test_lengths_around_blocks_and_tiles(dtype, d, hq, hkv):
+    L = [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 200, 257]
+    b = Batch(*drafted(L, d + hq), hq=hq, hkv=hkv, d=d, dtype=dtype, seed=hq).cuda()
+    b.check(b.call())
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n", [1, 2, 16, 63, 64, 65, 127, 128, 129, 200])
+def test_tree_sizes(dtype, n):
+    """One word of mask and more, whole and partial row tiles, one tile and several."""
+    b = Batch([n, 1, n], [0, 300, 1000 - n], hq=8, hkv=2, d=128, dtype=dtype, seed=n).cuda()
+    b.check(b.call())
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3, F32])
+@pytest.mark.parametrize("split", [64, 128, 320, 1024, 2048])
+def test_splits(dtype, split):
+    """A row's keys in one split or many, drafts that lie across a split's end."""
+    n, before = [7, 40, 1, 17, 33], [900, 0, 2000, 1270, 31]
+    b = Batch(n, before, hq=4, hkv=2, d=64 if split == 320 else 128, dtype=dtype, seed=split).cuda()
+    b.check(b.call(kv_split_tokens=split))
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (16, 16, 64), (64, 4, 128)])
+def test_long_contexts(dtype, hq, hkv, d):
+    b = Batch([16, 5], [9000, 4321], hq=hq, hkv=hkv, d=d, dtype=dtype, seed=d).cuda()
+    b.check(b.call())
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3, F32])
+def test_any_mask(dtype):
+    """Rows that see no draft, not themselves, every draft, later ones; rows that see nothing
+    (no keys before the drafts) are zero; bits from n on are ignored."""
+    rng = np.random.default_rng(1)
+    n, before = [70, 9, 64, 3], [20, 0, 0, 130]
+    masks = []
+    for k in n:
+        rows = [int.from_bytes(rng.bytes(9), "little") & (1 << k) - 1 for _ in range(k)]
+        rows[0], rows[1 % k] = 0, (1 << k) - 1
+        masks += [r | int(rng.integers(0, 1 << 60)) << k for r in rows]
+    b = Batch(n, before, hq=6, hkv=3, d=64, dtype=dtype, masks=masks).cuda()
+    out = b.call()
+    b.check(out)
+    assert bool((out[70] == 0).all()) and bool((out[79] == 0).all())
+
+
+@pytest.mark.parametrize("split", [0, 64])
+def test_a_chain_is_a_causal_chunk(split):
+    n, before = [5, 33, 64], [100, 0, 700]
+    masks = [(2 << i) - 1 for k in n for i in range(k)]
+    b = Batch(n, before, hq=8, hkv=2, d=128, masks=masks).cuda()
+    out = b.call(kv_split_tokens=split)
+    b.check(out)
+    g = b.g
+    chunk = torch.empty_like(out)
+    pkv.attention(chunk, g["q"], g["k"], g["v"], g["bt"], g["cl"], g["qsl"], b.scale,
+                  max_query_len=b.max_n, max_context_len=b.max_L)
+    want, tol = b.want()
+    assert bool(((out.double() - chunk.double()).abs().cpu() <= 2 * tol).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("split", [0, 64])
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_not_finite_drafts_reach_only_rows_that_see_them(dtype, split, what):
+    n, before = [20, 90], [50, 330]
+    b = Batch(n, before, hq=4, hkv=2, d=64, dtype=dtype, seed=5)
+    c = b.k if what == "k" else b.v
+    for s, draft in ((0, 3), (1, 0 if what == "k" else 37), (1, 88)):
+        p = before[s] + draft
+        row = c.view(torch.uint8) if b.fp8 else c
+        row[b.table[s, p // 16], p % 16, 1, 7] = 0x7F if b.fp8 else float("nan")
+        if not b.fp8 and what == "v":
+            row[b.table[s, p // 16], p % 16, 1, 9] = float("inf")
+    b.cuda()
+    out = b.call(kv_split_tokens=split)
+    seen = torch.zeros(110, dtype=torch.bool)
+    for s, draft in ((0, 3), (1, 0 if what == "k" else 37), (1, 88)):
+        t0 = int(b.starts[s])
+        for i in range(n[s]):
+            seen[t0 + i] |= bool(b.bits[t0 + i] >> draft & 1)
+    bad = ~torch.isfinite(out.cpu())
+    assert bool((bad[:, 2:].any(2).all(1) == seen).all()) and not bool(bad[:, :2].any())
+    if what == "v":
+        b.check(out)
+
+
+def test_scores_of_any_size():
+    """Large scores of both signs, and a few keys far above the rest, late in the row."""
+    b = Batch([12, 30], [500, 90], hq=4, hkv=2, d=128, seed=9)
+    b.q *= 30
+    b.k[b.table[0, 25]] *= 40
+    b.cuda()
+    b.check(b.call())
+    b.check(b.call(kv_split_tokens=128))
+    b.scale = -b.scale
+    b.check(b.call())
+
+
+def test_equal_keys_and_zero_queries_average_v():
+    b = Batch([8], [400], hq=2, hkv=1, d=64, seed=2)
+    b.q.zero_()
+    b.cuda()
+    b.check(b.call())
+
+
+def test_rows_of_no_sequence_and_empty_sequences():
+    b = Batch([0, 3, 0, 2, 0], [0, 40, 7, 15, 99], hq=4, hkv=2, d=64, extra_rows=6).cuda()
+    out = torch.full_like(b.g["q"], 5.0)
+    b.call(out)
+    b.check(out)
+    assert bool((out[5:] == 5.0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_bad_metadata_zeroes_its_sequence_alone(dtype):
+    n, before = [3, 4, 2, 5], [40, 50, 60, 70]
+    for s, what, value, bit in ((0, "cl", 0, pkv.ERR_CONTEXT_LEN), (1, "cl", 10 ** 6, pkv.ERR_CONTEXT_LEN),
+                                (2, "cl", 1, pkv.ERR_QUERY_LEN), (3, "cl", -5, pkv.ERR_CONTEXT_LEN)):
+        b = Batch(n, before, hq=4, hkv=2, d=64, dtype=dtype).cuda()
+        want, tol = b.want()
+        b.g[what][s] = value
+        out = b.call()
+        assert pkv.get_error() == bit
+        rows = slice(int(b.starts[s]), int(b.starts[s + 1]))
+        assert bool((out[rows] == 0).all())
+        want[rows] = 0
+        b.check(out, (want, tol))
+
+
+def test_drafts_past_the_stated_most():
+    b = Batch([3, 20], [40, 50], hq=4, hkv=2, d=64).cuda()
+    want, tol = b.want()
+    out = b.call(max_query_len=8)
+    assert pkv.get_error() == pkv.ERR_QUERY_LEN
+    assert bool((out[3:11] == 0).all())
+    assert bool(((out[:3].double().cpu() - want[:3]).abs() <= tol[:3]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3, F32])
+def test_bad_block_ids_leave_other_sequences_alone(dtype):
+    n, before = [3, 4, 2], [40, 500, 60]
+    b = Batch(n, before, hq=4, hkv=2, d=128, dtype=dtype).cuda()
+    want = b.want()
+    for bad in (-1, -2 ** 31, b.k.shape[0], 2 ** 31 - 1):
+        b.g["bt"][1, 7] = bad
+        out = b.call()
+        assert pkv.get_error() == pkv.ERR_BLOCK_ID
+        w, t = (x.clone() for x in want)
+        w[3:7], t[3:7] = out[3:7].double().cpu(), 1.0
+        b.check(out, (w, t))
+
+
+def test_rows_outside_the_batch():
+    b = Batch([3, 4], [40, 50], hq=4, hkv=2, d=64).cuda()
+    want, tol = b.want()
+    b.g["qsl"][2] = 1000
+    out = b.call()
+    assert pkv.get_error() == pkv.ERR_QUERY_LEN
+    assert bool(torch.isnan(out[3:]).all())
+    assert bool(((out[:3].double().cpu() - want[:3]).abs() <= tol[:3]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_two_graphs_on_two_streams(dtype):
+    """Captured calls with a workspace each, replayed beside each other on new inputs."""
+    bs = [Batch([16, 3], [1500, 700], hq=8, hkv=2, d=128, dtype=dtype, seed=s).cuda()
+          for s in range(2)]
+    outs = [b.call() for b in bs]
+    torch.cuda.synchronize()
+    graphs, streams = [], [torch.cuda.Stream() for _ in bs]
+    for b, out in zip(bs, outs):
+        n = pkv.workspace_size_tree(b.g["k"], pkv.attn_meta(
+            b.g["q"], b.g["bt"], b.g["cl"], max_query_len=b.max_n, max_context_len=b.max_L))
+        b.ws = torch.empty(max(n, 256), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.call(out, workspace=b.ws)
+        graphs.append(g)
+    for b in bs:     # other queries, fewer keys
+        b.q = torch.randn(b.q.shape).to(b.row)
+        b.g["q"].copy_(b.q)
+        b.L[0] -= 333
+        b.g["cl"][0] -= 333
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for b, out in zip(bs, outs):
+        b.check(out)
+
+
+def test_another_stream_than_the_current_one():
+    b = Batch([16], [3000], hq=8, hkv=2, d=128).cuda()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.full_like(b.g["q"], float("nan"))
+    b.call(out, stream=s)
+    s.synchronize()
+    b.check(out)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_offsets_past_32_bits(dtype):
+    """Blocks behind 2^31 elements of the cache."""
+    hkv, d = 8, 128
+    b = Batch([9], [200], hq=16, hkv=hkv, d=d, dtype=dtype)
+    want = b.want()
+    nb = (1 << 31) // (16 * hkv * d) + 20
+    used = b.table[0].copy()
+    b.cuda()
+    for c in ("k", "v"):
+        e = torch.uint8 if b.fp8 else dtype
+        big = torch.zeros((nb, 16, hkv, d), dtype=e, device="cuda")
+        new = torch.arange(nb - len(used), nb, device="cuda")
+        big[new] = b.g[c].view(e)[torch.from_numpy(used).long().cuda()]
+        b.g[c] = big.view(dtype)
+    b.g["bt"] = new.int()[None].contiguous()
+    b.check(b.call(), want)
+
+
+def test_no_queries_is_a_no_op():
+    b = Batch([2], [10], hq=4, hkv=2, d=64).cuda()
+    g = b.g
+    e = g["q"][:0]
+    pkv.attention_tree(e, e, g["k"], g["v"], g["bt"], g["cl"], g["qsl"], g["mask"][:0], b.scale,
+                       max_query_len=2, max_context_len=12)
+
+
+def test_refusals_of_gpu_tensors():
+    b = Batch([2, 70], [10, 30], hq=4, hkv=2, d=64).cuda()
+    g = dict(b.g)
+    for name, bad in (("mask", g["mask"][:, :1].contiguous()), ("mask", g["mask"].int()),
+                      ("mask", g["mask"][:10]), ("q", g["q"].float()), ("q", g["q"][:, :, :32]),
+                      ("k", g["k"][:1]), ("bt", g["bt"][:1]), ("qsl", g["qsl"][:2]),
+                      ("cl", g["cl"].long()), ("q", g["q"][:, :3].contiguous()),
+                      ("k", g["k"].to(torch.int8))):
+        b.g = {**g, name: bad}
+        with pytest.raises(pkv.PkvError):
+            b.call()
+    b.g = g
+    with pytest.raises(pkv.PkvError):
+        b.call(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"), kv_split_tokens=64)
+    with pytest.raises(pkv.PkvError):
+        b.call(kv_split_tokens=72)
