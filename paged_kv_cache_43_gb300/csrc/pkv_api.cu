@@ -1626,7 +1626,8 @@ int check_tree(const pkv_cache_desc* c, const pkv_attn_meta* m) {
 }
 
 void make_tree_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms, TreePlan* p) {
-  const int64_t tiles = tree_tiles(*c, *m);
+  // row tiles: 32 rows (fp32) or 128 (tcgen05)
+  const int64_t tiles = c->dtype == PKV_F32 ? tree_tiles(*c, *m) : (tree_tiles(*c, *m) + 3) / 4;
   *p = TreePlan{};
   const int64_t blocks = std::max<int64_t>((static_cast<int64_t>(m->max_context_len) + kBlock - 1) / kBlock, 1);
   const int64_t units = std::max<int64_t>(m->num_seqs * tiles * c->num_kv_heads, 1);
@@ -1698,7 +1699,14 @@ int tree_impl(void* out, const void* q, const void* k_cache, const void* v_cache
   a.max_splits = p.max_splits;
   a.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t st = as_stream(stream);
-  PKV_TRY(launch_tree(a, cache->dtype, cache->head_size, st));
+  if (cache->dtype == PKV_F32) {
+    PKV_TRY(launch_tree_f32(a, cache->head_size, st));
+  } else {
+    CUtensorMap kmap, vmap;
+    if (int e = encode_cache_map(&kmap, k_cache, *cache)) return e;
+    if (int e = encode_cache_map(&vmap, v_cache, *cache)) return e;
+    PKV_TRY(launch_tree_tc(kmap, vmap, a, cache->head_size, cache->dtype == PKV_FP8_E4M3, st));
+  }
   if (p.max_splits > 1) PKV_TRY(launch_tree_merge(a, cache->dtype == PKV_F32, cache->head_size, st));
   return PKV_OK;
 }

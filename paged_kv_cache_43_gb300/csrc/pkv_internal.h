@@ -331,8 +331,12 @@ struct TreeArgs {
   int32_t split_blocks;          // cache blocks per split (a multiple of 4)
   int32_t max_splits;
   float scale_log2;
+  uint64_t wait_limit_ns;        // test hook, as DecodeArgs (the tcgen05 kernel)
+  int32_t debug_stall;
 };
-cudaError_t launch_tree(const TreeArgs& a, int dtype, int head_size, cudaStream_t stream);
+cudaError_t launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeArgs& a,
+                           int head_size, bool fp8, cudaStream_t stream);
+cudaError_t launch_tree_f32(const TreeArgs& a, int head_size, cudaStream_t stream);
 cudaError_t launch_tree_merge(const TreeArgs& a, bool f32, int head_size, cudaStream_t stream);
 
 // ---- the rows of accepted drafts

@@ -21,20 +21,7 @@ namespace {
 
 constexpr int kRows = 32, kKeys = 32, kThreads = 128;
 
-template <typename T>
-__device__ __forceinline__ float load_f32(const T* p);
-template <>
-__device__ __forceinline__ float load_f32(const float* p) { return __ldg(p); }
-template <>
-__device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-template <>
-__device__ __forceinline__ float load_f32(const uint8_t* p) {   // an e4m3 code
-  const uint2 h = e4m3x4_to_f16x4(*p);
-  return f16_lo(h.x);
-}
-
-// T: what q and out hold; C: what the caches hold.
-template <typename T, typename C, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) pkv_tree_kernel(const TreeArgs a) {
   constexpr int LD = D + 4;
   extern __shared__ float sm[];
@@ -49,27 +36,22 @@ __global__ void __launch_bounds__(kThreads) pkv_tree_kernel(const TreeArgs a) {
   if (q.err != 0 && reporter) raise_error(a.err, q.err);
   const int row0 = tile * kRows, rows = min(q.n * G - row0, kRows);
   if (q.skip || rows <= 0) return;
-  T* out = static_cast<T*>(a.out);
+  float* out = static_cast<float*>(a.out);
   auto at = [&](int r) {   // row r of the tile in q and out
     return (static_cast<int64_t>(q.q0 + (row0 + r) / G) * Hq + kvh * G + (row0 + r) % G) * D;
   };
   if (q.err != 0) {
     if (split == 0)
-      for (int i = threadIdx.x; i < rows * D; i += kThreads) out[at(i / D) + i % D] = T(0.f);
+      for (int i = threadIdx.x; i < rows * D; i += kThreads) out[at(i / D) + i % D] = 0.f;
     return;
   }
   const int nsplit = tree_splits(a, q.L);
   if (split >= nsplit) return;
   const int key_begin = split * a.split_blocks * kBlock;
   const int key_end = min(q.L, key_begin + a.split_blocks * kBlock);
-  float ksc = 1.f, vsc = 1.f;
-  if (a.k_descale != nullptr) {
-    ksc = __ldg(a.k_descale + static_cast<int64_t>(s) * a.num_kv_heads + kvh);
-    vsc = __ldg(a.v_descale + static_cast<int64_t>(s) * a.num_kv_heads + kvh);
-  }
   for (int i = threadIdx.x; i < kRows * D; i += kThreads)
     sQ[i / D * LD + i % D] =
-        i / D < rows ? load_f32(static_cast<const T*>(a.q) + at(i / D) + i % D) : 0.f;
+        i / D < rows ? __ldg(static_cast<const float*>(a.q) + at(i / D) + i % D) : 0.f;
 
   // scores: thread = row of 4 neighbours, 8 keys 4 apart; output: the same row, D / 4 elements
   const int row = threadIdx.x / 4, part = threadIdx.x % 4;
@@ -89,8 +71,8 @@ __global__ void __launch_bounds__(kThreads) pkv_tree_kernel(const TreeArgs a) {
         const int b = __ldg(bt + p / kBlock);
         if (b >= 0 && b < a.num_blocks) {
           const int64_t src = ((static_cast<int64_t>(b) * kBlock + p % kBlock) * a.num_kv_heads + kvh) * D + i % D;
-          k = load_f32(static_cast<const C*>(a.k_cache) + src) * ksc;
-          v = load_f32(static_cast<const C*>(a.v_cache) + src) * vsc;
+          k = __ldg(static_cast<const float*>(a.k_cache) + src);
+          v = __ldg(static_cast<const float*>(a.v_cache) + src);
         } else if (i % D == 0) {
           raise_error(a.err, PKV_ERR_BLOCK_ID);
         }
@@ -159,8 +141,7 @@ __global__ void __launch_bounds__(kThreads) pkv_tree_kernel(const TreeArgs a) {
       const int d = 16 * i + 4 * part + e;
       const float r = o[4 * i + e] * inv;
       if (nsplit == 1) {
-        if constexpr (std::is_same_v<T, float>) out[dst + d] = r;
-        else out[dst + d] = __float2bfloat16(r);
+        out[dst + d] = r;
       } else {
         const int64_t w = tree_partial(a, q.q0 + (row0 + row) / G, kvh * G + (row0 + row) % G, split);
         a.ws_o[w * D + d] = r;
@@ -234,10 +215,10 @@ __global__ void __launch_bounds__(128) pkv_tree_merge_kernel(const TreeArgs a) {
   }
 }
 
-template <typename T, typename C, int D>
+template <int D>
 cudaError_t launch_t(const TreeArgs& a, cudaStream_t stream) {
   constexpr int smem = (3 * 32 * (D + 4) + kRows * (kKeys + 1)) * 4;
-  auto kfn = pkv_tree_kernel<T, C, D>;
+  auto kfn = pkv_tree_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const int tiles = (a.max_query_len * a.group + kRows - 1) / kRows;
@@ -248,14 +229,8 @@ cudaError_t launch_t(const TreeArgs& a, cudaStream_t stream) {
 }  // namespace
 
 
-cudaError_t launch_tree(const TreeArgs& a, int dtype, int head_size, cudaStream_t stream) {
-  if (dtype == PKV_F32) return head_size == 128 ? launch_t<float, float, 128>(a, stream)
-                                                : launch_t<float, float, 64>(a, stream);
-  if (dtype == PKV_BF16)
-    return head_size == 128 ? launch_t<__nv_bfloat16, __nv_bfloat16, 128>(a, stream)
-                            : launch_t<__nv_bfloat16, __nv_bfloat16, 64>(a, stream);
-  return head_size == 128 ? launch_t<__nv_bfloat16, uint8_t, 128>(a, stream)
-                          : launch_t<__nv_bfloat16, uint8_t, 64>(a, stream);
+cudaError_t launch_tree_f32(const TreeArgs& a, int head_size, cudaStream_t stream) {
+  return head_size == 128 ? launch_t<128>(a, stream) : launch_t<64>(a, stream);
 }
 
 cudaError_t launch_tree_merge(const TreeArgs& a, bool f32, int head_size, cudaStream_t stream) {

@@ -131,7 +131,9 @@ class Batch:
                         o[i] += p[i, j] * (v[j] - v0[j])
                     spread = torch.stack([(p[i, :, None] * (v0 - o[i]).abs()).sum(0)
                                           for i in range(n)])
-                    size = (q.abs() @ torch.nan_to_num(k, 0, 0, 0).abs().T * self.scale)
+                    if self.fp8:   # (the denominator sums the weights before they are rounded)
+                        spread = p @ v0.abs() + o.abs()
+                    size = (q.abs() @ torch.nan_to_num(k, 0, 0, 0).abs().T * abs(self.scale))
                     w = w_eps * 1.01 + 2.0 ** -20 + self.d * 2.0 ** -23 * size.amax(1, keepdim=True)
                     # The numerator and the denominator are fp32 sums of L terms: each product
                     # and partial sum is rounded once, so they are off by at most L 2^-24 of

@@ -273,3 +273,18 @@ def test_refusals_of_gpu_tensors():
         b.call(workspace=torch.empty(256, dtype=torch.uint8, device="cuda"), kv_split_tokens=64)
     with pytest.raises(pkv.PkvError):
         b.call(kv_split_tokens=72)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_bounded_waits_run_out_and_the_device_recovers(dtype):
+    """With the first K tile withheld the call returns, PKV_ERR_TIMEOUT set, and the next
+    one (which needs the same tensor and shared memory) is right."""
+    b = Batch([16, 40], [1500, 300], hq=8, hkv=2, d=128, dtype=dtype).cuda()
+    pkv.debug_wait_test(True)
+    try:
+        for split in (0, 64):
+            b.call(kv_split_tokens=split)
+            assert pkv.get_error() & pkv.ERR_TIMEOUT
+    finally:
+        pkv.debug_wait_test(False)
+    b.check(b.call())
