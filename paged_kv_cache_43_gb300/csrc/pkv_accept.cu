@@ -14,49 +14,52 @@ namespace pkv {
 
 namespace {
 
-constexpr int kAcceptThreads = 128;
+constexpr int kAcceptThreads = 256;
 constexpr int kRowsInFlight = 8;
+constexpr int kCtaBuffers = 4;   // buffers of a CTA, for which a path is looked up once
+constexpr int kChunk = 64;       // drafts of a path looked up at a time
 
+// Moves rows[u].x to rows[u].y, u < count (below zero: none), of buffers [b0, b0 + nb).
 template <typename V>
-__device__ __forceinline__ void move_rows(const AcceptArgs& a, const AcceptBuffer& b,
-                                          const int32_t* path, const int32_t* table, int first,
+__device__ __forceinline__ void move_rows(const AcceptArgs& a, int b0, int nb, const int2* rows,
                                           int count) {
-  char* base = static_cast<char*>(b.base);
-  const int64_t cols = b.row_bytes / static_cast<int64_t>(sizeof(V));
-  auto row_at = [&](int p) -> char* {
-    const int block = __ldg(table + p / kBlock);
-    return block >= 0 && block < a.num_blocks
-               ? base + (static_cast<int64_t>(block) * kBlock + p % kBlock) * b.row_bytes : nullptr;
-  };
-  for (int64_t col = threadIdx.x; col < cols; col += kAcceptThreads) {
+  int cols[kCtaBuffers], total = 0;   // vectors of a row
+#pragma unroll
+  for (int i = 0; i < kCtaBuffers; ++i) {
+    cols[i] = i < nb ? static_cast<int>(a.buffers[b0 + i].row_bytes / static_cast<int64_t>(sizeof(V))) : 0;
+    total += cols[i];
+  }
+  for (int at = threadIdx.x; at < total; at += kAcceptThreads) {
+    int col = at, i = 0;
+#pragma unroll
+    for (int k = 0; k + 1 < kCtaBuffers; ++k)
+      if (i == k && col >= cols[k]) {
+        col -= cols[k];
+        ++i;
+      }
+    const AcceptBuffer& b = a.buffers[b0 + i];
+    char* base = static_cast<char*>(b.base) + static_cast<int64_t>(col) * static_cast<int64_t>(sizeof(V));
     for (int j0 = 0; j0 < count; j0 += kRowsInFlight) {
       V v[kRowsInFlight];
-      char* to[kRowsInFlight];
+      int to[kRowsInFlight];
 #pragma unroll
       for (int u = 0; u < kRowsInFlight; ++u) {
-        to[u] = nullptr;
-        const int j = j0 + u;
-        if (j >= count) continue;
-        const int p = __ldg(path + j);
-        if (p == j) continue;
-        const char* from = row_at(first + p);
-        char* dst = row_at(first + j);
-        if (from == nullptr || dst == nullptr) continue;   // (a bad block id: the row stays)
-        v[u] = *(reinterpret_cast<const V*>(from) + col);
-        to[u] = dst;
+        const int2 r = j0 + u < count ? rows[j0 + u] : make_int2(-1, -1);
+        to[u] = r.y;
+        if (r.y >= 0) v[u] = *reinterpret_cast<const V*>(base + r.x * b.row_bytes);
       }
 #pragma unroll
       for (int u = 0; u < kRowsInFlight; ++u)
-        if (to[u] != nullptr) *(reinterpret_cast<V*>(to[u]) + col) = v[u];
+        if (to[u] >= 0) *reinterpret_cast<V*>(base + to[u] * b.row_bytes) = v[u];
     }
   }
 }
 
 __global__ void __launch_bounds__(kAcceptThreads)
     pkv_accept_kernel(const __grid_constant__ AcceptArgs a) {
+  __shared__ int2 rows[kChunk];
   const int s = blockIdx.x;
-  const AcceptBuffer& b = a.buffers[blockIdx.y];
-  const bool reporter = a.report != 0 && blockIdx.y == 0 && threadIdx.x == 0;
+  const bool first_cta = a.report != 0 && blockIdx.y == 0;
   const int L = __ldg(a.context_lens + s);
   const int n = __ldg(a.query_start_loc + s + 1) - __ldg(a.query_start_loc + s);
   const int count = __ldg(a.num_accepted + s);
@@ -75,32 +78,42 @@ __global__ void __launch_bounds__(kAcceptThreads)
     }
     if (!__syncthreads_and(fine)) bad = PKV_ERR_ACCEPTED;
   }
-  if (reporter && a.new_lens != nullptr) a.new_lens[s] = bad != 0 ? L : L - n + count;
-  if (bad != 0) {
-    if (reporter) raise_error(a.err, bad);
-    return;
+  if (first_cta && threadIdx.x == 0) {
+    if (a.new_lens != nullptr) a.new_lens[s] = bad != 0 ? L : L - n + count;
+    if (bad != 0) raise_error(a.err, bad);
   }
-  if (a.num_buffers == 0) return;   // (the lengths alone)
-  const int first = L - n;
-  if (reporter) {
-    for (int j = 0; j < count; ++j) {
-      const int p = __ldg(path + j);
-      const int x = __ldg(table + (first + p) / kBlock), y = __ldg(table + (first + j) / kBlock);
-      if (p != j && (x < 0 || x >= a.num_blocks || y < 0 || y >= a.num_blocks))
-        raise_error(a.err, PKV_ERR_BLOCK_ID);
+  if (bad != 0 || a.num_buffers == 0) return;
+  const int first = L - n, b0 = blockIdx.y * kCtaBuffers, nb = min(a.num_buffers - b0, kCtaBuffers);
+  bool wide = true;
+  for (int i = 0; i < nb; ++i)
+    wide = wide && ((reinterpret_cast<uintptr_t>(a.buffers[b0 + i].base) | a.buffers[b0 + i].row_bytes) & 15) == 0;
+  for (int c0 = 0; c0 < count; c0 += kChunk) {
+    const int m = min(count - c0, kChunk);
+    if (c0 > 0) __syncthreads();
+    if (threadIdx.x < m) {
+      const int j = c0 + threadIdx.x, p = __ldg(path + j);
+      int2 r = make_int2(-1, -1);
+      if (p != j) {
+        const int x = __ldg(table + (first + p) / kBlock), y = __ldg(table + (first + j) / kBlock);
+        if (x >= 0 && x < a.num_blocks && y >= 0 && y < a.num_blocks)
+          r = make_int2(x * kBlock + (first + p) % kBlock, y * kBlock + (first + j) % kBlock);
+        else if (first_cta)
+          raise_error(a.err, PKV_ERR_BLOCK_ID);   // (the row stays)
+      }
+      rows[threadIdx.x] = r;
     }
+    __syncthreads();
+    if (wide) move_rows<uint4>(a, b0, nb, rows, m);
+    else move_rows<uint32_t>(a, b0, nb, rows, m);
   }
-  if (((reinterpret_cast<uintptr_t>(b.base) | b.row_bytes) & 15) == 0)
-    move_rows<uint4>(a, b, path, table, first, count);
-  else
-    move_rows<uint32_t>(a, b, path, table, first, count);
 }
 
 }  // namespace
 
 cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream) {
   if (a.num_seqs == 0) return cudaSuccess;
-  pkv_accept_kernel<<<dim3(a.num_seqs, a.num_buffers > 0 ? a.num_buffers : 1), kAcceptThreads, 0, stream>>>(a);
+  pkv_accept_kernel<<<dim3(a.num_seqs, a.num_buffers > kCtaBuffers ? (a.num_buffers + kCtaBuffers - 1) / kCtaBuffers : 1),
+                      kAcceptThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -1525,7 +1525,7 @@ int rope_impl(void* q_out, void* k_out, const void* q, const void* k, const void
     return st;
   }
   if ((reinterpret_cast<uintptr_t>(positions) & 7u) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) ||
-      !aligned4(cos_sin) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned4(k_scale) ||
+      !aligned16(cos_sin) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned4(k_scale) ||
       !aligned4(v_scale))
     return PKV_E_ALIGN;
   RopeArgs a{};
@@ -1558,7 +1558,8 @@ int rope_impl(void* q_out, void* k_out, const void* q, const void* k, const void
   a.rot_dim = d.rot_dim;
   a.interleaved = d.interleaved != 0;
   a.eps = d.eps;
-  PKV_TRY(launch_rope(a, d.head_size, d.dtype == PKV_F32, k_scale != nullptr, as_stream(stream)));
+  PKV_TRY(launch_rope(a, d.head_size, d.dtype == PKV_F32, k_scale != nullptr, sms,
+                      as_stream(stream)));
   return PKV_OK;
 }
 

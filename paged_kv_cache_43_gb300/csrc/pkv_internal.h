@@ -301,7 +301,8 @@ struct RopeArgs {
   int32_t groups_per_token;      // set by the launch
   float eps;
 };
-cudaError_t launch_rope(const RopeArgs& a, int head_size, bool f32, bool fp8, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs& a, int head_size, bool f32, bool fp8, int num_sms,
+                        cudaStream_t stream);
 
 // ---- attention of a tree of drafted tokens
 struct TreeArgs {
