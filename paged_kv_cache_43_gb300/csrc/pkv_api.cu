@@ -226,9 +226,10 @@ int encode_heads_map(CUtensorMap* map, const void* base, const pkv_cache_desc& c
 
 // TMA descriptor of the bf16 query tensor [num_tokens, num_q_heads, D] viewed
 // as (D, Hq, T) with a box of 64 columns x `group` heads x 128/group tokens:
-// one box is the 128-row (token, head) tile of one kv head, 128 bytes wide.
+// one box is the 128-row (token, head) tile of one kv head, 128 bytes wide
+// (`toks` tokens instead, where it is given).
 int encode_query_map(CUtensorMap* map, const void* q, int num_tokens, int num_q_heads,
-                     int head_size, int group) {
+                     int head_size, int group, int toks = 0) {
   PFN_cuTensorMapEncodeTiled_v12000 fn;
   if (int st = encode_fn(&fn)) return st;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_size),
@@ -237,7 +238,7 @@ int encode_query_map(CUtensorMap* map, const void* q, int num_tokens, int num_q_
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_size) * 2,
                                  static_cast<cuuint64_t>(num_q_heads) * head_size * 2};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group),
-                             static_cast<cuuint32_t>(prefill_tc_tokens_per_tile(group))};
+                             static_cast<cuuint32_t>(toks > 0 ? toks : prefill_tc_tokens_per_tile(group))};
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1606,9 +1607,15 @@ namespace pkv {
 namespace {
 
 struct TreePlan {
+  // fp32
   int split_blocks = 0;
   int max_splits = 0;
-  size_t ws_o_bytes = 0;
+  // tcgen05
+  bool keys_on_m = false;
+  int tile_toks = 0, part_rows = 0, cta_tiles = 0, max_groups = 0, workers = 0;
+  bool whole = false;
+  int64_t range = 0;
+  size_t ws_o_bytes = 0, ws_lse_bytes = 0;
   size_t ws_bytes = 0;
 };
 
@@ -1623,27 +1630,63 @@ int check_tree(const pkv_cache_desc* c, const pkv_attn_meta* m) {
   if (m->sliding_window != 0) return PKV_E_META;
   if (m->num_seqs > 65535 || tree_tiles(*c, *m) * c->num_kv_heads > 65535)   // (the grid)
     return PKV_E_SHAPE;
+  if (c->dtype != PKV_F32 && m->num_q_heads / c->num_kv_heads > kTreeRows) return PKV_E_SHAPE;
   return PKV_OK;
 }
 
 void make_tree_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms, TreePlan* p) {
-  // row tiles: 32 rows (fp32) or 128 (tcgen05)
-  const int64_t tiles = c->dtype == PKV_F32 ? tree_tiles(*c, *m) : (tree_tiles(*c, *m) + 3) / 4;
   *p = TreePlan{};
-  const int64_t blocks = std::max<int64_t>((static_cast<int64_t>(m->max_context_len) + kBlock - 1) / kBlock, 1);
-  const int64_t units = std::max<int64_t>(m->num_seqs * tiles * c->num_kv_heads, 1);
-  int64_t sb = m->kv_split_tokens / kBlock;
-  if (sb == 0) {
-    sb = 64;
-    while (sb > 4 && units * ((blocks + sb - 1) / sb) < 2 * num_sms) sb /= 2;
+  if (c->dtype == PKV_F32) {
+    const int64_t blocks = std::max<int64_t>((static_cast<int64_t>(m->max_context_len) + kBlock - 1) / kBlock, 1);
+    const int64_t units = std::max<int64_t>(m->num_seqs * tree_tiles(*c, *m) * c->num_kv_heads, 1);
+    int64_t sb = m->kv_split_tokens / kBlock;
+    if (sb == 0) {
+      sb = 64;
+      while (sb > 4 && units * ((blocks + sb - 1) / sb) < 2 * num_sms) sb /= 2;
+    }
+    p->split_blocks = static_cast<int>(sb);
+    p->max_splits = static_cast<int>((blocks + sb - 1) / sb);
+    if (p->max_splits > 1) {
+      const size_t n = static_cast<size_t>(m->num_tokens) * m->num_q_heads * p->max_splits;
+      p->ws_o_bytes = round_up(n * c->head_size * sizeof(float), 256);
+      p->ws_lse_bytes = round_up(n * sizeof(float), 256);
+      p->ws_bytes = p->ws_o_bytes + p->ws_lse_bytes;
+    }
+    return;
   }
-  p->split_blocks = static_cast<int>(sb);
-  p->max_splits = static_cast<int>((blocks + sb - 1) / sb);
-  if (p->max_splits > 1) {
-    const size_t n = static_cast<size_t>(m->num_tokens) * m->num_q_heads * p->max_splits;
-    p->ws_o_bytes = round_up(n * c->head_size * sizeof(float), 256);
-    p->ws_bytes = p->ws_o_bytes + round_up(n * sizeof(float), 256);
+  // A worker is as many CTAs as the longest sequence has row tiles, 8 at most: they share
+  // the keys' way through L2.
+  constexpr int kMaxTiles = 8;
+  const int group = m->num_q_heads / c->num_kv_heads;
+  const int64_t most_rows = static_cast<int64_t>(m->max_query_len) * group;
+  p->keys_on_m = c->head_size == 128 && most_rows <= kTreeKeysRows;
+  const int step_keys = p->keys_on_m ? kTreeKeysStep : kTreeStepKeys;
+  const int tile_rows = p->keys_on_m ? kTreeKeysRows : kTreeRows;
+  p->tile_toks = std::max(std::min(m->max_query_len, tile_rows / group), 1);
+  p->part_rows = p->keys_on_m ? p->tile_toks * group : kTreeRows;
+  const int tiles = std::max((m->max_query_len + p->tile_toks - 1) / p->tile_toks, 1);
+  p->cta_tiles = std::min(tiles, kMaxTiles);
+  p->max_groups = (tiles + p->cta_tiles - 1) / p->cta_tiles;
+  const int ctas_per_sm = p->keys_on_m ? 1 : 2;
+  const int64_t most = std::max(num_sms * ctas_per_sm / p->cta_tiles, 1);
+  const int64_t units = std::max<int64_t>(static_cast<int64_t>(m->num_seqs) * p->max_groups * c->num_kv_heads, 1);
+  const int64_t steps = (static_cast<int64_t>(m->max_context_len) + step_keys - 1) / step_keys;
+  const int64_t kWholeSteps = p->keys_on_m ? 2 : 4, kMinRange = 4;
+  if (m->kv_split_tokens > 0) {
+    p->range = std::max(m->kv_split_tokens / step_keys, 1);
+    p->workers = static_cast<int>(std::min<int64_t>((units * (steps + kTreeStart) + p->range - 1) / p->range, INT32_MAX / 16));
+    p->range = std::max(p->range, (units * (steps + kTreeStart) + p->workers - 1) / p->workers);
+  } else if (steps <= kWholeSteps) {
+    p->whole = true;
+    p->workers = static_cast<int>(std::min(units, most));
+    return;
+  } else {
+    p->workers = static_cast<int>(std::max<int64_t>(std::min(most, units * (steps + kTreeStart) / kMinRange), 1));
   }
+  const size_t rows = static_cast<size_t>(p->workers) * 2 * p->cta_tiles * p->part_rows;
+  p->ws_o_bytes = round_up(rows * c->head_size * sizeof(float), 256);
+  p->ws_lse_bytes = round_up(rows * sizeof(float), 256);
+  p->ws_bytes = p->ws_o_bytes + p->ws_lse_bytes + round_up(static_cast<size_t>(units) * sizeof(int2), 256);
 }
 
 int tree_impl(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -1682,8 +1725,10 @@ int tree_impl(void* out, const void* q, const void* k_cache, const void* v_cache
   a.k_descale = k_descale;
   a.v_descale = v_descale;
   if (p.ws_bytes > 0) {
-    a.ws_o = static_cast<float*>(workspace);
-    a.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.ws_o_bytes);
+    char* ws = static_cast<char*>(workspace);
+    a.ws_o = reinterpret_cast<float*>(ws);
+    a.ws_lse = reinterpret_cast<float*>(ws + p.ws_o_bytes);
+    a.span = reinterpret_cast<int2*>(ws + p.ws_o_bytes + p.ws_lse_bytes);
   }
   a.err = err;
   a.bt_stride = meta->block_table_stride;
@@ -1699,16 +1744,26 @@ int tree_impl(void* out, const void* q, const void* k_cache, const void* v_cache
   a.split_blocks = p.split_blocks;
   a.max_splits = p.max_splits;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.keys_on_m = p.keys_on_m;
+  a.part_rows = p.part_rows;
+  a.tile_toks = p.tile_toks;
+  a.cta_tiles = p.cta_tiles;
+  a.max_groups = p.max_groups;
+  a.workers = p.workers;
+  a.whole = p.whole;
+  a.range = p.range;
   const cudaStream_t st = as_stream(stream);
   if (cache->dtype == PKV_F32) {
     PKV_TRY(launch_tree_f32(a, cache->head_size, st));
-  } else {
-    CUtensorMap kmap, vmap;
-    if (int e = encode_cache_map(&kmap, k_cache, *cache)) return e;
-    if (int e = encode_cache_map(&vmap, v_cache, *cache)) return e;
-    PKV_TRY(launch_tree_tc(kmap, vmap, a, cache->head_size, cache->dtype == PKV_FP8_E4M3, st));
+    return PKV_OK;
   }
-  if (p.max_splits > 1) PKV_TRY(launch_tree_merge(a, cache->dtype == PKV_F32, cache->head_size, st));
+  CUtensorMap qmap, kmap, vmap;
+  if (int e = encode_query_map(&qmap, q, meta->num_tokens, meta->num_q_heads, cache->head_size,
+                               a.group, a.tile_toks))
+    return e;
+  if (int e = encode_cache_map(&kmap, k_cache, *cache)) return e;
+  if (int e = encode_cache_map(&vmap, v_cache, *cache)) return e;
+  PKV_TRY(launch_tree_tc(qmap, kmap, vmap, a, cache->head_size, cache->dtype == PKV_FP8_E4M3, st));
   return PKV_OK;
 }
 

@@ -316,8 +316,9 @@ struct TreeArgs {
   const uint64_t* tree_mask;     // [T, mask_words]
   const float* k_descale;        // e4m3: [num_seqs, Hkv] (null otherwise)
   const float* v_descale;
-  float* ws_o;                   // [T, Hq, max_splits, D] fp32 (max_splits > 1 only)
-  float* ws_lse;                 // [T, Hq, max_splits], log2 domain
+  float* ws_o;                   // fp32 kernel: [T, Hq, max_splits, D] (max_splits > 1 only);
+                                 // tcgen05: [workers, 2, cta_tiles, part_rows, D]
+  float* ws_lse;                 // the same without D, log2 domain
   int32_t* err;
   int64_t bt_stride;
   int32_t num_seqs;
@@ -329,16 +330,36 @@ struct TreeArgs {
   int32_t max_query_len;
   int32_t max_context_len;
   int32_t mask_words;
-  int32_t split_blocks;          // cache blocks per split (a multiple of 4)
+  int32_t split_blocks;          // fp32 kernel: cache blocks per split (a multiple of 4)
   int32_t max_splits;
   float scale_log2;
-  uint64_t wait_limit_ns;        // test hook, as DecodeArgs (the tcgen05 kernel)
+  // The tcgen05 kernels.
+  int32_t keys_on_m;             // pkv_tree_keys.cu, else pkv_tree_tc.cu
+  int32_t part_rows;             // (row, q head) pairs that a tile has at most
+  int32_t tile_toks;             // query rows of a tile
+  int32_t cta_tiles;             // CTAs of a worker: row tiles of a unit, side by side
+  int32_t max_groups;            // groups of that many tiles, for the longest sequence
+  int32_t workers;
+  int32_t whole;                 // units are not cut: no workspace, no merge
+  int64_t range;                 // steps of a worker, 0: equal shares
+  int2* span;                    // [num_seqs, max_groups, Hkv]: a unit's first worker, workers
+  uint64_t wait_limit_ns;        // test hook, as DecodeArgs
   int32_t debug_stall;
 };
-cudaError_t launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeArgs& a,
-                           int head_size, bool fp8, cudaStream_t stream);
+constexpr int kTreeRows = 128, kTreeStepKeys = 64;         // pkv_tree_tc.cu
+// Steps that a unit counts on the line of work for its start and end (64 sequences of 128 to 4096
+// keys, 32 kv heads: 369 us with 1, 365 with 2, 347 with 4).
+constexpr int kTreeStart = 4;
+constexpr int kTreeKeysRows = 32, kTreeKeysStep = 128;     // pkv_tree_keys.cu
+// Tiles of at most kTreeKeysRows rows, head_size 128 (called by launch_tree_tc).
+cudaError_t launch_tree_keys(const CUtensorMap& qmap, const CUtensorMap& kmap,
+                             const CUtensorMap& vmap, const TreeArgs& a, bool fp8,
+                             cudaStream_t stream);
+// qmap: the queries in boxes of 64 columns x group heads x tile_toks rows.
+cudaError_t launch_tree_tc(const CUtensorMap& qmap, const CUtensorMap& kmap,
+                           const CUtensorMap& vmap, const TreeArgs& a, int head_size, bool fp8,
+                           cudaStream_t stream);
 cudaError_t launch_tree_f32(const TreeArgs& a, int head_size, cudaStream_t stream);
-cudaError_t launch_tree_merge(const TreeArgs& a, bool f32, int head_size, cudaStream_t stream);
 
 // ---- the rows of accepted drafts
 constexpr int kAcceptBuffers = 64;

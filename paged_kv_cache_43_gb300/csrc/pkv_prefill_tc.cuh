@@ -85,8 +85,8 @@ __device__ __forceinline__ uint2 codes_to_f16x4(uint32_t codes) {
   else return e4m3x4_to_f16x4(codes);
 }
 
-// Widens one tile of KEYS keys x 128 e4m3 or int8 codes (128-byte swizzled rows at
-// `tile`) in place into the fp16 tile layout (two 64-column halves, KEYS x 128 bytes apart,
+// Widens one 128-key x 128 tile of e4m3 or int8 codes (128-byte swizzled rows at `tile`) in
+// place into the fp16 tile layout (two 64-column halves, 16 KB apart,
 // 128-byte swizzled); all 32 lanes of the calling warp.  A batch covers 16
 // rows: a lane reads its 16-code chunk of 4 rows, and only after the warp has
 // read the whole batch does it write the batch's fp16 chunks (those of half 0
@@ -95,12 +95,12 @@ __device__ __forceinline__ uint2 codes_to_f16x4(uint32_t codes) {
 // one before it is converted.  8 lanes (which a shared-memory access serves
 // together) take 4 chunks of one half in two rows whose numbers differ in bits
 // 0 and 2: their reads and their writes fall into different banks.
-template <bool I8, int KEYS = kTcKeys>
+template <bool I8>
 __device__ __forceinline__ void widen_tile_fp8(uint8_t* tile, int lane, int b0, int b1) {
   const int c = 4 * ((lane >> 3) & 1) + (lane & 3);   // chunk: columns 16c .. 16c + 15
   const int j = 2 * (c & 3);        // its first 8-column chunk within the half
   const int r0 = (lane >> 4) ^ ((lane & 4) ? 5 : 0);
-  uint8_t* half = tile + (c >> 2) * (KEYS * 128);
+  uint8_t* half = tile + (c >> 2) * (kTcKeys * 128);
   uint4 codes[4], ahead[4];
   auto read = [&](int b, uint4 (&to)[4]) {
 #pragma unroll
@@ -141,7 +141,7 @@ __device__ __forceinline__ void widen_tile_fp8(uint8_t* tile, int lane, int b0, 
 // 2b + 1; going from the last batch to the first, those were read earlier
 // (or, for b = 0, by this batch before its writes).  A lane reads two 16-code
 // chunks per batch.
-template <bool I8, int KEYS = kTcKeys>
+template <bool I8>
 __device__ __forceinline__ void widen_tile_fp8_d64(uint8_t* tile, int lane) {
   const int c = lane & 3;           // code chunk: columns 16c .. 16c + 15
   uint4 codes[2], ahead[2];
@@ -164,7 +164,7 @@ __device__ __forceinline__ void widen_tile_fp8_d64(uint8_t* tile, int lane) {
           make_uint4(z.x, z.y, w.x, w.y);
     }
   };
-  constexpr int kBatches = KEYS / 16;
+  constexpr int kBatches = kTcKeys / 16;
   read(kBatches - 1, codes);
 #pragma unroll 1
   for (int b = kBatches - 1; b > 0; b -= 2) {   // (the next batch's codes are read first)

@@ -11,8 +11,6 @@
 // The fp32 kernel: a CTA has 32 rows (drafted token, q head of one kv head), walks its
 // split 32 keys at a time, K and V in shared memory, scores on CUDA cores (fp32 scores
 // cannot go through the tensor core's types at the accuracy that fp32 is held to).
-#include <type_traits>
-
 #include "pkv_tree.cuh"
 
 namespace pkv {
@@ -20,6 +18,16 @@ namespace pkv {
 namespace {
 
 constexpr int kRows = 32, kKeys = 32, kThreads = 128;
+
+// The row of the partials of query row t, head hq.
+__device__ __forceinline__ int64_t tree_partial(const TreeArgs& a, int64_t t, int hq, int split) {
+  return (t * a.num_q_heads + hq) * a.max_splits + split;
+}
+
+// Splits that a sequence's keys are cut into.
+__device__ __forceinline__ int tree_splits(const TreeArgs& a, int L) {
+  return ((L + kBlock - 1) / kBlock + a.split_blocks - 1) / a.split_blocks;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) pkv_tree_kernel(const TreeArgs a) {
@@ -151,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) pkv_tree_kernel(const TreeArgs a) {
 }
 
 // One warp per (query row, q head) of a sequence with several splits.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(128) pkv_tree_merge_kernel(const TreeArgs a) {
   constexpr int PER = D / 32;
   constexpr int kUnroll = 8;   // partials in flight
@@ -204,15 +212,9 @@ __global__ void __launch_bounds__(128) pkv_tree_merge_kernel(const TreeArgs a) {
     }
   }
   const float inv = den == 0.f ? 0.f : 1.f / den;
-  T* out = static_cast<T*>(a.out) + w * D + lane * PER;
-  if constexpr (std::is_same_v<T, float>) {
+  float* out = static_cast<float*>(a.out) + w * D + lane * PER;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) out[k] = acc[k] * inv;
-  } else {
-#pragma unroll
-    for (int k = 0; k < PER; k += 2)
-      *reinterpret_cast<__nv_bfloat162*>(out + k) = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
-  }
+  for (int k = 0; k < PER; ++k) out[k] = acc[k] * inv;
 }
 
 template <int D>
@@ -223,6 +225,10 @@ cudaError_t launch_t(const TreeArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int tiles = (a.max_query_len * a.group + kRows - 1) / kRows;
   kfn<<<dim3(a.max_splits, a.num_kv_heads * tiles, a.num_seqs), kThreads, smem, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.max_splits <= 1) return e;
+  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
+  pkv_tree_merge_kernel<D><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -231,19 +237,6 @@ cudaError_t launch_t(const TreeArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_tree_f32(const TreeArgs& a, int head_size, cudaStream_t stream) {
   return head_size == 128 ? launch_t<128>(a, stream) : launch_t<64>(a, stream);
-}
-
-cudaError_t launch_tree_merge(const TreeArgs& a, bool f32, int head_size, cudaStream_t stream) {
-  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
-  const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
-  if (f32) {
-    if (head_size == 128) pkv_tree_merge_kernel<float, 128><<<grid, 128, 0, stream>>>(a);
-    else pkv_tree_merge_kernel<float, 64><<<grid, 128, 0, stream>>>(a);
-  } else {
-    if (head_size == 128) pkv_tree_merge_kernel<__nv_bfloat16, 128><<<grid, 128, 0, stream>>>(a);
-    else pkv_tree_merge_kernel<__nv_bfloat16, 64><<<grid, 128, 0, stream>>>(a);
-  }
-  return cudaGetLastError();
 }
 
 }  // namespace pkv

@@ -1,5 +1,5 @@
-// pkv_tree.cuh -- what the tree-attention kernels share: a sequence's checks, the
-// bits of a query row's mask, where a partial goes.
+// pkv_tree.cuh -- what the tree-attention kernels share: a sequence's checks and the
+// bits of a query row's mask.
 #pragma once
 
 #include "pkv_common.cuh"
@@ -50,16 +50,6 @@ __device__ __forceinline__ uint64_t tree_bits(const uint64_t* mask, const TreeSe
   }
   const int left = q.n - j0;                 // keys of the sequence from key0 on
   return left < 64 ? bits & ((1ull << left) - 1) : bits;
-}
-
-// The row of the split partials of query row t, head hq.
-__device__ __forceinline__ int64_t tree_partial(const TreeArgs& a, int64_t t, int hq, int split) {
-  return (t * a.num_q_heads + hq) * a.max_splits + split;
-}
-
-// Splits that a sequence's keys are cut into.
-__device__ __forceinline__ int tree_splits(const TreeArgs& a, int L) {
-  return ((L + kBlock - 1) / kBlock + a.split_blocks - 1) / a.split_blocks;
 }
 
 }  // namespace pkv

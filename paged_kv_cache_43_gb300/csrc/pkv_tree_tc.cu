@@ -9,32 +9,35 @@
 // and no rescaling of O.  The denominator of bf16 sums the rounded weights, so the output
 // is a convex combination of V rows.
 //
-// Layout.  Few query rows share each key, so the keys' bytes are the bound (HBM) up to
-// about 100 rows a kv head, the chain S - softmax - P V beyond.  Keys are cut into splits,
-// one CTA each with one tile of 128 rows; two CTAs an SM (each 256 of the 512 TMEM columns),
-// so one's products and copies run under the other's softmax.  Warps:
-//   0-3  softmax, a thread a row; before that Q to shared memory, at the end the rows out
+// Work.  Few query rows share each key, so the keys' bytes are the bound (HBM) up to
+// about 100 rows a kv head, the chain S - softmax - P V beyond.  All units (sequence, kv
+// head) of the batch lie on one line, 64-key steps and a start each, which is cut into
+// equal ranges, one a worker (its lengths are read on the device).  A worker is a CTA for
+// each tile of 128 rows: they walk the same keys side by side, and find each other's in L2.
+// A unit that lies in several ranges leaves partials, at most two a worker, which a second
+// kernel merges; all others are written at once.  Two CTAs an SM (each 256 of the 512
+// TMEM columns), so one's products and copies run under the other's softmax.  Warps:
+//   0-3  softmax, a thread a row, and the rows out at the end of a unit
 //   4, 5 start the TMA copies of K, of V (a box per cache block and 64 columns)
 //   6    issues the products: S of the next 64 keys is formed while these are exponentiated
 //        (S has two buffers, P lies over S)
-//   7    tensor memory
-//   8-11 (e4m3) widen K and V codes in place, two warps each
+//   7    finds the CTA's units and starts the copies of Q
+//   8-11 (e4m3) widen codes, K's and V's in turn, from a ring of codes to one of fp16
+// The copies of a unit's keys begin while the one before it is computed.
+//
 // What a key that a row does not see holds must not reach the row, although P = 0 there
 // (0 x NaN): in the tiles with drafted keys the softmax warps zero V's rows behind the
 // last key and its values that are not finite, and the rows that see those get them at
 // the end.
-#include <float.h>
-
-#include "pkv_prefill_tc.cuh"
-#include "pkv_tree.cuh"
+#include "pkv_tree_tc.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kKeys = 64;                       // keys of a step
+constexpr int kKeys = kTreeStepKeys;            // keys of a step
 constexpr int kStepBlocks = kKeys / kBlock;
-constexpr int kRows = 128;
+constexpr int kRows = kTreeRows;
 constexpr uint32_t kCols = 256;                 // TMEM columns of a CTA
 // S of step h at 64 (h % 2), P over its first 32 columns; O at 128.
 __device__ __forceinline__ uint32_t col_s(int h) { return 64u * (h & 1); }
@@ -44,35 +47,41 @@ constexpr uint32_t kColO = 128;
 template <bool FP8>
 constexpr float kMost = FP8 ? 32768.f : 0x1p60f;
 
-template <int D>
+template <int D, bool FP8>
 struct Lay {
   static constexpr int kHalves = D / 64;
   static constexpr int kQHalf = kRows * 128;    // 64 columns: 128 rows x 128 B
   static constexpr int kQ = kHalves * kQHalf;
   static constexpr int kTHalf = kKeys * 128;
   static constexpr int kTile = kHalves * kTHalf;
-  // K tiles are read once by S, V tiles wait for their softmax: one slot more
-  static constexpr int kKSlots = 2 * 128 / D, kVSlots = 3 * 128 / D;
-  static constexpr int kRingBytes = (kKSlots + kVSlots) * kTile;
+  static constexpr int kCodes = kKeys * D;
+  // slots of K and as many of V: of operand tiles, of codes (e4m3)
+  static constexpr int kSlots = (FP8 ? 1 : 2) * 128 / D;
+  static constexpr int kCodeSlots = FP8 ? 2 * 128 / D : 0;
+  static constexpr int kRing = 2 * kSlots * kTile, kCodeRing = 2 * kCodeSlots * kCodes;
+  static constexpr int kStage = 4 * 32 * 128;   // rows on their way out: 32 x 32 fp32 a warp
 };
 
-template <int D>
+template <int D, bool FP8>
 struct Shared {
-  uint64_t q_full, pv_done, o_done, drain;
+  using L = Lay<D, FP8>;
+  uint64_t q_full, q_empty, q_conv, pv_done, o_done, fixed, drain;
   uint64_t s_full[2], p_full[2];
-  uint64_t k_full[Lay<D>::kKSlots], k_empty[Lay<D>::kKSlots], k_land[Lay<D>::kKSlots];
-  uint64_t v_full[Lay<D>::kVSlots], v_empty[Lay<D>::kVSlots], v_land[Lay<D>::kVSlots];
+  uint64_t full[2][L::kSlots], empty[2][L::kSlots];                    // of K, of V
+  uint64_t code_full[2][L::kCodeSlots + 1], code_empty[2][L::kCodeSlots + 1];
+  uint64_t seg_full[kSegs], seg_empty[kSegs];
+  Seg seg[kSegs];
   uint32_t tmem_base;
   int32_t abort;
-  int32_t v_odd;                                // a drafted V value is not finite
+  int32_t v_odd[2];   // by the segment's parity: its number + 1 if a drafted V value is not finite
 };
 
 // Two CTAs of 113 KB and the 1 KB that each costs are the SM's 228 KB.
-template <int D>
+template <int D, bool FP8>
 constexpr int smem_bytes() {
-  constexpr int need = Lay<D>::kQ + Lay<D>::kRingBytes + static_cast<int>(sizeof(Shared<D>));
+  using L = Lay<D, FP8>;
+  constexpr int need = L::kQ + L::kRing + L::kCodeRing + L::kStage + static_cast<int>(sizeof(Shared<D, FP8>));
   static_assert(need <= 113 * 1024, "two CTAs per SM");
-  static_assert(Lay<D>::kRingBytes >= kRows * D * 4, "the rows leave through the ring");
   return need;
 }
 
@@ -83,89 +92,84 @@ constexpr int kThreads = FP8 ? 384 : 256;
 constexpr int kRegsSoftmax = 128, kRegsOther = 56;
 static_assert(128 * kRegsSoftmax + 256 * kRegsOther <= 384 * 80, "register split");
 
-__device__ __forceinline__ bool quick_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort,
-                                           int32_t* err, uint64_t limit_ns) {
-  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) ||
-         warp_wait(bar, parity, abort, err, limit_ns);
-}
-
-// Whether one of the 16-bit values in w has its exponent all ones.
-template <bool FP8>
-__device__ __forceinline__ bool odd_value(uint32_t w) {
-  constexpr uint32_t e = FP8 ? 0x7C00u : 0x7F80u;
-  return (w & e) == e || (w & (e << 16)) == (e << 16);
-}
-template <bool FP8>
-__device__ __forceinline__ uint32_t even_value(uint32_t w) {   // those values as zero
-  constexpr uint32_t e = FP8 ? 0x7C00u : 0x7F80u;
-  if ((w & e) == e) w &= 0xffff0000u;
-  if ((w & (e << 16)) == (e << 16)) w &= 0xffffu;
-  return w;
+// Widens a tile's e4m3 codes (rows of D bytes, swizzled as they landed) into the fp16 tile
+// layout; four warps, 16 rows each.  D = 128: 8 lanes, which a shared-memory access serves
+// together, take 4 chunks of one half in two rows whose numbers differ in bits 0 and 2, so
+// that reads and writes fall into different banks.
+template <int D>
+__device__ __forceinline__ void widen(const uint8_t* codes, uint8_t* tile, int w, int lane) {
+  constexpr int kEach = D / 32;   // chunks of 16 codes of a lane
+  const int c = D == 128 ? 4 * ((lane >> 3) & 1) + (lane & 3) : lane & 3;
+  uint4 v[kEach];
+  auto row = [&](int i) {
+    return 16 * w + 8 * (D == 128 ? i >> 1 : i) +
+           (D == 128 ? ((lane >> 4) ^ ((lane & 4) ? 5 : 0)) ^ (2 * (i & 1)) : lane >> 2);
+  };
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int r = row(i);
+    v[i] = *reinterpret_cast<const uint4*>(codes + swz8<D>(r, c));
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int r = row(i), j = 2 * (c & 3);
+    uint8_t* to = tile + (c >> 2) * (kKeys * 128) + r * 128;
+    const uint2 a = e4m3x4_to_f16x4(v[i].x), b = e4m3x4_to_f16x4(v[i].y);
+    const uint2 d = e4m3x4_to_f16x4(v[i].z), e = e4m3x4_to_f16x4(v[i].w);
+    *reinterpret_cast<uint4*>(to + ((j ^ (r & 7)) << 4)) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint4*>(to + (((j + 1) ^ (r & 7)) << 4)) = make_uint4(d.x, d.y, e.x, e.y);
+  }
 }
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads<FP8>, 2)
-    pkv_tree_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+    pkv_tree_tc_kernel(const __grid_constant__ CUtensorMap qmap,
+                       const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
-  using L = Lay<D>;
+  using L = Lay<D, FP8>;
+  // (the merge, a programmatic dependent launch, waits for this grid's end itself)
+  asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;                            // [half][128 rows x 128 B]
-  uint8_t* sK = smem + L::kQ;                    // [slot][half][64 keys x 128 B]
-  uint8_t* sV = sK + L::kKSlots * L::kTile;
-  Shared<D>* sh = reinterpret_cast<Shared<D>*>(sK + L::kRingBytes);
+  uint8_t* sKV = smem + L::kQ;                   // [K, V][slot][half][64 keys x 128 B]
+  uint8_t* sCodes = sKV + L::kRing;              // [K, V][slot][64 keys x D]
+  uint8_t* sStage = sCodes + L::kCodeRing;
+  Shared<D, FP8>* sh = reinterpret_cast<Shared<D, FP8>*>(sStage + L::kStage);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    prefetch_tensor_map(&kmap);
-    prefetch_tensor_map(&vmap);
-  }
-  const int s = blockIdx.z, split = blockIdx.x, G = a.group, Hq = a.num_q_heads;
-  const int tile = blockIdx.y / a.num_kv_heads, kvh = blockIdx.y - tile * a.num_kv_heads;
-  const TreeSeq q = tree_seq(a, s);
-  if (q.err != 0 && split == 0 && blockIdx.y == 0 && threadIdx.x == 0) raise_error(a.err, q.err);
-  const int row0 = tile * kRows, rows = min(q.n * G - row0, kRows);
-  if (q.skip || rows <= 0) return;
+  const int G = a.group, Hq = a.num_q_heads;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-  // row r of the tile: its query row and head
-  auto tok_of = [&](int r) { return q.q0 + (row0 + r) / G; };
-  auto head_of = [&](int r) { return kvh * G + (row0 + r) % G; };
-  if (q.err != 0) {
-    if (split == 0)
-      for (int i = threadIdx.x; i < rows * D; i += blockDim.x)
-        out[(static_cast<int64_t>(tok_of(i / D)) * Hq + head_of(i / D)) * D + i % D] =
-            __float2bfloat16(0.f);
-    return;
-  }
-  const int nsplit = tree_splits(a, q.L);
-  if (split >= nsplit) return;
-  const int key_begin = split * a.split_blocks * kBlock;
-  const int key_end = min(q.L, key_begin + a.split_blocks * kBlock);
-  const int N = (key_end - key_begin + kKeys - 1) / kKeys;   // steps
-  const int b0 = key_begin / kBlock, b1 = (key_end + kBlock - 1) / kBlock;
-  const int32_t* bt = a.block_tables + s * a.bt_stride;
 
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
   if (threadIdx.x == 0) {
-    mbar_init(bar(sh->q_full), 4);
+    prefetch_tensor_map(&qmap);
+    prefetch_tensor_map(&kmap);
+    prefetch_tensor_map(&vmap);
+    mbar_init(bar(sh->q_full), 1);
+    mbar_init(bar(sh->q_empty), 1);
+    mbar_init(bar(sh->q_conv), 4);
     mbar_init(bar(sh->pv_done), 1);
     mbar_init(bar(sh->o_done), 1);
+    mbar_init(bar(sh->fixed), 4);
     mbar_init(bar(sh->drain), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(sh->s_full[i]), 1);
       mbar_init(bar(sh->p_full[i]), 4);
+      for (int j = 0; j < L::kSlots; ++j) {
+        mbar_init(bar(sh->full[i][j]), FP8 ? 4 : 1);
+        mbar_init(bar(sh->empty[i][j]), 1);
+      }
+      for (int j = 0; j < L::kCodeSlots; ++j) {
+        mbar_init(bar(sh->code_full[i][j]), 1);
+        mbar_init(bar(sh->code_empty[i][j]), 4);
+      }
     }
-    for (int i = 0; i < L::kKSlots; ++i) {
-      mbar_init(bar(sh->k_full[i]), FP8 && D == 128 ? 2 : 1);
-      mbar_init(bar(sh->k_empty[i]), 1);
-      mbar_init(bar(sh->k_land[i]), 1);
-    }
-    for (int i = 0; i < L::kVSlots; ++i) {
-      mbar_init(bar(sh->v_full[i]), FP8 && D == 128 ? 2 : 1);
-      mbar_init(bar(sh->v_empty[i]), 1);
-      mbar_init(bar(sh->v_land[i]), 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(bar(sh->seg_full[i]), 1);
+      mbar_init(bar(sh->seg_empty[i]), FP8 ? 11 : 7);   // the warps that read it
     }
     sh->abort = 0;
-    sh->v_odd = 0;
+    sh->v_odd[0] = sh->v_odd[1] = 0;
     fence_barrier_init();
   }
   if (warp == 7) tc::alloc(smem_u32(&sh->tmem_base), kCols);
@@ -175,73 +179,92 @@ __global__ void __launch_bounds__(kThreads<FP8>, 2)
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem_base, 0);
   volatile int32_t* abort = &sh->abort;
   const uint64_t wlim = wait_limit(a.wait_limit_ns);
-  auto wait = [&](uint64_t& b, int use, int slots) {   // the phase of a slot's `use`-th turn
+  auto wait = [&](uint64_t& b, int use, int slots) {   // the phase of a slot's turn in the use-th round
     return quick_wait(smem_u32(&b), static_cast<uint32_t>(use / slots) & 1, abort, a.err, wlim);
   };
+  // The CTA's i-th segment; false: there is none (or a wait gave up).
+  auto take = [&](int i, Seg& g) {
+    if (!wait(sh->seg_full[i % kSegs], i, kSegs)) return false;
+    g = sh->seg[i % kSegs];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(sh->seg_empty[i % kSegs]));
+    return g.steps >= 0;
+  };
+  Seg g;
 
   if (warp >= 4) {
     if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 4 || warp == 5) {
-      // ------------------------------------------------------------ copies
-      const bool is_v = warp == 5;
-      const int slots = is_v ? L::kVSlots : L::kKSlots;
-      uint64_t* land = FP8 ? (is_v ? sh->v_land : sh->k_land) : (is_v ? sh->v_full : sh->k_full);
-      uint64_t* empty = is_v ? sh->v_empty : sh->k_empty;
-      uint8_t* ring = is_v ? sV : sK;
+      // ------------------------------------------------------------ copies of K, V
+      const int is_v = warp - 4;
+      constexpr int kDepth = FP8 ? L::kCodeSlots : L::kSlots;
+      constexpr int kBytes = FP8 ? L::kCodes : L::kTile;
+      uint64_t* land = FP8 ? sh->code_full[is_v] : sh->full[is_v];
+      uint64_t* empty = FP8 ? sh->code_empty[is_v] : sh->empty[is_v];
+      uint8_t* ring = (FP8 ? sCodes : sKV) + is_v * kDepth * kBytes;
+      const CUtensorMap* map = is_v ? &vmap : &kmap;
       // several row tiles read the same keys: then they stay in L2
-      const uint64_t policy = q.n * G > kRows ? policy_evict_normal() : policy_evict_first();
-      auto ids = [&](int g) {   // block ids of eight steps, a lane a block
-        const int b = b0 + 32 * g + lane;
-        return b < b1 ? __ldg(bt + b) : -1;
-      };
-      int cur = ids(0), next = ids(1);
+      const uint64_t policy = a.cta_tiles > 1 ? policy_evict_normal() : policy_evict_first();
       // Test hook: the first K tile is withheld (no copy, no arrival).
       const bool withhold = a.debug_stall != 0 && !is_v;
-      int n = 0;
-      for (; n < N; ++n) {
-        if (n > 0 && (n & 7) == 0) {
-          cur = next;
-          next = ids((n >> 3) + 1);
-        }
-        if (n >= slots && !wait(empty[n % slots], n - slots, slots)) break;
-        if (withhold && n == 0) continue;
-        const uint32_t dst = smem_u32(ring + n % slots * L::kTile), full = bar(land[n % slots]);
-        int id[kStepBlocks];
-        bool ok[kStepBlocks];
-        uint32_t bytes = 0;
+      int n = 0;   // steps so far
+      bool go = true;
+      for (int si = 0; go && take(si, g); ++si) {
+        const int32_t* bt = a.block_tables + g.s * a.bt_stride;
+        const int b0 = g.step0 * kStepBlocks;
+        const int b1 = min((g.L + kBlock - 1) / kBlock, b0 + g.steps * kStepBlocks);
+        auto ids = [&](int k) {   // block ids of eight steps, a lane a block
+          const int b = b0 + 32 * k + lane;
+          return b < b1 ? __ldg(bt + b) : -1;
+        };
+        int cur = ids(0), next = ids(1);
+        for (int h = 0; h < g.steps; ++h, ++n) {
+          if (h > 0 && (h & 7) == 0) {
+            cur = next;
+            next = ids((h >> 3) + 1);
+          }
+          if (n >= kDepth && !wait(empty[n % kDepth], n - kDepth, kDepth)) {
+            go = false;
+            break;
+          }
+          if (withhold && n == 0) continue;
+          const uint32_t dst = smem_u32(ring + n % kDepth * kBytes), full = bar(land[n % kDepth]);
+          int id[kStepBlocks];
+          bool ok[kStepBlocks];
+          uint32_t bytes = 0;
 #pragma unroll
-        for (int b = 0; b < kStepBlocks; ++b) {
-          id[b] = __shfl_sync(0xffffffffu, cur, kStepBlocks * (n & 7) + b);
-          const bool in = b0 + n * kStepBlocks + b < b1;
-          ok[b] = in && id[b] >= 0 && id[b] < a.num_blocks;
-          if (!is_v && in && !ok[b] && lane == 0) raise_error(a.err, PKV_ERR_BLOCK_ID);
-          bytes += ok[b] ? kBlock * D * (FP8 ? 1 : 2) : 0;
-        }
-        if (lane == 0) {
-          if (bytes == 0) {
-            mbar_arrive(full);
-          } else {
-            mbar_arrive_expect_tx(full, bytes);
+          for (int b = 0; b < kStepBlocks; ++b) {
+            id[b] = __shfl_sync(0xffffffffu, cur, kStepBlocks * (h & 7) + b);
+            const bool in = b0 + h * kStepBlocks + b < b1;
+            ok[b] = in && id[b] >= 0 && id[b] < a.num_blocks;
+            if (!is_v && in && !ok[b] && lane == 0) raise_error(a.err, PKV_ERR_BLOCK_ID);
+            bytes += ok[b] ? kBlock * D * (FP8 ? 1 : 2) : 0;
+          }
+          if (lane == 0) {
+            if (bytes == 0) {
+              mbar_arrive(full);
+            } else {
+              mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
-            for (int b = 0; b < kStepBlocks; ++b) {
-              if (!ok[b]) continue;
-              if constexpr (FP8) {
-                tma_load_3d(dst + b * kBlock * D, is_v ? &vmap : &kmap, full, 0, kvh,
-                            id[b] * kBlock, policy);
-              } else {
+              for (int b = 0; b < kStepBlocks; ++b) {
+                if (!ok[b]) continue;
+                if constexpr (FP8) {
+                  tma_load_3d(dst + b * kBlock * D, map, full, 0, g.kvh, id[b] * kBlock, policy);
+                } else {
 #pragma unroll
-                for (int h = 0; h < L::kHalves; ++h)
-                  tma_load_3d(dst + h * L::kTHalf + b * 2048, is_v ? &vmap : &kmap, full, h * 64,
-                              kvh, id[b] * kBlock, policy);
+                  for (int k = 0; k < L::kHalves; ++k)
+                    tma_load_3d(dst + k * L::kTHalf + b * 2048, map, full, k * 64, g.kvh,
+                                id[b] * kBlock, policy);
+                }
               }
             }
           }
         }
       }
       // every copy has landed before the CTA's shared memory is given up
-      for (int i = max(0, n - slots); i < n; ++i)
+      for (int i = max(0, n - kDepth); i < n; ++i)
         if (lane == 0 && !(withhold && i == 0))
-          (void)mbar_wait(bar(land[i % slots]), static_cast<uint32_t>(i / slots) & 1);
+          (void)mbar_wait(bar(land[i % kDepth]), static_cast<uint32_t>(i / kDepth) & 1);
       __syncwarp();
     } else if (warp == 6) {
       // ------------------------------------------------------------ products
@@ -250,184 +273,243 @@ __global__ void __launch_bounds__(kThreads<FP8>, 2)
       constexpr uint32_t idO = FP8 ? tc::idesc_f16_f32(kRows, D, 0, 1)
                                    : tc::idesc_bf16_f32(kRows, D, 0, 1);
       const uint64_t dq = tc::smem_desc_sw128(smem_u32(sQ), 16, 1024);
-      const uint64_t dk = tc::smem_desc_sw128(smem_u32(sK), 16, 1024);
-      const uint64_t dv = tc::smem_desc_sw128(smem_u32(sV), L::kTHalf, 1024);
-      auto issue_s = [&](int h) {
-        const uint64_t db = dk + static_cast<uint64_t>((h % L::kKSlots * L::kTile) >> 4);
-        const uint32_t d = tmem + col_s(h);
-        if constexpr (D == 128) {
-          tc::mma_ss_x8<2, 4, 6, 1024, 1026, 1028, 1030, 2, 4, 6, 512, 514, 516, 518>(d, dq, db,
-                                                                                    idS, 0u);
-        } else {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_ss(d, dq + (kk * 32 >> 4), db + (kk * 32 >> 4), idS, kk > 0 ? 1u : 0u);
-        }
-        tc::commit(bar(sh->s_full[h & 1]));
-        tc::commit(bar(sh->k_empty[h % L::kKSlots]));
-      };
-      auto issue_pv = [&](int h) {
-        const uint64_t db = dv + static_cast<uint64_t>((h % L::kVSlots * L::kTile) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc::mma_ts(tmem + kColO, tmem + col_s(h) + 8 * kk, db + 128 * kk, idO,
-                     h > 0 || kk > 0 ? 1u : 0u);
-        tc::commit(bar(h == N - 1 ? sh->o_done : sh->pv_done));
-        tc::commit(bar(sh->v_empty[h % L::kVSlots]));
-      };
-      auto start_s = [&](int h) {
-        if (!wait(sh->k_full[h % L::kKSlots], h, L::kKSlots)) return false;
+      const uint64_t dk = tc::smem_desc_sw128(smem_u32(sKV), 16, 1024);
+      const uint64_t dv = tc::smem_desc_sw128(smem_u32(sKV) + L::kSlots * L::kTile, L::kTHalf, 1024);
+      int base = 0;   // steps before this segment
+      auto start_s = [&](int h) {   // S of the segment's step h
+        const int n = base + h;
+        if (!wait(sh->full[0][n % L::kSlots], n, L::kSlots)) return false;
         tc::fence_after_sync();
-        if (tc::elect_one()) issue_s(h);
+        if (tc::elect_one()) {
+          const uint64_t db = dk + static_cast<uint64_t>((n % L::kSlots * L::kTile) >> 4);
+          const uint32_t d = tmem + col_s(n);
+          if constexpr (D == 128) {
+            tc::mma_ss_x8<2, 4, 6, 1024, 1026, 1028, 1030, 2, 4, 6, 512, 514, 516, 518>(d, dq, db,
+                                                                                      idS, 0u);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              tc::mma_ss(d, dq + (kk * 32 >> 4), db + (kk * 32 >> 4), idS, kk > 0 ? 1u : 0u);
+          }
+          tc::commit(bar(sh->s_full[n & 1]));
+          tc::commit(bar(sh->empty[0][n % L::kSlots]));
+          if (h == g.steps - 1) tc::commit(bar(sh->q_empty));
+        }
         __syncwarp();
         return true;
       };
-      bool go = wait(sh->q_full, 0, 1) && start_s(0) && (N < 2 || start_s(1));
-      for (int h = 0; go && h < N; ++h) {
-        go = wait(sh->p_full[h & 1], h >> 1, 1) &&
-             wait(sh->v_full[h % L::kVSlots], h, L::kVSlots);
-        if (!go) break;
-        tc::fence_after_sync();
-        if (tc::elect_one()) issue_pv(h);
-        __syncwarp();
-        // (S over the columns that P was read from: products execute in their order)
-        if (h + 2 < N) go = start_s(h + 2);
+      bool go = true;
+      for (int si = 0; go && take(si, g); ++si) {
+        go = wait(FP8 ? sh->q_conv : sh->q_full, si, 1) && start_s(0) && (g.steps < 2 || start_s(1));
+        for (int h = 0; go && h < g.steps; ++h) {
+          const int n = base + h;
+          go = wait(sh->p_full[n & 1], n >> 1, 1) && wait(sh->full[1][n % L::kSlots], n, L::kSlots);
+          if (!go) break;
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            const uint64_t db = dv + static_cast<uint64_t>((n % L::kSlots * L::kTile) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              tc::mma_ts(tmem + kColO, tmem + col_s(n) + 8 * kk, db + 128 * kk, idO,
+                         h > 0 || kk > 0 ? 1u : 0u);
+            tc::commit(bar(h == g.steps - 1 ? sh->o_done : sh->pv_done));
+            tc::commit(bar(sh->empty[1][n % L::kSlots]));
+          }
+          __syncwarp();
+          // (S over the columns that P was read from: products execute in their order)
+          if (h + 2 < g.steps) go = start_s(h + 2);
+        }
+        base += g.steps;
       }
       if (tc::elect_one()) {   // every product completes before TMEM is freed
         tc::commit(bar(sh->drain));
         (void)mbar_wait(bar(sh->drain), 0);
       }
       __syncwarp();
-    } else if (FP8 && warp >= 8 && (D == 128 || warp == 8 || warp == 10)) {
-      // ------------------------------------------------------------ widening
-      // (D = 64: the widened rows lie over later rows' codes, so one warp takes a tile)
-      const bool is_v = warp >= 10;
-      const int slots = is_v ? L::kVSlots : L::kKSlots;
-      for (int n = 0; n < N; ++n) {
-        if (!wait((is_v ? sh->v_land : sh->k_land)[n % slots], n, slots)) break;
-        uint8_t* t = (is_v ? sV : sK) + n % slots * L::kTile;
-        if constexpr (D == 128) widen_tile_fp8<false, kKeys>(t, lane, (warp & 1) * 2, (warp & 1) * 2 + 2);
-        else widen_tile_fp8_d64<false, kKeys>(t, lane);
-        fence_proxy_async();   // generic writes, then the tensor core reads
+    } else if (warp == 7) {
+      // ------------------------------------------------------------ units, copies of Q
+      const int tile_rows = a.tile_toks * G;
+      int count = 0;         // segments so far
+      tree_walk(a, kKeys, [&](const Seg& e) {
+        if (count >= kSegs && !wait(sh->seg_empty[count % kSegs], count - kSegs, kSegs)) return false;
+        if (lane == 0) {
+          sh->seg[count % kSegs] = e;
+          mbar_arrive(bar(sh->seg_full[count % kSegs]));
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar((is_v ? sh->v_full : sh->k_full)[n % slots]));
+        if (count > 0 && !wait(sh->q_empty, count - 1, 1)) return false;
+        if (lane == 0) {   // (rows behind the sequence's: other rows, or zeros; not used)
+          mbar_arrive_expect_tx(bar(sh->q_full), L::kHalves * tile_rows * 128);
+#pragma unroll
+          for (int k = 0; k < L::kHalves; ++k)
+            tma_load_3d(smem_u32(sQ + k * L::kQHalf), &qmap, bar(sh->q_full), k * 64, e.kvh * G,
+                        e.q0 + e.row0 / G, policy_evict_normal());
+        }
+        ++count;
+        return true;
+      });
+      if (count > 0 && lane == 0) (void)mbar_wait(bar(sh->q_full), (count - 1) & 1);   // (landed)
+      __syncwarp();
+      if (count < kSegs || wait(sh->seg_empty[count % kSegs], count - kSegs, kSegs)) {
+        if (lane == 0) {
+          sh->seg[count % kSegs].steps = -1;
+          mbar_arrive(bar(sh->seg_full[count % kSegs]));
+        }
+      }
+      __syncwarp();
+    } else if constexpr (FP8) {
+      // ------------------------------------------------------------ widening
+      const int w = warp - 8;
+      int base = 0;
+      auto one = [&](int v, int n) {   // K's (0) or V's (1) tile of step n
+        if (!wait(sh->code_full[v][n % L::kCodeSlots], n, L::kCodeSlots)) return false;
+        if (n >= L::kSlots && !wait(sh->empty[v][n % L::kSlots], n - L::kSlots, L::kSlots)) return false;
+        widen<D>(sCodes + (v * L::kCodeSlots + n % L::kCodeSlots) * L::kCodes,
+                 sKV + (v * L::kSlots + n % L::kSlots) * L::kTile, w, lane);
+        fence_proxy_async();   // generic accesses, then the tensor core's reads and the next copy
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(sh->full[v][n % L::kSlots]));
+          mbar_arrive(bar(sh->code_empty[v][n % L::kCodeSlots]));
+        }
+        return true;
+      };
+      bool go = true;
+      for (int si = 0; go && take(si, g); ++si) {
+        go = one(0, base);
+        for (int h = 0; go && h < g.steps; ++h)   // (K a step ahead, as S is of P V)
+          go = (h + 1 >= g.steps || one(0, base + h + 1)) && one(1, base + h);
+        base += g.steps;
       }
     }
   } else {
     // ------------------------------------------------------------ softmax
     if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    tree_bad_sequences<D>(a, threadIdx.x, 128);
     const int row = warp * 32 + lane;            // tile row == TMEM lane
     const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const bool valid = row < rows, warp_valid = warp * 32 < rows;
-    float sl2 = fabsf(a.scale_log2), out_scale = 1.f;
-    // ---- this warp's rows of Q to shared memory (a negative scale's sign goes with them)
-    {
-      constexpr int kChunks = D / 8, kPer = 32 / kChunks, kIters = 32 / kPer;
-      const int c = lane % kChunks;
-      uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-      if constexpr (FP8) {
-        const int64_t at = static_cast<int64_t>(s) * a.num_kv_heads + kvh;
-        const float kd = __ldg(a.k_descale + at);
-        if (kd < 0.f) flip ^= 0x80008000u;
-        sl2 *= fabsf(kd);
-        out_scale = __ldg(a.v_descale + at);
-      }
-      int row_e = 0;
-#pragma unroll
-      for (int i0 = 0; i0 < kIters; i0 += 8) {
-        uint4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = warp * 32 + (i0 + i) * kPer + lane / kChunks;
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (r < rows)
-            v[i] = __ldg(reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(a.q) +
-                (static_cast<int64_t>(tok_of(r)) * Hq + head_of(r)) * D + 8 * c));
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = warp * 32 + (i0 + i) * kPer + lane / kChunks;
-          uint32_t w[4] = {v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip};
-          if constexpr (FP8) {   // to fp16, a row beyond its range scaled by a power of two
-            float amax = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
-#pragma unroll
-            for (int off = kChunks / 2; off > 0; off >>= 1)
-              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-            const int e = f16_fit_exponent(amax);
-            const float down = pow2f(-e);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = bf16x2_to_f16x2(w[k], down);
-            // lane j keeps the exponent of the warp's row j
-            const int mine = __shfl_sync(0xffffffffu, e, lane % kPer * kChunks);
-            if (lane / kPer == i0 + i) row_e = mine;
-          }
-          *reinterpret_cast<uint4*>(sQ + (c >> 3) * L::kQHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      if constexpr (FP8) sl2 *= pow2f(row_e);
-      fence_proxy_async();   // generic writes, then the tensor core reads
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sh->q_full));
-    }
-    sl2 = fmaxf(sl2, FLT_MIN);   // (above zero, so that a masked -inf stays what it is)
-    const uint64_t* mask =
-        a.tree_mask + static_cast<int64_t>(tok_of(valid ? row : rows - 1)) * a.mask_words;
-    float m = -INFINITY, l = 0.f;
+    int base = 0, pv = 0;                        // steps, and products' pv_done, before this segment
     bool done = true;
-    for (int h = 0; h < N; ++h) {
-      if (!wait(sh->s_full[h & 1], h >> 1, 1)) {
-        done = false;
-        break;
+    for (int si = 0; done && take(si, g); ++si) {
+      const bool valid = row < g.rows, warp_valid = warp * 32 < g.rows;
+      const TreeSeq q{g.q0, g.n, g.L, g.L - g.n, 0, false};
+      // row r of the tile: its query row and head
+      auto tok_of = [&](int r) { return g.q0 + (g.row0 + r) / G; };
+      auto head_of = [&](int r) { return g.kvh * G + (g.row0 + r) % G; };
+      const uint64_t* mask =
+          a.tree_mask + static_cast<int64_t>(tok_of(valid ? row : g.rows - 1)) * a.mask_words;
+      float sl2 = a.scale_log2, out_scale = 1.f;
+      if constexpr (FP8) {   // this thread's row of Q to fp16, scaled by a power of two into its range
+        const int64_t at = static_cast<int64_t>(g.s) * a.num_kv_heads + g.kvh;
+        sl2 *= __ldg(a.k_descale + at);
+        out_scale = __ldg(a.v_descale + at);
+        if (!wait(sh->q_full, si, 1)) break;
+        if (warp_valid) {
+          uint8_t* qrow = sQ + row * 128;
+          float amax = 0.f;
+#pragma unroll
+          for (int i = 0; i < L::kHalves * 8; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(qrow + (i >> 3) * L::kQHalf +
+                                                            (((i & 7) ^ (row & 7)) << 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+          }
+          const int ex = f16_fit_exponent(amax);
+          const float down = pow2f(-ex);
+          sl2 *= pow2f(ex);
+#pragma unroll
+          for (int i = 0; i < L::kHalves * 8; ++i) {
+            uint4* p = reinterpret_cast<uint4*>(qrow + (i >> 3) * L::kQHalf + (((i & 7) ^ (row & 7)) << 4));
+            const uint4 v = *p;
+            *p = make_uint4(bf16x2_to_f16x2(v.x, down), bf16x2_to_f16x2(v.y, down),
+                            bf16x2_to_f16x2(v.z, down), bf16x2_to_f16x2(v.w, down));
+          }
+          fence_proxy_async();   // generic writes, then the tensor core reads
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->q_conv));
       }
-      tc::fence_after_sync();
-      const uint32_t tS = lanes + col_s(h);
-      const int key0 = key_begin + h * kKeys;
-      const bool drafts = key0 + kKeys > q.first;   // keys that not every row sees, or none
-      if (drafts) {
-        // V's rows behind the last key become zero, and so do its drafted values that
-        // are not finite
-        if (!wait(sh->v_full[h % L::kVSlots], h, L::kVSlots)) {
+      float m = -INFINITY, l = 0.f;
+      for (int h = 0; h < g.steps; ++h) {
+        const int n = base + h;
+        if (!wait(sh->s_full[n & 1], n >> 1, 1)) {
           done = false;
           break;
         }
-        constexpr int kEach = L::kHalves * 4;       // 16-byte chunks of a thread
-        const int r = threadIdx.x >> 1, p = key0 + r;
-        uint8_t* vrow = sV + h % L::kVSlots * L::kTile + r * 128 +
-                        (D == 128 ? (threadIdx.x & 1) * L::kTHalf : 0);
-        if (p >= q.first) {
+        tc::fence_after_sync();
+        const uint32_t tS = lanes + col_s(n);
+        const int key0 = (g.step0 + h) * kKeys;
+        const bool drafts = key0 + kKeys > q.first;   // keys that not every row sees, or none
+        if (drafts) {
+          // V's rows behind the last key become zero, and so do its drafted values that
+          // are not finite.  (With one slot, the last step's V may not be there yet: its
+          // product is awaited first, else the wait for this one's would take the one before
+          // it, whose phase has the same parity.)
+          if ((L::kSlots == 1 && h > 0 && !wait(sh->pv_done, pv + h - 1, 1)) ||
+              !wait(sh->full[1][n % L::kSlots], n, L::kSlots)) {
+            done = false;
+            break;
+          }
+          constexpr int kEach = L::kHalves * 4;       // 16-byte chunks of a thread
+          const int r = threadIdx.x >> 1, p = key0 + r;
+          uint8_t* vrow = sKV + (L::kSlots + n % L::kSlots) * L::kTile + r * 128 +
+                          (D == 128 ? (threadIdx.x & 1) * L::kTHalf : 0);
+          auto chunk = [&](int i) {   // (in turns, so that 8 lanes' chunks lie in different banks)
+            return reinterpret_cast<uint4*>(
+                vrow + 16 * (D == 128 ? (i + r) & 7 : 4 * (threadIdx.x & 1) + ((i + r) & 3)));
+          };
+          if (p >= q.L) {
 #pragma unroll
-          for (int i = 0; i < kEach; ++i) {
-            const int c = D == 128 ? (i + r) & 7 : (4 * (threadIdx.x & 1) + ((i + r) & 3));
-            uint4* at = reinterpret_cast<uint4*>(vrow + 16 * c);
-            if (p >= q.L) {
-              *at = make_uint4(0, 0, 0, 0);
-            } else {
-              const uint4 v = *at;
-              if (odd_value<FP8>(v.x) || odd_value<FP8>(v.y) || odd_value<FP8>(v.z) ||
-                  odd_value<FP8>(v.w)) {
-                *at = make_uint4(even_value<FP8>(v.x), even_value<FP8>(v.y), even_value<FP8>(v.z),
-                                 even_value<FP8>(v.w));
-                sh->v_odd = 1;
+            for (int i = 0; i < kEach; ++i) *chunk(i) = make_uint4(0, 0, 0, 0);
+          } else if (p >= q.first) {
+            uint32_t odd = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+              const uint4 v = *chunk(i);
+              odd |= odd_halves<FP8>(v.x) | odd_halves<FP8>(v.y) | odd_halves<FP8>(v.z) | odd_halves<FP8>(v.w);
+            }
+            if (odd != 0) {
+              sh->v_odd[si & 1] = si + 1;
+#pragma unroll 1
+              for (int i = 0; i < kEach; ++i) {
+                const uint4 v = *chunk(i);
+                *chunk(i) = make_uint4(even_value<FP8>(v.x), even_value<FP8>(v.y), even_value<FP8>(v.z),
+                                       even_value<FP8>(v.w));
               }
             }
           }
+          fence_proxy_async();   // generic writes, then the tensor core reads
         }
-        fence_proxy_async();   // generic writes, then the tensor core reads
-      }
-      if (warp_valid) {
-        const uint64_t seen = drafts ? tree_bits(mask, q, key0) : ~0ull;
-        float alpha = 1.f, ls;
-        uint32_t pk[kKeys / 2];
-        bool find = __any_sync(0xffffffffu, valid && m == -INFINITY);
+        if (warp_valid) {
+          const uint64_t seen = drafts ? tree_bits(mask, q, key0) : ~0ull;
+          float alpha = 1.f, ls;
+          uint32_t pk[kKeys / 2];
+          bool find = __any_sync(0xffffffffu, valid && m == -INFINITY);
 #pragma unroll 1
-        while (true) {
-          if (find) {   // the largest visible score
-            float top = -INFINITY;
+          while (true) {
+            if (find) {   // the largest visible score
+              float top = -INFINITY;
+#pragma unroll 1
+              for (int c0 = 0; c0 < kKeys; c0 += 32) {
+                uint32_t r[32];
+                tc::ld32(tS + c0, r);
+                tc::wait_ld();
+                const uint32_t bits = static_cast<uint32_t>(seen >> c0);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  top = fmaxf(top, (bits >> c & 1) ? __uint_as_float(r[c]) * sl2 : -INFINITY);
+              }
+              if (top > m) {
+                alpha = m == -INFINITY ? 0.f : ex2(m - top);
+                l *= alpha;
+                m = top;
+              }
+            }
+            const float neg_m = m == -INFINITY ? 0.f : -m;
+            const uint64_t f2 = tc::pack_f32x2(sl2, sl2), a2 = tc::pack_f32x2(neg_m, neg_m);
+            uint64_t acc = 0;
 #pragma unroll
             for (int c0 = 0; c0 < kKeys; c0 += 32) {
               uint32_t r[32];
@@ -435,134 +517,115 @@ __global__ void __launch_bounds__(kThreads<FP8>, 2)
               tc::wait_ld();
               const uint32_t bits = static_cast<uint32_t>(seen >> c0);
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                top = fmaxf(top, (bits >> c & 1) ? __uint_as_float(r[c]) : -INFINITY);
+              for (int c = 0; c < 32; c += 2) {
+                float y0, y1;
+                tc::fma_f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1]), f2, a2, y0, y1);
+                if (drafts) {   // (warp-uniform)
+                  y0 = (bits >> c & 1) ? y0 : -INFINITY;
+                  y1 = (bits >> (c + 1) & 1) ? y1 : -INFINITY;
+                }
+                y0 = ex2(y0);
+                y1 = ex2(y1);
+                const uint32_t w = pack2<FP8>(y0, y1);
+                pk[(c0 + c) / 2] = w;
+                if constexpr (FP8) tc::add_f32x2(acc, y0, y1);
+                else tc::add_f32x2(acc, bf16_lo(w), bf16_hi(w));
+              }
             }
-            const float mt = top * sl2;
-            if (mt > m) {
-              alpha = m == -INFINITY ? 0.f : ex2(m - mt);
-              l *= alpha;
-              m = mt;
-            }
+            ls = tc::sum_f32x2(acc);
+            if (find || !__any_sync(0xffffffffu, valid && !(ls <= kMost<FP8>))) break;
+            find = true;
           }
-          const float neg_m = m == -INFINITY ? 0.f : -m;
-          const uint64_t f2 = tc::pack_f32x2(sl2, sl2), a2 = tc::pack_f32x2(neg_m, neg_m);
-          uint64_t acc = 0;
-#pragma unroll
-          for (int c0 = 0; c0 < kKeys; c0 += 32) {
-            uint32_t r[32];
-            tc::ld32(tS + c0, r);
-            tc::wait_ld();
-            if (drafts) {
-              const uint32_t bits = static_cast<uint32_t>(seen >> c0);
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (!(bits >> c & 1)) r[c] = 0xff800000u;   // -infinity
+          if (h > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // rescale O
+            // (P V of h - 1 is the last that was issued: that of h waits for this warp)
+            if (!wait(sh->pv_done, pv + h - 1, 1)) {
+              done = false;
+              break;
             }
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              float y0, y1;
-              tc::fma_f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1]), f2, a2, y0, y1);
-              y0 = ex2(y0);
-              y1 = ex2(y1);
-              const uint32_t w = pack2<FP8>(y0, y1);
-              pk[(c0 + c) / 2] = w;
-              if constexpr (FP8) tc::add_f32x2(acc, y0, y1);
-              else tc::add_f32x2(acc, bf16_lo(w), bf16_hi(w));
-            }
-          }
-          ls = tc::sum_f32x2(acc);
-          if (find || !__any_sync(0xffffffffu, valid && !(ls <= kMost<FP8>))) break;
-          find = true;
-        }
-        if (h > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // rescale O
-          // (P V of h - 1 is the last that was issued: that of h waits for this warp)
-          if (!quick_wait(bar(sh->pv_done), (h - 1) & 1, abort, a.err, wlim)) {
-            done = false;
-            break;
-          }
-          tc::fence_after_sync();
+            tc::fence_after_sync();
 #pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t o[32];
-            tc::ld32(lanes + kColO + c0, o);
-            tc::wait_ld();
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o[32];
+              tc::ld32(lanes + kColO + c0, o);
+              tc::wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-            tc::st32(lanes + kColO + c0, o);
+              for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+              tc::st32(lanes + kColO + c0, o);
+            }
           }
+          tc::st32(tS, pk);
+          l += ls;
+          tc::wait_st();
+          tc::fence_before_sync();
         }
-        tc::st32(tS, pk);
-        l += ls;
-        tc::wait_st();
-        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sh->p_full[n & 1]));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(sh->p_full[h & 1]));
-    }
-    // ---- the rows out, through the ring (every tile has been read), 16-byte chunks of a
-    // row swapped about so that neither a column nor a row of them falls into one bank
-    const bool ok = done && quick_wait(bar(sh->o_done), 0, abort, a.err, wlim);
-    named_barrier(1, 128);       // (v_odd: every softmax warp's)
-    if (ok && warp_valid) {
-      tc::fence_after_sync();
-      const bool odd = *reinterpret_cast<volatile int32_t*>(&sh->v_odd) != 0;
-      const float inv = l == 0.f ? 0.f : out_scale / l;   // (a NaN stays)
-      uint8_t* mine = sK + warp * 32 * D * 4;
+      // ---- the rows out, 32 columns at a time through shared memory, 16-byte chunks of a row
+      // swapped about so that neither a column nor a row of them falls into one bank
+      if (lane == 0) mbar_arrive(bar(sh->fixed));   // (v_odd: every softmax warp's)
+      done = done && wait(sh->o_done, si, 1) && wait(sh->fixed, si, 1);
+      if (done && warp_valid) {
+        tc::fence_after_sync();
+        const bool odd = *reinterpret_cast<volatile int32_t*>(&sh->v_odd[si & 1]) == si + 1;
+        const float inv = l == 0.f ? 0.f : out_scale / l;   // (a NaN stays)
+        uint8_t* mine = sStage + warp * 32 * 128;
+        const int count = min(g.rows - warp * 32, 32);
+        const int64_t part = (static_cast<int64_t>(g.part) * a.cta_tiles + blockIdx.x % a.cta_tiles) * a.part_rows + warp * 32;
+        // where this lane's row begins, in out or in the partials (rows behind the last: the last)
+        const int mine_row = min(row, g.rows - 1);
+        const int64_t at = (g.part < 0 ? static_cast<int64_t>(tok_of(mine_row)) * Hq + head_of(mine_row)
+                                       : part + lane) * D;
+        // (this lane's part of a row's 32 columns: 4 lanes a row of bf16, 8 of fp32)
+        const int oc = g.part < 0 ? lane & 3 : lane & 7, orow = g.part < 0 ? lane >> 2 : lane >> 3;
+        const int ostep = g.part < 0 ? 8 : 4;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        uint32_t o[32];
-        tc::ld32(lanes + kColO + c0, o);
-        tc::wait_ld();
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t o[32];
+          tc::ld32(lanes + kColO + c0, o);
+          tc::wait_ld();
+          __syncwarp();   // (the columns before are read)
 #pragma unroll
-        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
-        if (odd && valid) {   // V values that are not finite, of the drafts that this row sees
-          for (int p = max(q.first, key_begin); p < key_end; ++p) {
-            const int j = p - q.first, b = __ldg(bt + p / kBlock);
-            if (!(__ldg(mask + (j >> 6)) >> (j & 63) & 1) || b < 0 || b >= a.num_blocks) continue;
-            const int64_t at = ((static_cast<int64_t>(b) * kBlock + p % kBlock) * a.num_kv_heads + kvh) * D + c0;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              float v;
-              if constexpr (FP8)
-                v = f16_lo(e4m3x4_to_f16x4(static_cast<const uint8_t*>(a.v_cache)[at + c]).x);
-              else
-                v = __bfloat162float(static_cast<const __nv_bfloat16*>(a.v_cache)[at + c]);
-              if (!(fabsf(v) <= FLT_MAX)) o[c] = __float_as_uint(__uint_as_float(o[c]) + v);
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(mine + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                            __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+          __syncwarp();
+#pragma unroll 2
+          for (int r = orow; r < 32; r += ostep) {
+            const uint8_t* src = mine + r * 128;
+            const int64_t to = __shfl_sync(0xffffffffu, at, r) + c0;
+            if (g.part < 0) {
+              const float4 x = *reinterpret_cast<const float4*>(src + (((2 * oc) ^ (r & 7)) << 4));
+              const float4 y = *reinterpret_cast<const float4*>(src + (((2 * oc + 1) ^ (r & 7)) << 4));
+              if (r < count)
+                *reinterpret_cast<uint4*>(out + to + 8 * oc) =
+                    make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y),
+                               pack_bf16(y.z, y.w));
+            } else if (r < count) {
+              *reinterpret_cast<float4*>(a.ws_o + to + 4 * oc) =
+                  *reinterpret_cast<const float4*>(src + ((oc ^ (r & 7)) << 4));
             }
           }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(mine + lane * D * 4 + (((c0 / 4 + i) ^ (lane & 7)) << 4)) =
-              make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-      }
-      __syncwarp();
-      const int count = min(rows - warp * 32, 32);
-      if (nsplit == 1) {
-        constexpr int kLanes = D / 8;              // lanes of a bf16 row
-        const int c = lane % kLanes;
-        for (int r = lane / kLanes; r < count; r += 32 / kLanes) {
-          const uint8_t* src = mine + r * D * 4;
-          const float4 x = *reinterpret_cast<const float4*>(src + (((2 * c) ^ (r & 7)) << 4));
-          const float4 y = *reinterpret_cast<const float4*>(src + (((2 * c + 1) ^ (r & 7)) << 4));
-          const int t = warp * 32 + r;
-          *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(tok_of(t)) * Hq + head_of(t)) * D + 8 * c) =
-              make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y),
-                         pack_bf16(y.z, y.w));
+        if (odd) {
+          __syncwarp();
+#pragma unroll 1
+          for (int r = 0; r < count; ++r) {
+            const int64_t to = __shfl_sync(0xffffffffu, at, r);
+#pragma unroll 1
+            for (int d = lane; d < D; d += 32)
+              add_odd_values<FP8, D>(a, g.s, g.kvh, q.first, g.step0 * kKeys,
+                                     min(g.L, (g.step0 + g.steps) * kKeys),
+                                     a.tree_mask + static_cast<int64_t>(tok_of(warp * 32 + r)) * a.mask_words,
+                                     d, g.part < 0 ? nullptr : a.ws_o + to + d,
+                                     g.part < 0 ? out + to + d : nullptr);
+          }
         }
-      } else {
-        constexpr int kLanes = D / 4;              // lanes of an fp32 row
-        const int c = lane % kLanes;
-        for (int r = lane / kLanes; r < count; r += 32 / kLanes) {
-          const int t = warp * 32 + r;
-          *reinterpret_cast<float4*>(a.ws_o + tree_partial(a, tok_of(t), head_of(t), split) * D + 4 * c) =
-              *reinterpret_cast<const float4*>(mine + r * D * 4 + ((c ^ (r & 7)) << 4));
-        }
-        if (valid)
-          a.ws_lse[tree_partial(a, tok_of(row), head_of(row), split)] =
-              l == 0.f ? -INFINITY : m + log2f(l);
+        if (g.part >= 0 && valid) a.ws_lse[part + lane] = l == 0.f ? -INFINITY : m + log2f(l);
       }
+      base += g.steps;
+      pv += g.steps - 1;
     }
   }
   tc::fence_before_sync();
@@ -573,29 +636,117 @@ __global__ void __launch_bounds__(kThreads<FP8>, 2)
   }
 }
 
+// Merges the partials of the units that several workers computed: one warp per (query row,
+// q head), out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).  The first worker of a unit
+// holds its partial in the second of its two places, the others in their first.
+template <int D>
+__global__ void __launch_bounds__(128) pkv_tree_tc_merge_kernel(const TreeArgs a) {
+  constexpr int PER = D / 32;
+  constexpr int kUnroll = 8;   // partials in flight
+  // (a programmatic dependent launch: the partials are visible once this returns)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int64_t t = w / a.num_q_heads;
+  if (t >= a.num_tokens) return;
+  const int s = seq_of_row(a.query_start_loc, a.num_seqs, static_cast<int>(t));
+  if (s < 0) return;   // a row of no sequence
+  const TreeSeq q = tree_seq(a, s);
+  if (q.skip || q.err != 0 || t < q.q0 || t >= q.q0 + q.n) return;
+  const int hq = static_cast<int>(w - t * a.num_q_heads), kvh = hq / a.group;
+  const int tile_rows = a.tile_toks * a.group;
+  const int r = (static_cast<int>(t) - q.q0) * a.group + hq - kvh * a.group;
+  const int tile = r / tile_rows, tg = tile / a.cta_tiles;
+  const int2 span = a.span[(static_cast<int64_t>(s) * a.max_groups + tg) * a.num_kv_heads + kvh];
+  if (span.y <= 1) return;
+  auto place = [&](int i) {   // row of partial i
+    return ((static_cast<int64_t>(span.x + i) * 2 + (i == 0 ? 1 : 0)) * a.cta_tiles +
+            tile - tg * a.cta_tiles) * a.part_rows + r - tile * tile_rows;
+  };
+  float M = -INFINITY;
+  bool nan = false;
+  for (int i = lane; i < span.y; i += 32) {
+    const float e = a.ws_lse[place(i)];
+    M = fmaxf(M, e);
+    nan = nan || e != e;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  if (__any_sync(0xffffffffu, nan)) M = NAN;
+  float acc[PER] = {}, den = 0.f;
+  if (M != -INFINITY) {
+    for (int i0 = 0; i0 < span.y; i0 += kUnroll) {
+      float v[kUnroll][PER], e[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        e[u] = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[u][k] = 0.f;
+        if (i0 + u < span.y) {
+          const int64_t at = place(i0 + u);
+          e[u] = a.ws_lse[at];
+          const float* src = a.ws_o + at * D + lane * PER;
+          if constexpr (PER == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src);
+          else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (e[u] == -INFINITY) continue;   // a part that the row sees nothing of
+        const float f = exp2f(e[u] - M);
+        den += f;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) acc[k] = fmaf(f, v[u][k], acc[k]);
+      }
+    }
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + w * D + lane * PER;
+#pragma unroll
+  for (int k = 0; k < PER; k += 2)
+    *reinterpret_cast<__nv_bfloat162*>(out + k) = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
+}
+
 template <int D, bool FP8>
-cudaError_t launch_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeArgs& a,
-                     cudaStream_t stream) {
-  constexpr int smem = smem_bytes<D>();
+cudaError_t launch_t(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                     const TreeArgs& a, cudaStream_t stream) {
+  constexpr int smem = smem_bytes<D, FP8>();
   auto kfn = pkv_tree_tc_kernel<D, FP8>;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  TreeArgs b = a;
-  debug_wait_settings(&b.wait_limit_ns, &b.debug_stall);
-  const int64_t tiles = (static_cast<int64_t>(a.max_query_len) * a.group + kRows - 1) / kRows;
-  kfn<<<dim3(a.max_splits, static_cast<unsigned>(a.num_kv_heads * tiles), a.num_seqs),
-        kThreads<FP8>, smem, stream>>>(kmap, vmap, b);
+  kfn<<<static_cast<unsigned>(a.workers) * a.cta_tiles, kThreads<FP8>, smem, stream>>>(qmap, kmap, vmap, a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_tree_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeArgs& a,
-                           int head_size, bool fp8, cudaStream_t stream) {
-  if (fp8) return head_size == 128 ? launch_t<128, true>(kmap, vmap, a, stream)
-                                   : launch_t<64, true>(kmap, vmap, a, stream);
-  return head_size == 128 ? launch_t<128, false>(kmap, vmap, a, stream)
-                          : launch_t<64, false>(kmap, vmap, a, stream);
+cudaError_t launch_tree_tc(const CUtensorMap& qmap, const CUtensorMap& kmap,
+                           const CUtensorMap& vmap, const TreeArgs& a, int head_size, bool fp8,
+                           cudaStream_t stream) {
+  TreeArgs b = a;
+  debug_wait_settings(&b.wait_limit_ns, &b.debug_stall);
+  cudaError_t e;
+  if (a.keys_on_m)
+    e = launch_tree_keys(qmap, kmap, vmap, b, fp8, stream);
+  else if (fp8)
+    e = head_size == 128 ? launch_t<128, true>(qmap, kmap, vmap, b, stream)
+                         : launch_t<64, true>(qmap, kmap, vmap, b, stream);
+  else
+    e = head_size == 128 ? launch_t<128, false>(qmap, kmap, vmap, b, stream)
+                         : launch_t<64, false>(qmap, kmap, vmap, b, stream);
+  if (e != cudaSuccess || a.whole) return e;
+  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return head_size == 128 ? cudaLaunchKernelEx(&cfg, pkv_tree_tc_merge_kernel<128>, a)
+                          : cudaLaunchKernelEx(&cfg, pkv_tree_tc_merge_kernel<64>, a);
 }
 
 }  // namespace pkv
