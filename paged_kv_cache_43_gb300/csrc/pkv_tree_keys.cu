@@ -27,7 +27,7 @@ namespace {
 constexpr int D = 128;
 constexpr int kKeys = kTreeKeysStep;            // keys of a step
 constexpr int kStepBlocks = kKeys / kBlock;
-constexpr int kTHalf = kKeys * 128, kTile = 2 * kTHalf, kCodes = kKeys * D;
+constexpr int kTHalf = kKeys * 128, kTile = 2 * kTHalf;
 // Steps under way, with an S^T and a P^T each: a step's way from S^T over the softmax warps, P V and
 // the next S^T into the same buffer takes 2.5 us, most of it the warps' waits for one another.
 constexpr int kBufs = 3;
@@ -38,22 +38,19 @@ __device__ __forceinline__ uint32_t col_o(int i) { return 128u + 32u * (i & 1); 
 template <bool FP8>
 constexpr float kMost = FP8 ? 32768.f : 0x1p60f;   // (fp16 weights reach 65504)
 
-template <bool FP8>
-struct Lay {
-  static constexpr int kKSlots = FP8 ? 1 : 2, kVSlots = FP8 ? 2 : 3;         // operand tiles
-  static constexpr int kKCodes = FP8 ? 2 : 0, kVCodes = FP8 ? 2 : 0;         // tiles of codes
-  static constexpr int kRing = (kKSlots + kVSlots) * kTile + (kKCodes + kVCodes) * kCodes;
-};
+// Slots of K and V tiles.  e4m3 codes land in the first half of a slot (its columns 0-63) and are
+// widened in place: with rings of their own for the codes there was room for one tile of K to
+// be multiplied from, and its way round (widen, product, widen) took 2 us a step.
+constexpr int kKSlots = 2, kVSlots = 3;
 
 template <bool FP8, int N>
 struct Shared {
-  using L = Lay<FP8>;
   uint64_t q_full, q_empty, q_conv, drain;
   uint64_t s_full[kBufs], p_full[kBufs];
   // of segment i: [i % 2]; its rows' sums and last product are there, its rows are out
   uint64_t sum_full[2], o_done[2], sum_empty[2];
-  uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3];
-  uint64_t kc_full[2], kc_empty[2], vc_full[2], vc_empty[2];
+  uint64_t k_full[kKSlots], k_empty[kKSlots], v_full[kVSlots], v_empty[kVSlots];
+  uint64_t k_land[kKSlots], v_land[kVSlots];   // e4m3: the codes are there
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   Seg seg[kSegs];
   uint32_t tmem_base;
@@ -70,7 +67,7 @@ struct Shared {
 
 template <bool FP8, int N>
 constexpr int smem_bytes() {
-  constexpr int need = 2 * N * 128 + kBufs * kKeys * 128 + Lay<FP8>::kRing +
+  constexpr int need = 2 * N * 128 + kBufs * kKeys * 128 + (kKSlots + kVSlots) * kTile +
                        static_cast<int>(sizeof(Shared<FP8, N>)) + 1024;
   static_assert(need <= 227 * 1024, "shared memory");
   return need > 120 * 1024 ? need : 120 * 1024;   // (one CTA per SM)
@@ -128,16 +125,18 @@ __device__ __forceinline__ int across(float (&v)[N], int lane, Op op) {   // (of
   }
 }
 
-// Widens 16 rows (of batch b) of a tile's e4m3 codes into the fp16 tile layout: 8 lanes, which a
-// shared-memory access serves together, take 4 chunks of one half in two rows whose numbers
+// Widens 16 rows (of batch b) of a tile's e4m3 codes in place into the fp16 tile layout (a row's
+// codes lie where the first half of its fp16 values goes, and the warp reads all of its
+// rows before it writes): 8 lanes, which a shared-memory access serves together, take 4 chunks of one half in two rows whose numbers
 // differ in bits 0 and 2, so that reads and writes fall into different banks.
-__device__ __forceinline__ void widen16(const uint8_t* codes, uint8_t* tile, int b, int lane) {
+__device__ __forceinline__ void widen16(uint8_t* tile, int b, int lane) {
   const int c = 4 * ((lane >> 3) & 1) + (lane & 3), j = 2 * (c & 3);
   const int r0 = (lane >> 4) ^ ((lane & 4) ? 5 : 0);
   uint4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    v[i] = *reinterpret_cast<const uint4*>(codes + swz8<D>(16 * b + 8 * (i >> 1) + (r0 ^ (2 * (i & 1))), c));
+    v[i] = *reinterpret_cast<const uint4*>(tile + swz8<D>(16 * b + 8 * (i >> 1) + (r0 ^ (2 * (i & 1))), c));
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 16 * b + 8 * (i >> 1) + (r0 ^ (2 * (i & 1)));
@@ -154,7 +153,6 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
     pkv_tree_keys_kernel(const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const TreeArgs a) {
-  using L = Lay<FP8>;
   using Sh = Shared<FP8, N>;
   // (the merge, a programmatic dependent launch, waits for this grid's end itself)
   asm volatile("griddepcontrol.launch_dependents;");
@@ -162,10 +160,8 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sK = smem;                                   // [slot][half][128 keys x 128 B]
-  uint8_t* sV = sK + L::kKSlots * kTile;
-  uint8_t* sKc = sV + L::kVSlots * kTile;               // [slot][128 keys x 128 codes]
-  uint8_t* sVc = sKc + L::kKCodes * kCodes;
-  uint8_t* sP = sVc + L::kVCodes * kCodes;              // [3][128 keys x 64 rows]
+  uint8_t* sV = sK + kKSlots * kTile;
+  uint8_t* sP = sV + kVSlots * kTile;                   // [3][128 keys x 64 rows]
   uint8_t* sQ = sP + kBufs * kKeys * 128;                   // [half][N rows x 128 B]
   Sh* sh = reinterpret_cast<Sh*>(sQ + 2 * N * 128);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -186,20 +182,20 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
       mbar_init(bar(sh->o_done[i]), 1);
       mbar_init(bar(sh->sum_full[i]), 4);
       mbar_init(bar(sh->sum_empty[i]), 4);
-      mbar_init(bar(sh->k_full[i]), FP8 ? 8 : 1);
-      mbar_init(bar(sh->k_empty[i]), 1);
-      mbar_init(bar(sh->kc_full[i]), 1);
-      mbar_init(bar(sh->kc_empty[i]), 8);
-      mbar_init(bar(sh->vc_full[i]), 1);
-      mbar_init(bar(sh->vc_empty[i]), 8);
     }
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(bar(sh->s_full[i]), 1);
       mbar_init(bar(sh->p_full[i]), 4);
     }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < kKSlots; ++i) {
+      mbar_init(bar(sh->k_full[i]), FP8 ? 8 : 1);
+      mbar_init(bar(sh->k_empty[i]), 1);
+      mbar_init(bar(sh->k_land[i]), 1);
+    }
+    for (int i = 0; i < kVSlots; ++i) {
       mbar_init(bar(sh->v_full[i]), FP8 ? 8 : 1);
       mbar_init(bar(sh->v_empty[i]), 1);
+      mbar_init(bar(sh->v_land[i]), 1);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar(sh->seg_full[i]), 1);
@@ -234,11 +230,10 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
     if (warp == 4 || warp == 5) {
       // ------------------------------------------------------------ copies of K, V
       const bool is_v = warp == 5;
-      const int depth = is_v ? (FP8 ? L::kVCodes : L::kVSlots) : (FP8 ? L::kKCodes : L::kKSlots);
-      constexpr int kBytes = FP8 ? kCodes : kTile;
-      uint64_t* land = FP8 ? (is_v ? sh->vc_full : sh->kc_full) : (is_v ? sh->v_full : sh->k_full);
-      uint64_t* empty = FP8 ? (is_v ? sh->vc_empty : sh->kc_empty) : (is_v ? sh->v_empty : sh->k_empty);
-      uint8_t* ring = FP8 ? (is_v ? sVc : sKc) : (is_v ? sV : sK);
+      const int depth = is_v ? kVSlots : kKSlots;
+      uint64_t* land = FP8 ? (is_v ? sh->v_land : sh->k_land) : (is_v ? sh->v_full : sh->k_full);
+      uint64_t* empty = is_v ? sh->v_empty : sh->k_empty;
+      uint8_t* ring = is_v ? sV : sK;
       const CUtensorMap* map = is_v ? &vmap : &kmap;
       // several row tiles read the same keys: then they stay in L2
       const uint64_t policy = a.cta_tiles > 1 ? policy_evict_normal() : policy_evict_first();
@@ -265,7 +260,7 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
             break;
           }
           if (withhold && n == 0) continue;
-          const uint32_t dst = smem_u32(ring + n % depth * kBytes), full = bar(land[n % depth]);
+          const uint32_t dst = smem_u32(ring + n % depth * kTile), full = bar(land[n % depth]);
           // blocks that there are, a bit each (bad ids are said once, and left out)
           const int blk = b0 + h * kStepBlocks + (lane & 7);
           const int id = __shfl_sync(0xffffffffu, cur, 8 * (h & 3) + (lane & 7));
@@ -307,14 +302,14 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
       int base = 0;   // steps before this segment
       auto start_s = [&](int h) {   // S^T of the segment's step h
         const int n = base + h;
-        if (!wait(sh->k_full[n % L::kKSlots], n, L::kKSlots)) return false;
+        if (!wait(sh->k_full[n % kKSlots], n, kKSlots)) return false;
         tc::fence_after_sync();
         if (tc::elect_one()) {
-          const uint64_t da = dk + static_cast<uint64_t>((n % L::kKSlots * kTile) >> 4);
+          const uint64_t da = dk + static_cast<uint64_t>((n % kKSlots * kTile) >> 4);
           tc::mma_ss_x8<2, 4, 6, 1024, 1026, 1028, 1030, 2, 4, 6, QH, QH + 2, QH + 4, QH + 6>(
               tmem + col_s(n), da, dq, idS, 0u);
           tc::commit(bar(sh->s_full[n % kBufs]));
-          tc::commit(bar(sh->k_empty[n % L::kKSlots]));
+          tc::commit(bar(sh->k_empty[n % kKSlots]));
           if (h == g.steps - 1) tc::commit(bar(sh->q_empty));
         }
         __syncwarp();
@@ -326,18 +321,18 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
         for (int h = 0; go && h < min(kBufs, g.steps); ++h) go = start_s(h);
         for (int h = 0; go && h < g.steps; ++h) {
           const int n = base + h;
-          go = wait(sh->p_full[n % kBufs], n, kBufs) && wait(sh->v_full[n % L::kVSlots], n, L::kVSlots);
+          go = wait(sh->p_full[n % kBufs], n, kBufs) && wait(sh->v_full[n % kVSlots], n, kVSlots);
           // (O^T of the segment before the last is out)
           if (go && h == 0 && si >= 2) go = wait(sh->sum_empty[si & 1], (si >> 1) - 1, 1);
           if (!go) break;
           tc::fence_after_sync();
           if (tc::elect_one()) {
-            const uint64_t da = dv + static_cast<uint64_t>((n % L::kVSlots * kTile) >> 4);
+            const uint64_t da = dv + static_cast<uint64_t>((n % kVSlots * kTile) >> 4);
             const uint64_t db = dp + static_cast<uint64_t>((n % kBufs * kKeys * 128) >> 4);
             tc::mma_ss_x8<128, 256, 384, 512, 640, 768, 896, 128, 256, 384, 512, 640, 768, 896>(
                 tmem + col_o(si), da, db, idO, h > 0 ? 1u : 0u);
             if (h == g.steps - 1) tc::commit(bar(sh->o_done[si & 1]));
-            tc::commit(bar(sh->v_empty[n % L::kVSlots]));
+            tc::commit(bar(sh->v_empty[n % kVSlots]));
           }
           __syncwarp();
           if (h + kBufs < g.steps) go = start_s(h + kBufs);
@@ -470,33 +465,21 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
       // ------------------------------------------------------------ widening
       const int w = warp - 12;
       int base = 0;
-      auto ready = [&] {
+      auto one = [&](uint64_t& land, uint64_t& full, uint8_t* tile, int n, int slots) {
+        if (!wait(land, n, slots)) return false;
+        widen16(tile, w, lane);
         fence_proxy_async();   // generic accesses, then the tensor core's reads and the next copy
         __syncwarp();
+        if (lane == 0) mbar_arrive(bar(full));
+        return true;
       };
       auto one_k = [&](int n) {
-        if (!wait(sh->kc_full[n % L::kKCodes], n, L::kKCodes) ||
-            (n >= L::kKSlots && !wait(sh->k_empty[n % L::kKSlots], n - L::kKSlots, L::kKSlots)))
-          return false;
-        widen16(sKc + n % L::kKCodes * kCodes, sK + n % L::kKSlots * kTile, w, lane);
-        ready();
-        if (lane == 0) {
-          mbar_arrive(bar(sh->k_full[n % L::kKSlots]));
-          mbar_arrive(bar(sh->kc_empty[n % L::kKCodes]));
-        }
-        return true;
+        const int i = n % kKSlots;
+        return one(sh->k_land[i], sh->k_full[i], sK + i * kTile, n, kKSlots);
       };
       auto one_v = [&](int n) {
-        if (!wait(sh->vc_full[n % L::kVCodes], n, L::kVCodes) ||
-            (n >= L::kVSlots && !wait(sh->v_empty[n % L::kVSlots], n - L::kVSlots, L::kVSlots)))
-          return false;
-        widen16(sVc + n % L::kVCodes * kCodes, sV + n % L::kVSlots * kTile, w, lane);
-        ready();
-        if (lane == 0) {
-          mbar_arrive(bar(sh->v_full[n % L::kVSlots]));
-          mbar_arrive(bar(sh->vc_empty[n % L::kVCodes]));
-        }
-        return true;
+        const int i = n % kVSlots;
+        return one(sh->v_land[i], sh->v_full[i], sV + i * kTile, n, kVSlots);
       };
       bool go = true;
       for (int si = 0; go && take(si, g); ++si) {
@@ -556,13 +539,11 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
         uint64_t seen = ~0ull;
         if (drafts) {
           // V's rows behind the last key become zero, and so do its drafted values that
-          // are not finite.  (P V of step n - 3 is done, since S of this step was issued after
-          // it; with two slots that of n - 2 is awaited too, else the wait for this V could take
-          // the one before it in the slot, whose phase has the same parity.)
-          if (L::kVSlots < kBufs && n >= L::kVSlots)
-            ok = ok && wait(sh->v_empty[n % L::kVSlots], n - L::kVSlots, L::kVSlots);
-          ok = ok && wait(sh->v_full[n % L::kVSlots], n, L::kVSlots);
-          uint8_t* const vrow = sV + n % L::kVSlots * kTile + key * 128;
+          // are not finite.  (The wait for V is for its slot's next phase: P V of step n - 3 is
+          // done, since S of this step was issued after it.)
+          static_assert(kVSlots >= kBufs, "phases of V's slots");
+          ok = ok && wait(sh->v_full[n % kVSlots], n, kVSlots);
+          uint8_t* const vrow = sV + n % kVSlots * kTile + key * 128;
           auto chunk = [&](int i) {   // (in turns, so that 8 lanes' chunks lie in different banks)
             return reinterpret_cast<uint4*>(vrow + (i >> 3) * kTHalf + (((i + key) & 7) << 4));
           };
@@ -689,7 +670,7 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
           }
           named_barrier(1, 128);
           if (h > 0) {   // the sums so far, and O^T (once P V of the last step is done)
-            ok = ok && wait(sh->v_empty[(n - 1) % L::kVSlots], n - 1, L::kVSlots);
+            ok = ok && wait(sh->v_empty[(n - 1) % kVSlots], n - 1, kVSlots);
             tc::fence_after_sync();
 #pragma unroll 1
             for (int c0 = 0; ok && c0 < N; c0 += 16) {

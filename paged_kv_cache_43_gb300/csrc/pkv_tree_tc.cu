@@ -22,7 +22,7 @@
 //   6    issues the products: S of the next 64 keys is formed while these are exponentiated
 //        (S has two buffers, P lies over S)
 //   7    finds the CTA's units and starts the copies of Q
-//   8-11 (e4m3) widen codes, K's and V's in turn, from a ring of codes to one of fp16
+//   8-11 (e4m3) widen codes, K's and V's in turn
 // The copies of a unit's keys begin while the one before it is computed.
 //
 // What a key that a row does not see holds must not reach the row, although P = 0 there
@@ -55,9 +55,14 @@ struct Lay {
   static constexpr int kTHalf = kKeys * 128;
   static constexpr int kTile = kHalves * kTHalf;
   static constexpr int kCodes = kKeys * D;
-  // slots of K and as many of V: of operand tiles, of codes (e4m3)
-  static constexpr int kSlots = (FP8 ? 1 : 2) * 128 / D;
-  static constexpr int kCodeSlots = FP8 ? 2 * 128 / D : 0;
+  // Slots of K and as many of V.  e4m3: head_size 128 widens codes in place, in the first half
+  // of the slot (its columns 0-63) where they landed; with 64, where a row's fp16 values lie over
+  // other rows' codes, codes have a ring of their own.  (Of their own with 128, too, they left
+  // room for one tile to be multiplied from: 128 sequences of 64 to 8192 keys 331 us.)
+  static constexpr bool kInPlace = FP8 && D == 128;
+  static constexpr int kSlots = FP8 && D == 64 ? 3 : 2 * 128 / D;
+  static constexpr int kCodeSlots = FP8 && D == 64 ? 4 : 0;
+  static constexpr int kLandSlots = kInPlace ? kSlots : kCodeSlots;
   static constexpr int kRing = 2 * kSlots * kTile, kCodeRing = 2 * kCodeSlots * kCodes;
   static constexpr int kStage = 4 * 32 * 128;   // rows on their way out: 32 x 32 fp32 a warp
 };
@@ -68,7 +73,7 @@ struct Shared {
   uint64_t q_full, q_empty, q_conv, pv_done, o_done, fixed, drain;
   uint64_t s_full[2], p_full[2];
   uint64_t full[2][L::kSlots], empty[2][L::kSlots];                    // of K, of V
-  uint64_t code_full[2][L::kCodeSlots + 1], code_empty[2][L::kCodeSlots + 1];
+  uint64_t code_full[2][L::kLandSlots + 1], code_empty[2][L::kLandSlots + 1];   // e4m3: codes there
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   Seg seg[kSegs];
   uint32_t tmem_base;
@@ -93,7 +98,7 @@ constexpr int kRegsSoftmax = 128, kRegsOther = 56;
 static_assert(128 * kRegsSoftmax + 256 * kRegsOther <= 384 * 80, "register split");
 
 // Widens a tile's e4m3 codes (rows of D bytes, swizzled as they landed) into the fp16 tile
-// layout; four warps, 16 rows each.  D = 128: 8 lanes, which a shared-memory access serves
+// layout; four warps, 16 rows each, read before they are written.  D = 128: 8 lanes, which a shared-memory access serves
 // together, take 4 chunks of one half in two rows whose numbers differ in bits 0 and 2, so
 // that reads and writes fall into different banks.
 template <int D>
@@ -110,6 +115,7 @@ __device__ __forceinline__ void widen(const uint8_t* codes, uint8_t* tile, int w
     const int r = row(i);
     v[i] = *reinterpret_cast<const uint4*>(codes + swz8<D>(r, c));
   }
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int r = row(i), j = 2 * (c & 3);
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(kThreads<FP8>, 2)
         mbar_init(bar(sh->full[i][j]), FP8 ? 4 : 1);
         mbar_init(bar(sh->empty[i][j]), 1);
       }
-      for (int j = 0; j < L::kCodeSlots; ++j) {
+      for (int j = 0; j < L::kLandSlots; ++j) {
         mbar_init(bar(sh->code_full[i][j]), 1);
         mbar_init(bar(sh->code_empty[i][j]), 4);
       }
@@ -197,11 +203,12 @@ __global__ void __launch_bounds__(kThreads<FP8>, 2)
     if (warp == 4 || warp == 5) {
       // ------------------------------------------------------------ copies of K, V
       const int is_v = warp - 4;
-      constexpr int kDepth = FP8 ? L::kCodeSlots : L::kSlots;
-      constexpr int kBytes = FP8 ? L::kCodes : L::kTile;
+      constexpr bool kApart = FP8 && !L::kInPlace;   // codes have their own ring
+      constexpr int kDepth = kApart ? L::kCodeSlots : L::kSlots;
+      constexpr int kBytes = kApart ? L::kCodes : L::kTile;
       uint64_t* land = FP8 ? sh->code_full[is_v] : sh->full[is_v];
-      uint64_t* empty = FP8 ? sh->code_empty[is_v] : sh->empty[is_v];
-      uint8_t* ring = (FP8 ? sCodes : sKV) + is_v * kDepth * kBytes;
+      uint64_t* empty = kApart ? sh->code_empty[is_v] : sh->empty[is_v];
+      uint8_t* ring = (kApart ? sCodes : sKV) + is_v * kDepth * kBytes;
       const CUtensorMap* map = is_v ? &vmap : &kmap;
       // several row tiles read the same keys: then they stay in L2
       const uint64_t policy = a.cta_tiles > 1 ? policy_evict_normal() : policy_evict_first();
@@ -362,15 +369,19 @@ __global__ void __launch_bounds__(kThreads<FP8>, 2)
       const int w = warp - 8;
       int base = 0;
       auto one = [&](int v, int n) {   // K's (0) or V's (1) tile of step n
-        if (!wait(sh->code_full[v][n % L::kCodeSlots], n, L::kCodeSlots)) return false;
-        if (n >= L::kSlots && !wait(sh->empty[v][n % L::kSlots], n - L::kSlots, L::kSlots)) return false;
-        widen<D>(sCodes + (v * L::kCodeSlots + n % L::kCodeSlots) * L::kCodes,
-                 sKV + (v * L::kSlots + n % L::kSlots) * L::kTile, w, lane);
+        if (!wait(sh->code_full[v][n % L::kLandSlots], n, L::kLandSlots)) return false;
+        uint8_t* tile = sKV + (v * L::kSlots + n % L::kSlots) * L::kTile;
+        const uint8_t* codes = tile;
+        if constexpr (!L::kInPlace) {
+          codes = sCodes + (v * L::kCodeSlots + n % L::kCodeSlots) * L::kCodes;
+          if (n >= L::kSlots && !wait(sh->empty[v][n % L::kSlots], n - L::kSlots, L::kSlots)) return false;
+        }
+        widen<D>(codes, tile, w, lane);
         fence_proxy_async();   // generic accesses, then the tensor core's reads and the next copy
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(sh->full[v][n % L::kSlots]));
-          mbar_arrive(bar(sh->code_empty[v][n % L::kCodeSlots]));
+          if (!L::kInPlace) mbar_arrive(bar(sh->code_empty[v][n % L::kLandSlots]));
         }
         return true;
       };
@@ -444,11 +455,10 @@ __global__ void __launch_bounds__(kThreads<FP8>, 2)
         const bool drafts = key0 + kKeys > q.first;   // keys that not every row sees, or none
         if (drafts) {
           // V's rows behind the last key become zero, and so do its drafted values that
-          // are not finite.  (With one slot, the last step's V may not be there yet: its
-          // product is awaited first, else the wait for this one's would take the one before
-          // it, whose phase has the same parity.)
-          if ((L::kSlots == 1 && h > 0 && !wait(sh->pv_done, pv + h - 1, 1)) ||
-              !wait(sh->full[1][n % L::kSlots], n, L::kSlots)) {
+          // are not finite.  (The wait for V is for its slot's next phase: P V of step n - 2 is
+          // done, since S of this step was issued after it.)
+          static_assert(L::kSlots >= 2, "phases of V's slots");
+          if (!wait(sh->full[1][n % L::kSlots], n, L::kSlots)) {
             done = false;
             break;
           }
