@@ -1671,7 +1671,7 @@ void make_tree_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms
   const int64_t most = std::max(num_sms * ctas_per_sm / p->cta_tiles, 1);
   const int64_t units = std::max<int64_t>(static_cast<int64_t>(m->num_seqs) * p->max_groups * c->num_kv_heads, 1);
   const int64_t steps = (static_cast<int64_t>(m->max_context_len) + step_keys - 1) / step_keys;
-  const int64_t kWholeSteps = p->keys_on_m ? 2 : 4, kMinRange = 4;
+  const int64_t kWholeSteps = p->keys_on_m ? 8 : 16, kMinRange = 4;
   if (m->kv_split_tokens > 0) {
     p->range = std::max(m->kv_split_tokens / step_keys, 1);
     p->workers = static_cast<int>(std::min<int64_t>((units * (steps + kTreeStart) + p->range - 1) / p->range, INT32_MAX / 16));

@@ -631,31 +631,37 @@ _I64 = torch.int64
 _FP8 = frozenset(FP8_DTYPES)
 
 
-def _rows_ok(t, dtype, heads, d, tokens, dev) -> bool:
+def _rows_ok(t, dtype, shape, dev) -> bool:
     """Rows [tokens, heads, d] whose heads lie densely; tokens any stride apart."""
-    return (t.dtype is dtype and t.get_device() == dev and t.shape == (tokens, heads, d)
-            and (t.is_contiguous() or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == d))))
+    return (t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and (t.is_contiguous() or (t.stride(2) == 1 and (shape[1] == 1
+                                                             or t.stride(1) == shape[2]))))
 
 
-def _rope_call(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, dev, **rows):
-    """Checks what the rope calls share; the descriptor.  `rows`: the further tensors of
-    rows by name, with their heads' number."""
+def _rope_desc(dev, q, k, v, q_out, k_out, positions, cos_sin, q_weight, k_weight, eps,
+               interleaved) -> RopeDesc:
+    """Checks the tensors of a rope call (v or k_out None) and describes them."""
     if q.dim() != 3 or k.dim() != 3:
         raise PkvError("q and k must be [num_tokens, heads, head_size]")
-    (tokens, hq, d), hkv, dt = q.shape, k.shape[1], q.dtype
+    dt, qs, ks = q.dtype, q.shape, k.shape
+    tokens, hq, d = qs
+    hkv = ks[1]
     if dt is not _BF16 and dt is not _F32:
         raise PkvError(f"unsupported dtype {dt}")
-    if not _rows_ok(q, dt, hq, d, tokens, dev) or not _rows_ok(k, dt, hkv, d, tokens, dev):
-        rows = dict(q=(q, hq), k=(k, hkv), **rows)
-    for n, (t, h) in rows.items():
-        if not _rows_ok(t, dt, h, d, tokens, dev):
+    other = k_out if v is None else v
+    if not (_rows_ok(q, dt, qs, dev) and _rows_ok(k, dt, (tokens, hkv, d), dev)
+            and _rows_ok(q_out, dt, qs, dev) and _rows_ok(other, dt, ks, dev)):
+        for n, t, h in (("q", q, hq), ("k", k, hkv), ("q_out", q_out, hq),
+                        ("v" if v is not None else "k_out", other, hkv)):
             if t.get_device() != dev:
                 raise PkvError(f"{n} must be on the current CUDA device ({dev})")
-            raise PkvError(f"{n} must be {dt} [{tokens}, {h}, {d}] with dense heads")
+            if not _rows_ok(t, dt, (tokens, h, d), dev):
+                raise PkvError(f"{n} must be {dt} [{tokens}, {h}, {d}] with dense heads")
+    cs = cos_sin.shape
     if not (positions.dtype is _I64 and cos_sin.dtype is _F32
             and positions.get_device() == dev == cos_sin.get_device()
             and positions.is_contiguous() and cos_sin.is_contiguous()
-            and positions.shape == (tokens,) and cos_sin.dim() == 2):
+            and positions.shape == (tokens,) and len(cs) == 2):
         _refuse(dev, positions=(positions, _I64), cos_sin=(cos_sin, _F32))
         raise PkvError("positions must be [num_tokens], cos_sin [max_position, rot_dim]")
     for n, w in (("q_weight", q_weight), ("k_weight", k_weight)):
@@ -663,27 +669,27 @@ def _rope_call(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, d
                                   and w.is_contiguous()):
             _refuse(dev, **{n: (w, dt)})
             raise PkvError(f"{n} must be [{d}]")
-    strides = [t.stride(0) if tokens > 1 else t.shape[1] * d
-               for t in (q, k, *(r[0] for n, r in rows.items() if n not in ("q", "k")))]
-    return strides, RopeDesc(tokens, hq, hkv, d, PKV_BF16 if dt is _BF16 else PKV_F32,
-                             cos_sin.shape[1], cos_sin.shape[0], bool(interleaved), 0, 0, 0, 0, 0,
-                             eps)
+    if tokens > 1:
+        sq, sk, so, s2 = q.stride(0), k.stride(0), q_out.stride(0), other.stride(0)
+    else:
+        sq = so = hq * d
+        sk = s2 = hkv * d
+    return RopeDesc(tokens, hq, hkv, d, PKV_BF16 if dt is _BF16 else PKV_F32, cs[1], cs[0],
+                    1 if interleaved else 0, sq, sk, s2, so, s2, eps)
 
 
 def _rope_write(call, q_out, q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, scales,
                 fp8, q_weight, k_weight, eps, interleaved, stream) -> None:
     dev = _current_device()
-    hq, hkv = q.shape[1] if q.dim() == 3 else 0, k.shape[1] if k.dim() == 3 else 0
-    strides, desc = _rope_call(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved,
-                               dev, v=(v, hkv), q_out=(q_out, hq))
-    desc.q_stride, desc.k_stride, desc.v_stride, desc.q_out_stride = strides
-    kd = k_cache.dtype
+    desc = _rope_desc(dev, q, k, v, q_out, None, positions, cos_sin, q_weight, k_weight, eps,
+                      interleaved)
+    kd, c = k_cache.dtype, k_cache.shape
     if not ((kd in _FP8 if fp8 else kd is q.dtype) and v_cache.dtype is kd
             and slot_mapping.dtype is _I64
             and k_cache.get_device() == dev == v_cache.get_device() == slot_mapping.get_device()
             and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and slot_mapping.is_contiguous() and k_cache.dim() == 4
-            and v_cache.shape == k_cache.shape and k_cache.shape[2:] == k.shape[1:]
+            and slot_mapping.is_contiguous() and len(c) == 4 and v_cache.shape == c
+            and c[2] == desc.num_kv_heads and c[3] == desc.head_size
             and slot_mapping.shape == positions.shape):
         if fp8 and (kd not in _FP8 or v_cache.dtype not in _FP8):
             raise PkvError("the caches must hold e4m3 codes (uint8 or float8_e4m3fn)")
@@ -693,12 +699,11 @@ def _rope_write(call, q_out, q, k, v, positions, cos_sin, slot_mapping, k_cache,
         raise PkvError("k_cache and v_cache must both be [num_blocks, 16, num_kv_heads, "
                        "head_size], slot_mapping [num_tokens]")
     for n, t in zip(("k_scale", "v_scale"), scales):
-        if not (t.dtype is _F32 and t.shape == (hkv,) and t.get_device() == dev
+        if not (t.dtype is _F32 and t.shape == (c[2],) and t.get_device() == dev
                 and t.is_contiguous()):
             _refuse(dev, **{n: (t, _F32)})
             raise PkvError(f"{n} must have num_kv_heads entries")
-    nb, bs, _, d = k_cache.shape
-    cache = CacheDesc(nb, bs, hkv, d, PKV_FP8_E4M3 if fp8 else desc.dtype)
+    cache = CacheDesc(c[0], c[1], c[2], c[3], PKV_FP8_E4M3 if fp8 else desc.dtype)
     st = call(q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(),
               cos_sin.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(),
               0 if k_weight is None else k_weight.data_ptr(), slot_mapping.data_ptr(),
@@ -734,10 +739,8 @@ def rope(q_out, k_out, q, k, positions, cos_sin, *, q_weight=None, k_weight=None
     write_int8 wants them."""
     lib = _lib or load()
     dev = _current_device()
-    hq, hkv = q.shape[1] if q.dim() == 3 else 0, k.shape[1] if k.dim() == 3 else 0
-    strides, desc = _rope_call(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved,
-                               dev, q_out=(q_out, hq), k_out=(k_out, hkv))
-    desc.q_stride, desc.k_stride, desc.q_out_stride, desc.k_out_stride = strides
+    desc = _rope_desc(dev, q, k, None, q_out, k_out, positions, cos_sin, q_weight, k_weight, eps,
+                      interleaved)
     st = lib.pkv_rope(q_out.data_ptr(), k_out.data_ptr(), q.data_ptr(), k.data_ptr(),
                       positions.data_ptr(), cos_sin.data_ptr(),
                       0 if q_weight is None else q_weight.data_ptr(),
@@ -879,17 +882,30 @@ def accept_drafts(buffers, block_tables, context_lens, query_start_loc, accepted
         raise PkvError("block_tables [num_seqs, stride], context_lens, num_accepted and "
                        "new_context_lens [num_seqs], accepted [num_seqs, most] and "
                        "query_start_loc [num_seqs + 1] must fit together")
-    head = buffers[0].shape[:2] if len(buffers) else (0, 16)
-    nb = head[0]
-    for t in buffers:
-        if (t.get_device() != dev or not t.is_contiguous() or t.dtype is _I8 or t.dim() < 3
-                or t.shape[:2] != head or head[1] != 16):
-            _refuse(dev, buffers=(t, None))
-            raise PkvError("buffers must all be [num_blocks, 16, ...] of the same number of "
-                           "blocks, and not of an int8 cache")
-    ptrs = array.array("Q", [t.data_ptr() for t in buffers])
-    rows = array.array("q", [t.nbytes // (16 * nb) for t in buffers] if nb else
-                       [4] * len(buffers))
+    if len(buffers):
+        # (mostly all alike: then one row's bytes are all rows')
+        t0 = buffers[0]
+        shape, dtype = t0.shape, t0.dtype
+        alike = (len(shape) >= 3 and shape[1] == 16 and dtype is not _I8
+                 and all([t.shape == shape and t.dtype is dtype and t.is_contiguous()
+                          and t.get_device() == dev for t in buffers]))
+        nb = shape[0] if len(shape) else 0
+        if not alike:
+            for t in buffers:
+                if (t.get_device() != dev or not t.is_contiguous() or t.dtype is _I8
+                        or t.dim() < 3 or t.shape[0] != nb or t.shape[1] != 16):
+                    _refuse(dev, buffers=(t, None))
+                    raise PkvError("buffers must all be [num_blocks, 16, ...] of the same number "
+                                   "of blocks, and not of an int8 cache")
+        ptrs = array.array("Q", [t.data_ptr() for t in buffers])
+        if nb == 0:
+            rows = array.array("q", [4]) * len(buffers)
+        elif alike:
+            rows = array.array("q", [t0.nbytes // (16 * nb)]) * len(buffers)
+        else:
+            rows = array.array("q", [t.nbytes // (16 * nb) for t in buffers])
+    else:
+        nb, ptrs, rows = 0, array.array("Q"), array.array("q")
     st = lib.pkv_accept_drafts(ptrs.buffer_info()[0], rows.buffer_info()[0], len(buffers), nb,
                                block_tables.data_ptr(), block_tables.shape[1],
                                context_lens.data_ptr(), query_start_loc.data_ptr(), n[0],
