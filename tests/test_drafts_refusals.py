@@ -188,3 +188,25 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
         tree(cache, pkv.attention_tree_fp8, torch.ones(1, hkv), torch.ones(1, hkv))
     with pytest.raises(pkv.PkvError):
         pkv.accept_drafts([cache], i32(1, 2), i32(1), i32(2), i32(1, 4), i32(1))
+
+
+def test_groups_past_a_tile(lib):
+    """More q heads on a kv head than a tile has rows (fp32 takes them)."""
+    assert tree(lib, m=meta(num_q_heads=2 * 129)) == E_SHAPE
+    assert tree_fp8(lib, m=meta(num_q_heads=2 * 129)) == E_SHAPE
+
+
+def test_rope_struct_layout_matches_header(tmp_path):
+    import os
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "sizes.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "pkv.h"\n'
+                   'int main(void){printf("%zu %zu %zu\\n", sizeof(pkv_rope_desc), '
+                   'offsetof(pkv_rope_desc, q_stride), offsetof(pkv_rope_desc, eps));return 0;}\n')
+    exe = tmp_path / "sizes"
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(root, "include"), str(src), "-o",
+                    str(exe)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(x) for x in got] == [ctypes.sizeof(pkv.RopeDesc), pkv.RopeDesc.q_stride.offset,
+                                     pkv.RopeDesc.eps.offset]

@@ -288,3 +288,103 @@ def test_bounded_waits_run_out_and_the_device_recovers(dtype):
     finally:
         pkv.debug_wait_test(False)
     b.check(b.call())
+
+
+# ---- few query rows a kv head (at most 32, head_size 128: keys on the products' M dimension)
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n,g", [(1, 1), (3, 5), (16, 1), (17, 1), (8, 4), (2, 16), (4, 7), (1, 32)])
+@pytest.mark.parametrize("split", [0, 64])
+def test_few_rows(dtype, n, g, split):
+    L = [n, n + 1, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300, 700, 1025]
+    L = [x for x in L if x >= n]
+    b = Batch([n] * len(L), [x - n for x in L], hq=2 * g, hkv=2, d=128, dtype=dtype, seed=n + g).cuda()
+    b.check(b.call(kv_split_tokens=split))
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("split", [0, 64])
+def test_few_rows_any_mask(dtype, split):
+    """Rows that see no draft, every draft, later ones; steps of drafts alone, in which some rows
+    see their first key and others none."""
+    rng = np.random.default_rng(3)
+    n, before = [32, 32, 32, 9, 1, 31], [128, 0, 256, 0, 0, 97]
+    masks = []
+    for k in n:
+        rows = [int(rng.integers(0, 1 << k)) for _ in range(k)]
+        rows[0] = 0
+        masks += [r | int(rng.integers(0, 1 << 40)) << k & (1 << 64) - 1 for r in rows]
+    b = Batch(n, before, hq=2, hkv=2, d=128, dtype=dtype, masks=masks, seed=4).cuda()
+    b.check(b.call(kv_split_tokens=split))
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("hq", [2, 8])
+@pytest.mark.parametrize("split", [0, 64, 128])
+def test_not_finite_drafts_with_heads_of_128(dtype, hq, split):
+    n, before = [14, 16], [50, 330]
+    b = Batch(n, before, hq=hq, hkv=2, d=128, dtype=dtype, seed=6)
+    seen = torch.zeros(30, dtype=torch.bool)
+    for s, draft in ((0, 3), (1, 7), (1, 15)):
+        p = before[s] + draft
+        row = b.v.view(torch.uint8) if b.fp8 else b.v
+        row[b.table[s, p // 16], p % 16, 1, 77] = 0x7F if b.fp8 else float("nan")
+        if not b.fp8:
+            row[b.table[s, p // 16], p % 16, 1, 9] = float("-inf")
+        t0 = int(b.starts[s])
+        for i in range(n[s]):
+            seen[t0 + i] |= bool(b.bits[t0 + i] >> draft & 1)
+    b.cuda()
+    out = b.call(kv_split_tokens=split)
+    want = b.want()
+    # (e4m3: a few of the random K and V are past 448 and NaN, too; the reference has them)
+    bad = ~torch.isfinite(out.cpu())
+    assert torch.equal(bad, ~torch.isfinite(want[0]))
+    assert bool(bad[seen][:, hq // 2:].any(2).all())
+    b.check(out, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("hq", [1, 4])
+def test_scores_of_any_size_with_few_rows(dtype, hq):
+    """References far above or below what comes later, and the other sign of the scale."""
+    b = Batch([8, 5], [1500, 90], hq=hq, hkv=1, d=128, dtype=dtype, seed=9)
+    b.q *= 30
+    if not b.fp8:
+        b.k[b.table[0, 25]] *= 40
+        b.k[b.table[0, 0], 0] *= 100
+    b.cuda()
+    for kw in ({}, dict(kv_split_tokens=128)):
+        b.check(b.call(**kw))
+    b.scale = -b.scale
+    b.check(b.call())
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("d,hq", [(128, 2), (128, 16), (64, 6)])
+def test_many_sequences(dtype, d, hq):
+    """More sequences than a warp's lanes hold at a time, short, long, empty and bad ones."""
+    rng = np.random.default_rng(7)
+    n = [int(x) for x in rng.integers(0, 9, 83)]
+    before = [int(x) for x in rng.integers(0, 200, 83)]
+    before[17], before[60] = 3000, 1500
+    n[17], n[60], n[40], n[82] = 5, 8, 3, 4
+    b = Batch(n, before, hq=hq, hkv=2, d=d, dtype=dtype, seed=8).cuda()
+    want, tol = b.want()
+    b.g["cl"][40] = 2                      # fewer keys than drafts
+    for kw in ({}, dict(kv_split_tokens=64), dict(kv_split_tokens=448)):
+        out = b.call(**kw)
+        assert pkv.get_error() == pkv.ERR_QUERY_LEN
+        rows = slice(int(b.starts[40]), int(b.starts[41]))
+        assert bool((out[rows] == 0).all())
+        w = want.clone()
+        w[rows] = 0
+        b.check(out, (w, tol))
+
+
+def test_no_key_at_all():
+    """Sequences of drafts alone whose rows see nothing: zeros, whatever the caches hold."""
+    for d, n in ((128, 4), (128, 40), (64, 9)):
+        b = Batch([n], [0], hq=2, hkv=1, d=d, masks=[0] * n).cuda()
+        for kw in ({}, dict(kv_split_tokens=64)):
+            assert bool((b.call(**kw) == 0).all())
