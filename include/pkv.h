@@ -443,12 +443,14 @@ int pkv_rope(void *q_out, void *k_out, const void *q, const void *k, const int64
  * Every sequence is taken alike (num_decode_seqs is ignored); sliding_window
  * must be 0 (PKV_E_META).  A sequence longer than max_query_len or
  * max_context_len: its bit of pkv_attention, its first max_query_len rows zero.
- * num_seqs is 65535 at most, and so are num_kv_heads x the tiles of 32
- * (row, head) pairs that max_query_len rows make (PKV_E_SHAPE).  Int8 caches are
- * not taken: keeping some of a block's drafted rows would leave it with a scale
- * that its dropped rows made.  Workspace: scratch of one call, size from the
- * function below; calls that may overlap, captured graphs included, need one
- * each. */
+ * num_seqs is 65535 at most, so are num_kv_heads x the tiles of 32 (row, head)
+ * pairs that max_query_len rows make, and over bf16 and e4m3 caches a kv head has
+ * 128 q heads at most (PKV_E_SHAPE).  Int8 caches are not taken: keeping some of a
+ * block's drafted rows would leave it with a scale that its dropped rows made.
+ * kv_split_tokens: keys of each of the equal parts that the batch's work is cut
+ * into (fp32: of each sequence's splits); 0 = as many parts as the GPU holds.
+ * Workspace: scratch of one call, size from the function below; calls that may
+ * overlap, captured graphs included, need one each. */
 size_t pkv_attention_tree_workspace_size(const pkv_cache_desc *cache, const pkv_attn_meta *meta);
 int pkv_attention_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
                        const int32_t *block_tables, const int32_t *context_lens,
@@ -499,8 +501,8 @@ int pkv_get_error(int32_t *error_bits, int clear);
 /* TEST HOOK for the timeout path; no counterpart in the pages.  Every on-chip
  * wait of the kernels gives up after a bounded time (1 s), sets
  * PKV_ERR_TIMEOUT, lets the CTA's own copies in flight land, frees its tensor
- * memory and returns.  With enable != 0, the decode and tcgen05 prefill
- * launches this process makes afterwards (on any device, from any thread)
+ * memory and returns.  With enable != 0, the decode, tcgen05 prefill and
+ * tcgen05 tree launches this process makes afterwards (on any device, from any thread)
  * wait at most 20 us and withhold their first key block or tile, so that
  * those waits run out and the attention calls return with PKV_ERR_TIMEOUT
  * set and meaningless output; enable = 0 restores normal launches.  Host

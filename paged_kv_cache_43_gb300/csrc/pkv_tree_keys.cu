@@ -1,5 +1,5 @@
 // pkv_tree_keys.cu -- attention of a tree of drafted tokens on tcgen05 where a kv head has
-// few query rows (a tile of at most 64), head_size 128.
+// few query rows (at most 32), head_size 128.
 //
 // Mathematics as in pkv_tree_tc.cu, with keys instead of query rows on the products' M
 // dimension: S^T = K Q^T (128 keys x N rows), O^T += V^T P^T (128 elements of the head x N).
@@ -56,20 +56,21 @@ struct Shared {
   uint32_t tmem_base;
   int32_t abort;
   int32_t v_odd[2];              // a drafted V value of segment i is not finite: [i % 2]
-  uint32_t bits[4][N];           // of a step's keys 32 w + ..: which of them row c sees
-  alignas(16) float scale[2][N];   // of segment i's rows: what scores are multiplied with (e4m3:
-  alignas(16) float negm[2][N];    // Q's exponent is in it), and -m
-  float alpha[N];                // what a step's new m makes of the sums so far
-  float wide[2][4][N];           // a row's sum (of segment i), or maximum, over a warp's keys
-  float inv[N];                  // what a row's O^T is multiplied with
-  int64_t at[N];                 // where it goes: elements of out, or of the partials
+  // (read and written 16 bytes at a time)
+  alignas(16) uint32_t bits[4][N];   // of a step's keys 32 w + ..: which of them row c sees
+  alignas(16) float scale[2][N];     // of segment i's rows: what scores are multiplied with (e4m3:
+  alignas(16) float negm[2][N];      // Q's exponent is in it), and -m
+  alignas(16) float alpha[N];        // what a step's new m makes of the sums so far, -1: no m yet
+  float wide[2][4][N];               // a row's sum (of segment i), or maximum, over a warp's keys
+  float inv[N];                      // what a row's O^T is multiplied with
+  int64_t at[N];                     // where it goes: elements of out, or of the partials
 };
 
 template <bool FP8, int N>
 constexpr int smem_bytes() {
   constexpr int need = 2 * N * 128 + kBufs * kKeys * 128 + (kKSlots + kVSlots) * kTile +
                        static_cast<int>(sizeof(Shared<FP8, N>)) + 1024;
-  static_assert(need <= 227 * 1024, "shared memory");
+  static_assert(need <= 227 * 1024 && N <= 32, "shared memory; a row's bit of 32");
   return need > 120 * 1024 ? need : 120 * 1024;   // (one CTA per SM)
 }
 
@@ -103,9 +104,9 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// Reduces N values a lane over the warp's lanes; lane's results, N / 32 of them (one, the same in
-// two lanes, for N = 16), stay in v[0], v[1] and are those of the values first, first + 1.  Each
-// step halves what a lane holds: N - N / 32 shuffles instead of 5 N.
+// Reduces M values a lane over the warp's lanes; a lane's result, that of the value whose number is
+// returned, stays in v[0] (M = 16: two lanes have each).  A step halves what a lane holds: M - 1
+// shuffles (and one) instead of 5 M.
 template <int OFF, int N, int M, typename Op>
 __device__ __forceinline__ int across(float (&v)[N], int lane, Op op) {   // (of the first M)
   if constexpr (OFF == 0) {
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sK = smem;                                   // [slot][half][128 keys x 128 B]
   uint8_t* sV = sK + kKSlots * kTile;
-  uint8_t* sP = sV + kVSlots * kTile;                   // [3][128 keys x 64 rows]
+  uint8_t* sP = sV + kVSlots * kTile;                   // [3][128 keys x 128 B]
   uint8_t* sQ = sP + kBufs * kKeys * 128;                   // [half][N rows x 128 B]
   Sh* sh = reinterpret_cast<Sh*>(sQ + 2 * N * 128);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
         ok = ok && wait(sh->s_full[n % kBufs], n, kBufs);
         tc::fence_after_sync();
         // bit c: row c sees this thread's key
-        uint64_t seen = ~0ull;
+        uint32_t seen = ~0u;
         if (drafts) {
           // V's rows behind the last key become zero, and so do its drafted values that
           // are not finite.  (The wait for V is for its slot's next phase: P V of step n - 3 is
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
             const uint4 w = *reinterpret_cast<const uint4*>(&sh->bits[warp][c]);
             const uint32_t four = (w.x >> lane & 1) | (w.y >> lane & 1) << 1 | (w.z >> lane & 1) << 2 |
                                   (w.w >> lane & 1) << 3;
-            seen |= static_cast<uint64_t>(four) << c;
+            seen |= four << c;
           }
         }
         // ---- weights against the references that there are, N of this key, and the largest.  No
@@ -651,7 +652,6 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
           for (int c = 0; c < N; ++c) x[c] = (seen >> c & 1) ? x[c] * scale[c] : -INFINITY;
           const int at = across<16, N, N>(x, lane, [](float u, float v) { return fmaxf(u, v); });
           sh->wide[i2][warp][at] = x[0];
-          if constexpr (N == 64) sh->wide[i2][warp][at + 1] = x[1];
           named_barrier(1, 128);
           if (threadIdx.x < N) {
             const int c = threadIdx.x;
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
           if (ok) (void)weigh();
         }
         // ---- to the sums (rounded, as they meet V: the output is a convex combination), and to
-        // shared memory: a row of 64 for each key
+        // shared memory: 128 bytes for each key, N weights in them
         if (ok) {   // (else the next barrier ends it)
           uint8_t* prow = sP + n % kBufs * kKeys * 128 + key * 128;
 #pragma unroll
@@ -720,7 +720,6 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
       }
       const int at = across<16, N, N>(sum, lane, [](float u, float v) { return u + v; });
       sh->wide[i2][warp][at] = sum[0];
-      if constexpr (N == 64) sh->wide[i2][warp][at + 1] = sum[1];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(sh->sum_full[i2]));
       base += g.steps;

@@ -668,7 +668,9 @@ __global__ void __launch_bounds__(128) pkv_tree_tc_merge_kernel(const TreeArgs a
   const int r = (static_cast<int>(t) - q.q0) * a.group + hq - kvh * a.group;
   const int tile = r / tile_rows, tg = tile / a.cta_tiles;
   const int2 span = a.span[(static_cast<int64_t>(s) * a.max_groups + tg) * a.num_kv_heads + kvh];
-  if (span.y <= 1) return;
+  // (one worker wrote the row itself; a span that there cannot be was not written, because a
+  // wait gave up)
+  if (span.y <= 1 || span.x < 0 || span.x >= a.workers || span.y > a.workers - span.x) return;
   auto place = [&](int i) {   // row of partial i
     return ((static_cast<int64_t>(span.x + i) * 2 + (i == 0 ? 1 : 0)) * a.cta_tiles +
             tile - tg * a.cta_tiles) * a.part_rows + r - tile * tile_rows;

@@ -37,11 +37,10 @@ __device__ __forceinline__ void tree_walk(const TreeArgs& a, int step_keys, Emit
   const int ct = a.cta_tiles, W = gridDim.x / ct;
   const int worker = blockIdx.x / ct, tile_c = blockIdx.x - worker * ct;
   const int tile_rows = a.tile_toks * a.group;
-  int s0 = 0;            // the 32 sequences that the lanes hold, one each:
+  // the 32 sequences that the lanes hold, one each:
   int q0, n, len, steps, groups;
   int64_t unit_cost, cost;
   auto hold = [&](int at) {
-    s0 = at;
     q0 = n = len = steps = groups = 0;
     unit_cost = cost = 0;
     if (at + lane >= a.num_seqs) return;
@@ -55,14 +54,23 @@ __device__ __forceinline__ void tree_walk(const TreeArgs& a, int step_keys, Emit
     unit_cost = a.whole ? 1 : steps + kStart;
     cost = unit_cost * groups * a.num_kv_heads;
   };
-  int64_t total = 0;
-  for (int at = 0; at < a.num_seqs; at += 32) {
-    hold(at);
-    int64_t c = cost;
+  // the cost of the 128 sequences from `at` on, four a lane at a time
+  auto cost_of = [&](int at) {
+    int64_t c = 0;
+#pragma unroll
+    for (int i = 0; i < 128; i += 32) {
+      const int s = at + i + lane;
+      TreeSeq q = tree_seq(a, min(s, a.num_seqs - 1));
+      if (s >= a.num_seqs || q.skip || q.err != 0) q.n = 0;
+      const int64_t uc = a.whole ? 1 : (q.L + step_keys - 1) / step_keys + kStart;
+      c += uc * (((q.n + a.tile_toks - 1) / a.tile_toks + ct - 1) / ct) * a.num_kv_heads;
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
-    total += c;
-  }
+    return c;
+  };
+  int64_t total = 0;
+  for (int at = 0; at < a.num_seqs; at += 128) total += cost_of(at);
   // this worker's part of the line
   const int64_t begin = a.range > 0 ? a.range * worker : total * worker / W;
   const int64_t end = a.range > 0 ? min(total, begin + a.range) : total * (worker + 1) / W;
@@ -70,8 +78,15 @@ __device__ __forceinline__ void tree_walk(const TreeArgs& a, int step_keys, Emit
     return static_cast<int>(a.range > 0 ? p / a.range : ((p + 1) * W - 1) / total);
   };
   int64_t before = 0;    // the line up to the sequences that the lanes hold
-  for (int at = 0; at < a.num_seqs && before < end; at += 32) {
-    if (at != s0 || a.num_seqs > 32) hold(at);
+  int from = 0;          // (128 at a time past those that lie before this part)
+  while (from + 128 < a.num_seqs) {
+    const int64_t c = cost_of(from);
+    if (before + c > begin) break;
+    before += c;
+    from += 128;
+  }
+  for (int at = from; at < a.num_seqs && before < end; at += 32) {
+    hold(at);
     int64_t upto = cost;   // inclusive sums over the lanes
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
