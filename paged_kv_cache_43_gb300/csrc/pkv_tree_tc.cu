@@ -646,77 +646,98 @@ __global__ void __launch_bounds__(kThreads<FP8>, 2)
   }
 }
 
-// Merges the partials of the units that several workers computed: one warp per (query row,
-// q head), out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).  The first worker of a unit
-// holds its partial in the second of its two places, the others in their first.
+// Merges the partials of the units that several workers computed: out = sum_i 2^(lse_i - M) O_i /
+// sum_i 2^(lse_i - M).  The first worker of a unit holds its partial in the second of its
+// two places, the others in their first.  A warp takes kMergeRows q heads of a query row, so that
+// its way to the span (row, sequence, lengths: loads one after the other) is gone once for
+// them, and their partials' loads overlap (8 sequences of 64 drafts, 32 q heads: 17 us with a
+// warp a head).
+constexpr int kMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(128) pkv_tree_tc_merge_kernel(const TreeArgs a) {
   constexpr int PER = D / 32;
-  constexpr int kUnroll = 8;   // partials in flight
+  constexpr int kEach = 32 / kMergeRows;   // partials looked up at a time
   // (a programmatic dependent launch: the partials are visible once this returns)
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int chunks = (a.group + kMergeRows - 1) / kMergeRows;   // warps of a query row and kv head
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int64_t t = w / a.num_q_heads;
+  const int64_t t = w / (static_cast<int64_t>(a.num_kv_heads) * chunks);
   if (t >= a.num_tokens) return;
+  const int in_row = static_cast<int>(w - t * a.num_kv_heads * chunks);
+  const int kvh = in_row / chunks, g0 = (in_row - kvh * chunks) * kMergeRows;
+  const int rows = min(a.group - g0, kMergeRows);
   const int s = seq_of_row(a.query_start_loc, a.num_seqs, static_cast<int>(t));
   if (s < 0) return;   // a row of no sequence
   const TreeSeq q = tree_seq(a, s);
   if (q.skip || q.err != 0 || t < q.q0 || t >= q.q0 + q.n) return;
-  const int hq = static_cast<int>(w - t * a.num_q_heads), kvh = hq / a.group;
   const int tile_rows = a.tile_toks * a.group;
-  const int r = (static_cast<int>(t) - q.q0) * a.group + hq - kvh * a.group;
+  const int r = (static_cast<int>(t) - q.q0) * a.group + g0;   // (a token's rows are in one tile)
   const int tile = r / tile_rows, tg = tile / a.cta_tiles;
   const int2 span = a.span[(static_cast<int64_t>(s) * a.max_groups + tg) * a.num_kv_heads + kvh];
   // (one worker wrote the row itself; a span that there cannot be was not written, because a
   // wait gave up)
   if (span.y <= 1 || span.x < 0 || span.x >= a.workers || span.y > a.workers - span.x) return;
-  auto place = [&](int i) {   // row of partial i
+  auto place = [&](int i) {   // the first of the rows, in partial i
     return ((static_cast<int64_t>(span.x + i) * 2 + (i == 0 ? 1 : 0)) * a.cta_tiles +
             tile - tg * a.cta_tiles) * a.part_rows + r - tile * tile_rows;
   };
-  float M = -INFINITY;
-  bool nan = false;
-  for (int i = lane; i < span.y; i += 32) {
-    const float e = a.ws_lse[place(i)];
+  // lane: row lane / kEach, partial lane % kEach of those looked up
+  const int my_row = lane / kEach, my_part = lane % kEach;
+  auto lse = [&](int i0) {
+    return my_row < rows && i0 + my_part < span.y ? a.ws_lse[place(i0 + my_part) + my_row] : -INFINITY;
+  };
+  const float e0 = lse(0);
+  float M = e0;
+  bool nan = e0 != e0;
+  for (int i0 = kEach; i0 < span.y; i0 += kEach) {
+    const float e = lse(i0);
     M = fmaxf(M, e);
     nan = nan || e != e;
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  if (__any_sync(0xffffffffu, nan)) M = NAN;
-  float acc[PER] = {}, den = 0.f;
-  if (M != -INFINITY) {
-    for (int i0 = 0; i0 < span.y; i0 += kUnroll) {
-      float v[kUnroll][PER], e[kUnroll];
+  for (int off = kEach / 2; off > 0; off >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    nan = __shfl_xor_sync(0xffffffffu, nan ? 1 : 0, off) != 0 || nan;
+  }
+  if (nan) M = NAN;
+  float acc[kMergeRows][PER] = {}, den = 0.f;
+  for (int i0 = 0; i0 < span.y; i0 += kEach) {
+    const float e = i0 == 0 ? e0 : lse(i0);
+    // (a part that the row sees nothing of; a NaN stays)
+    const float f = e == -INFINITY ? 0.f : exp2f(e - M);
+    den += f;
+#pragma unroll 2
+    for (int p = 0; p < kEach; ++p) {
+      if (i0 + p >= span.y) break;
+      const float* o = a.ws_o + place(i0 + p) * D + lane * PER;
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        e[u] = -INFINITY;
+      for (int k = 0; k < kMergeRows; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, f, k * kEach + p);
+        if (k < rows && wk != 0.f) {
+          float v[PER];
+          if constexpr (PER == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o + k * D);
+          else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o + k * D);
 #pragma unroll
-        for (int k = 0; k < PER; ++k) v[u][k] = 0.f;
-        if (i0 + u < span.y) {
-          const int64_t at = place(i0 + u);
-          e[u] = a.ws_lse[at];
-          const float* src = a.ws_o + at * D + lane * PER;
-          if constexpr (PER == 4) *reinterpret_cast<float4*>(v[u]) = *reinterpret_cast<const float4*>(src);
-          else *reinterpret_cast<float2*>(v[u]) = *reinterpret_cast<const float2*>(src);
+          for (int x = 0; x < PER; ++x) acc[k][x] = fmaf(wk, v[x], acc[k][x]);
         }
-      }
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        if (e[u] == -INFINITY) continue;   // a part that the row sees nothing of
-        const float f = exp2f(e[u] - M);
-        den += f;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) acc[k] = fmaf(f, v[u][k], acc[k]);
       }
     }
   }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + w * D + lane * PER;
 #pragma unroll
-  for (int k = 0; k < PER; k += 2)
-    *reinterpret_cast<__nv_bfloat162*>(out + k) = __floats2bfloat162_rn(acc[k] * inv, acc[k + 1] * inv);
+  for (int off = kEach / 2; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) +
+                       (t * a.num_q_heads + kvh * a.group + g0) * D + lane * PER;
+#pragma unroll
+  for (int k = 0; k < kMergeRows; ++k) {
+    const float ik = __shfl_sync(0xffffffffu, inv, k * kEach);
+    if (k >= rows) break;
+#pragma unroll
+    for (int x = 0; x < PER; x += 2)
+      *reinterpret_cast<__nv_bfloat162*>(out + k * D + x) =
+          __floats2bfloat162_rn(acc[k][x] * ik, acc[k][x + 1] * ik);
+  }
 }
 
 template <int D, bool FP8>
@@ -747,7 +768,8 @@ cudaError_t launch_tree_tc(const CUtensorMap& qmap, const CUtensorMap& kmap,
     e = head_size == 128 ? launch_t<128, false>(qmap, kmap, vmap, b, stream)
                          : launch_t<64, false>(qmap, kmap, vmap, b, stream);
   if (e != cudaSuccess || a.whole) return e;
-  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.num_q_heads;
+  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.num_kv_heads *
+                        ((a.group + kMergeRows - 1) / kMergeRows);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
   cfg.blockDim = dim3(128);
