@@ -1654,9 +1654,9 @@ void make_tree_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms
     }
     return;
   }
-  // A worker is as many CTAs as the longest sequence has row tiles, 8 at most: they share
-  // the keys' way through L2.
-  constexpr int kMaxTiles = 8;
+  // Keys on M: at most 32 rows a kv head and head_size 128 (64 sequences of 500 to 4000 keys, 8 kv
+  // heads, us, rows on M / keys on M: bf16 4 rows 98 / 97, 32 rows 108 / 100, 64 rows 107 / 167;
+  // e4m3 159 / 106, 167 / 137, 160 / 234).
   const int group = m->num_q_heads / c->num_kv_heads;
   const int64_t most_rows = static_cast<int64_t>(m->max_query_len) * group;
   p->keys_on_m = c->head_size == 128 && most_rows <= kTreeKeysRows;
@@ -1665,12 +1665,26 @@ void make_tree_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms
   p->tile_toks = std::max(std::min(m->max_query_len, tile_rows / group), 1);
   p->part_rows = p->keys_on_m ? p->tile_toks * group : kTreeRows;
   const int tiles = std::max((m->max_query_len + p->tile_toks - 1) / p->tile_toks, 1);
+  // A worker is as many CTAs as there are row tiles: they share the keys' way through L2 (16
+  // sequences of 16K to 32K keys with 2 tiles: 356 us, with a CTA a worker 456).  Of more than
+  // 8 tiles it takes 2 to 8 at a time, so that the last group is as full as can be (one
+  // sequence of 16000 keys, 19 tiles, us: 2 or 4 at a time, 20 in all, 155; 3 at a time, 21,
+  // 163; 8 at a time, 24, 179).
+  constexpr int kMaxTiles = 8;
   p->cta_tiles = std::min(tiles, kMaxTiles);
+  auto padded = [&](int c) { return (tiles + c - 1) / c * c; };
+  if (tiles > kMaxTiles)
+    for (int c = kMaxTiles - 1; c >= 2; --c)
+      if (padded(c) < padded(p->cta_tiles)) p->cta_tiles = c;
   p->max_groups = (tiles + p->cta_tiles - 1) / p->cta_tiles;
   const int ctas_per_sm = p->keys_on_m ? 1 : 2;
   const int64_t most = std::max(num_sms * ctas_per_sm / p->cta_tiles, 1);
   const int64_t units = std::max<int64_t>(static_cast<int64_t>(m->num_seqs) * p->max_groups * c->num_kv_heads, 1);
   const int64_t steps = (static_cast<int64_t>(m->max_context_len) + step_keys - 1) / step_keys;
+  // Contexts of up to 1024 keys are not cut: no partials, no second kernel (200 sequences of 100
+  // to 600 keys with 64 rows a kv head 124 us, cut 177; 16 drafts over 1000 keys 22.5, cut
+  // 25.8).  A range has 4 steps at least (one sequence of 1500 keys, 8 kv heads, 64 rows, us: with 1
+  // 32.6, 2 23.4, 4 21.1, 6 22.9, 16 29.2).
   const int64_t kWholeSteps = p->keys_on_m ? 8 : 16, kMinRange = 4;
   if (m->kv_split_tokens > 0) {
     p->range = std::max(m->kv_split_tokens / step_keys, 1);

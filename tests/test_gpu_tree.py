@@ -39,6 +39,15 @@ def test_tree_sizes(dtype, n):
     b.check(b.call())
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("n", [140, 176, 300])
+@pytest.mark.parametrize("before", [100, 1500])
+def test_more_than_eight_row_tiles(dtype, n, before):
+    """9, 11 and 19 row tiles, some at a time, beside sequences of one tile; keys cut and whole."""
+    b = Batch([n, 3, n - 17], [before, 200, 0], hq=8, hkv=1, d=128, dtype=dtype, seed=n).cuda()
+    b.check(b.call())
+
+
 @pytest.mark.parametrize("dtype", [BF16, E4M3, F32])
 @pytest.mark.parametrize("split", [64, 128, 320, 1024, 2048])
 def test_splits(dtype, split):
