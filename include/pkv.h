@@ -409,7 +409,8 @@ typedef struct {
  *   cos_sin        fp32 [max_position, rot_dim]: rot_dim / 2 cosines, then as many
  *                  sines (may be NULL when rot_dim is 0)
  *   q_weight, k_weight  [head_size], rope->dtype, or NULL: no norm
- *   slot_mapping   int64 [num_tokens]; two tokens with the same slot: either row
+ *   slot_mapping   int64 [num_tokens]; two tokens with the same slot: each value
+ *                  is of one of the two (unspecified which)
  * Skipped whole, their rows of q_out left as they are: tokens with a slot < 0,
  * with a slot past the cache (PKV_ERR_SLOT) or with a position outside
  * [0, max_position) (PKV_ERR_POSITION).  cache->dtype must be rope->dtype. */
@@ -481,7 +482,7 @@ int pkv_attention_tree_fp8(void *out, const void *q, const void *k_cache, const 
  *                       are not read
  *   num_accepted        int32 [num_seqs], 0 .. min(n, max_accepted)
  *   new_context_lens    int32 [num_seqs] or NULL: becomes L - n + num_accepted[s]; it
- *                       must not overlap context_lens (PKV_E_META)
+ *                       overlaps none of the other arrays (PKV_E_META)
  * Sequences with bad lengths (PKV_ERR_QUERY_LEN, PKV_ERR_CONTEXT_LEN) or a bad path
  * (PKV_ERR_ACCEPTED) are left alone, their new length is L; a row whose block id is
  * bad is not moved (PKV_ERR_BLOCK_ID).  Drafted rows of two sequences in the same

@@ -1850,9 +1850,16 @@ extern "C" int pkv_accept_drafts(void* const* buffers, const int64_t* row_bytes,
   if (!aligned4(block_tables) || !aligned4(context_lens) || !aligned4(query_start_loc) ||
       !aligned4(accepted) || !aligned4(num_accepted) || !aligned4(new_context_lens))
     return PKV_E_ALIGN;
-  // (every CTA of a sequence reads its length, so its new one goes elsewhere)
-  if (new_context_lens != nullptr && new_context_lens < context_lens + num_seqs &&
-      context_lens < new_context_lens + num_seqs)
+  // (every CTA of a sequence reads all of these, so its new length goes elsewhere)
+  auto over_new = [&](const int32_t* p, int64_t n) {
+    const uintptr_t in = reinterpret_cast<uintptr_t>(p), to = reinterpret_cast<uintptr_t>(new_context_lens);
+    return to < in + n * sizeof(int32_t) && in < to + num_seqs * sizeof(int32_t);
+  };
+  if (new_context_lens != nullptr &&
+      (over_new(context_lens, num_seqs) || over_new(num_accepted, num_seqs) ||
+       over_new(query_start_loc, static_cast<int64_t>(num_seqs) + 1) ||
+       over_new(accepted, static_cast<int64_t>(num_seqs) * max_accepted) ||
+       over_new(block_tables, static_cast<int64_t>(num_seqs) * block_table_stride)))
     return PKV_E_META;
   AcceptArgs a{};
   int sms;

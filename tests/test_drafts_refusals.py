@@ -159,6 +159,14 @@ def test_accept_descriptions(lib):
     assert accept(lib, seqs=4, new=P - 12) == E_META
 
 
+def test_new_lengths_over_other_arrays(lib):
+    """Every CTA of a sequence reads these while the first writes the new length."""
+    new = P + (1 << 16)
+    for name, size in (("num", 16), ("qsl", 20), ("acc", 64), ("bt", 32)):
+        for at in (new, new + 12, new - size + 4):
+            assert accept(lib, seqs=4, new=new, **{name: at}) == E_META, (name, at)
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
     T, hq, hkv, d = 3, 4, 2, 64
     b = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
