@@ -1684,10 +1684,8 @@ void make_tree_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms
   // Contexts of up to 1024 keys are not cut: no partials, no second kernel (200 sequences of 100
   // to 600 keys with 64 rows a kv head 124 us, cut 177; 16 of 1000 keys 24.8, cut 30.8).  One
   // sequence of 1000 keys is faster cut on the device (22.4, cut 19.9), but not as a plain
-  // call, which then has a workspace to get and a second launch (22.6, cut 27.3).  A range has
-  // 4 steps at least (one sequence of 1500 keys, 8 kv heads, 64 rows, us: with 1 32.6, 2 23.4,
-  // 4 21.1, 6 22.9, 16 29.2).
-  const int64_t kWholeSteps = p->keys_on_m ? 8 : 16, kMinRange = 4;
+  // call, which then has a workspace to get and a second launch (22.6, cut 27.3).
+  const int64_t kWholeSteps = p->keys_on_m ? 8 : 16;
   if (m->kv_split_tokens > 0) {
     p->range = std::max(m->kv_split_tokens / step_keys, 1);
     p->workers = static_cast<int>(std::min<int64_t>((units * (steps + kTreeStart) + p->range - 1) / p->range, INT32_MAX / 16));
@@ -1697,7 +1695,7 @@ void make_tree_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms
     p->workers = static_cast<int>(std::min(units, most));
     return;
   } else {
-    p->workers = static_cast<int>(std::max<int64_t>(std::min(most, units * (steps + kTreeStart) / kMinRange), 1));
+    p->workers = static_cast<int>(std::max<int64_t>(std::min(most, units * (steps + kTreeStart) / kTreeMinRange), 1));
   }
   const size_t rows = static_cast<size_t>(p->workers) * 2 * p->cta_tiles * p->part_rows;
   p->ws_o_bytes = round_up(rows * c->head_size * sizeof(float), 256);

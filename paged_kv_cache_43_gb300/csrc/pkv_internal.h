@@ -341,7 +341,7 @@ struct TreeArgs {
   int32_t max_groups;            // groups of that many tiles, for the longest sequence
   int32_t workers;
   int32_t whole;                 // units are not cut: no workspace, no merge
-  int64_t range;                 // steps of a worker, 0: equal shares
+  int64_t range;                 // steps of a worker, 0: equal shares (of kTreeMinRange or more)
   int2* span;                    // [num_seqs, max_groups, Hkv]: a unit's first worker, workers
   uint64_t wait_limit_ns;        // test hook, as DecodeArgs
   int32_t debug_stall;
@@ -350,6 +350,9 @@ constexpr int kTreeRows = 128, kTreeStepKeys = 64;         // pkv_tree_tc.cu
 // Steps that a unit counts on the line of work for its start and end (64 sequences of 128 to 4096
 // keys, 32 kv heads: 369 us with 1, 365 with 2, 347 with 4).
 constexpr int kTreeStart = 4;
+// Steps that a worker has at least where the work is cut into equal parts (one sequence of 1500
+// keys, 8 kv heads, 64 rows, us: with 1 32.6, 2 23.4, 4 21.1, 6 22.9, 16 29.2).
+constexpr int kTreeMinRange = 4;
 constexpr int kTreeKeysRows = 32, kTreeKeysStep = 128;     // pkv_tree_keys.cu
 // Tiles of at most kTreeKeysRows rows, head_size 128 (called by launch_tree_tc).
 cudaError_t launch_tree_keys(const CUtensorMap& qmap, const CUtensorMap& kmap,

@@ -34,7 +34,7 @@ constexpr int kStart = kTreeStart;
 template <typename Emit>
 __device__ __forceinline__ void tree_walk(const TreeArgs& a, int step_keys, Emit emit) {
   const int lane = threadIdx.x & 31;
-  const int ct = a.cta_tiles, W = gridDim.x / ct;
+  const int ct = a.cta_tiles;
   const int worker = blockIdx.x / ct, tile_c = blockIdx.x - worker * ct;
   const int tile_rows = a.tile_toks * a.group;
   // the 32 sequences that the lanes hold, one each:
@@ -71,12 +71,20 @@ __device__ __forceinline__ void tree_walk(const TreeArgs& a, int step_keys, Emit
   };
   int64_t total = 0;
   for (int at = 0; at < a.num_seqs; at += 128) total += cost_of(at);
-  // this worker's part of the line
-  const int64_t begin = a.range > 0 ? a.range * worker : total * worker / W;
-  const int64_t end = a.range > 0 ? min(total, begin + a.range) : total * (worker + 1) / W;
-  auto worker_of = [&](int64_t p) {
-    return static_cast<int>(a.range > 0 ? p / a.range : ((p + 1) * W - 1) / total);
-  };
+  // This worker's part of the line.  The contexts may be far shorter than max_context_len, which
+  // made the number of workers: the first of them share the line then, so that none between
+  // a unit's first and last is without a step (the merge reads a partial of each).
+  const int W = gridDim.x / ct;
+  int64_t range = a.range, begin, end;
+  if (a.whole) {
+    begin = total * worker / W;
+    end = total * (worker + 1) / W;
+  } else {
+    if (range == 0) range = max((total + W - 1) / W, static_cast<int64_t>(kTreeMinRange));
+    begin = range * worker;
+    end = min(total, begin + range);
+  }
+  auto worker_of = [&](int64_t p) { return static_cast<int>(p / range); };
   int64_t before = 0;    // the line up to the sequences that the lanes hold
   int from = 0;          // (128 at a time past those that lie before this part)
   while (from + 128 < a.num_seqs) {
