@@ -711,9 +711,10 @@ __global__ void __launch_bounds__(128) pkv_tree_tc_merge_kernel(const TreeArgs a
   float acc[kMergeRows][PER] = {}, den = 0.f;
   for (int i0 = 0; i0 < span.y; i0 += kEach) {
     const float e = i0 == 0 ? e0 : lse(i0);
-    // (a part that the row sees nothing of; a NaN stays)
-    const float f = e == -INFINITY ? 0.f : exp2f(e - M);
-    den += f;
+    // (below zero: a part that the row sees nothing of; one whose share is too small for fp32 still
+    // counts, as what it holds may be infinite or NaN)
+    const float f = e == -INFINITY ? -1.f : exp2f(e - M);
+    den += e == -INFINITY ? 0.f : f;
 #pragma unroll 2
     for (int p = 0; p < kEach; ++p) {
       if (i0 + p >= span.y) break;
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(128) pkv_tree_tc_merge_kernel(const TreeArgs a
 #pragma unroll
       for (int k = 0; k < kMergeRows; ++k) {
         const float wk = __shfl_sync(0xffffffffu, f, k * kEach + p);
-        if (k < rows && wk != 0.f) {
+        if (k < rows && !(wk < 0.f)) {   // (a NaN is a share)
           float v[PER];
           if constexpr (PER == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o + k * D);
           else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o + k * D);
