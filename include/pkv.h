@@ -438,7 +438,9 @@ int pkv_rope(void *q_out, void *k_out, const void *q, const void *k, const int64
  * from row i, the keys 0 .. L - n - 1 and those keys L - n + j, j < n, whose bit
  * j of row i's mask is set (its ancestors and itself; any set of bits is
  * allowed).  A row that sees no key is zero.  What a key's K and V hold reaches
- * only the rows that see it, NaN and infinities too.
+ * only the rows that see it, NaN and infinities too.  bf16: a row's sums before they
+ * are divided reach 2^15 |V| for each of its keys, and are finite while |V| x keys is
+ * below 2^113.
  *   tree_mask  int64 [num_tokens, ceil(max_query_len / 64)]: bit j % 64 of word
  *              j / 64; bits from n on are ignored
  * Every sequence is taken alike (num_decode_seqs is ignored); sliding_window

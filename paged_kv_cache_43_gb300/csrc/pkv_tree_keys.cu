@@ -7,7 +7,7 @@
 // cost is that of K's and V's way out of shared memory.
 //
 // A thread has a key: N scores in its TMEM lane.  The rows' references m lie in shared memory:
-// the score of a unit's first key, and a row's maximum once a weight has passed kMost
+// the score of a unit's first key, and a row's maximum once a weight has passed kTreeMost
 // (or if the first key is a draft, which not every row sees), which the four softmax warps
 // agree on at a barrier every step; so most steps need no maximum over keys, which would go
 // across lanes.  Denominators are sums a thread keeps for every row, added up at the end.  P^T
@@ -39,8 +39,6 @@ constexpr int kBufs = 3;
 constexpr uint32_t kCols = 256;
 __device__ __forceinline__ uint32_t col_s(int h) { return 32u * (h % kBufs); }
 __device__ __forceinline__ uint32_t col_o(int i) { return 128u + 32u * (i & 1); }
-template <bool FP8>
-constexpr float kMost = FP8 ? 32768.f : 0x1p60f;   // (fp16 weights reach 65504)
 
 // Slots of K and V tiles.  e4m3 codes land in the first half of a slot (its columns 0-63) and are
 // widened in place: with rings of their own for the codes there was room for one tile of K to
@@ -646,7 +644,7 @@ __global__ void __launch_bounds__(kThreads<FP8>, 1)
           over = true;
           break;
         }
-        if (!all((h > 0 || given) && top <= kMost<FP8> && !lacking)) {
+        if (!all((h > 0 || given) && top <= kTreeMost && !lacking)) {
           // new references: each row's maximum over the step's keys
           float x[N];
 #pragma unroll

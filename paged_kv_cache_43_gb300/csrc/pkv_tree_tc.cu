@@ -5,7 +5,7 @@
 // S = Q K^T and O += P V run on 128 rows x 64 keys, P = 2^(scale log2(e) s - m) rounded to
 // bf16, as both operands of a product have one type (e4m3 caches: everything on fp16, to which
 // codes widen exactly; K's descale joins the score scale, V's the output).  m is a reference, not the running maximum: it moves only
-// when a step's weights sum to more than kMost, so most steps need no pass for the maximum
+// when a step's weights sum to more than kTreeMost, so most steps need no pass for the maximum
 // and no rescaling of O.  The denominator of bf16 sums the rounded weights, so the output
 // is a convex combination of V rows.
 //
@@ -49,10 +49,6 @@ constexpr uint32_t kCols = 256;                 // TMEM columns of a CTA
 // S of step h at 64 (h % 2), P over its first 32 columns; O at 128.
 __device__ __forceinline__ uint32_t col_s(int h) { return 64u * (h & 1); }
 constexpr uint32_t kColO = 128;
-// A step's weights may sum to this before the reference moves: bf16 weights and fp32 sums
-// hold it easily; fp16 weights reach 65504.
-template <bool FP8>
-constexpr float kMost = FP8 ? 32768.f : 0x1p60f;
 
 template <int D, bool FP8>
 struct Lay {
@@ -550,7 +546,7 @@ __global__ void __launch_bounds__(kThreads<FP8>, 2)
               }
             }
             ls = tc::sum_f32x2(acc);
-            if (find || !__any_sync(0xffffffffu, valid && !(ls <= kMost<FP8>))) break;
+            if (find || !__any_sync(0xffffffffu, valid && !(ls <= kTreeMost))) break;
             find = true;
           }
           if (h > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {   // rescale O

@@ -27,6 +27,11 @@ struct alignas(16) Seg {
   int32_t part;                                 // where its partial goes, -1: the whole unit
 };
 constexpr int kSegs = 4;
+// What weights (of 64 keys together, or one) may come to before a row's reference moves.  fp16 weights
+// reach 65504; of bf16 ones O holds up to this times a V value for each key in fp32, so |V| x keys
+// stays right below 2^113.  (One sequence of 4000 keys, 8 drafts x 4 heads: with 2^60 29.9 us,
+// 2^15 29.9, 2^8 33.9; larger batches 0 to 2 % apart.)
+constexpr float kTreeMost = 32768.f;
 constexpr int kStart = kTreeStart;
 
 // Calls emit(seg) for each segment of this CTA, one warp's lanes together, until it returns

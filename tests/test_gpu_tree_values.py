@@ -47,3 +47,22 @@ def test_not_finite_v_of_a_far_key_is_not_lost(dtype, n, d, split):
     out = b.call(kv_split_tokens=split).float()
     assert not bool(torch.isfinite(out[:, :, 7]).any())
     assert bool(torch.isfinite(out[:, :, :7]).all()) and bool(torch.isfinite(out[:, :, 8:]).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,d", [(6, 128), (40, 128), (20, 64)])
+@pytest.mark.parametrize("split", [0, 64, 2048])
+@pytest.mark.parametrize("rise", [3.0, 12.0, 35.0])
+def test_rising_scores_over_large_v(dtype, n, d, split, rise):
+    """V of about 1e25; the last keys' scores lie `rise` nats above the first's, in one step or many."""
+    b = Batch([n, n], [1200, 100], hq=2, hkv=1, d=d, dtype=dtype, seed=n)
+    b.v = (b.v.float() * 1e25).to(dtype)
+    b.q[..., 0] = 8
+    for s, L in enumerate(b.L):
+        for p in range(L):
+            up = rise * (p / L if s == 0 else p >= 70)
+            row(b, b.k, s, p)[0, 0] = up / (8 * b.scale)
+    b.cuda()
+    out = b.call(kv_split_tokens=split)
+    assert bool(torch.isfinite(out).all())
+    b.check(out)
