@@ -45,7 +45,8 @@ __global__ void __launch_bounds__(kThreads) pkv_tree_kernel(const TreeArgs a) {
   const TreeSeq q = tree_seq(a, s);
   const bool reporter = split == 0 && blockIdx.y == 0 && threadIdx.x == 0;
   if (q.err != 0 && reporter) raise_error(a.err, q.err);
-  const int row0 = tile * kRows, rows = min(q.n * G - row0, kRows);
+  const int row0 = tile * kRows;   // (more drafts than the stated most: the first are zeroed)
+  const int rows = min(min(q.n, a.max_query_len) * G - row0, kRows);
   if (q.skip || rows <= 0) return;
   float* out = static_cast<float*>(a.out);
   auto at = [&](int r) {   // row r of the tile in q and out
