@@ -1,4 +1,5 @@
-"""Tree attention over values at the ends of their range."""
+"""Tree attention over values at the ends of their range: V that is not finite far below the rest, large V with
+scores that rise, drafts of K and V that are not finite in every kernel."""
 import pytest
 import torch
 
@@ -66,3 +67,65 @@ def test_rising_scores_over_large_v(dtype, n, d, split, rise):
     out = b.call(kv_split_tokens=split)
     assert bool(torch.isfinite(out).all())
     b.check(out)
+
+
+def odd(b, what, s, p, h, e, value):
+    c = row(b, b.k if what == "k" else b.v, s, p)
+    c[h, e] = 0x7F if b.fp8 else value
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3, F32])
+@pytest.mark.parametrize("hq,d", [(2, 128), (4, 128), (24, 128), (4, 64)])
+@pytest.mark.parametrize("split", [0, 64, 128])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("before", [[50, 330], [0, 1100]])
+def test_not_finite_k_of_drafts_reaches_only_rows_that_see_it(dtype, hq, d, split, value, before):
+    """Rows that see such a K have scores that are not finite; all others are as without it."""
+    if dtype == E4M3 and value == value:
+        pytest.skip("e4m3 has no infinity")
+    n = [14, 16]
+    b = Batch(n, before, hq=hq, hkv=2, d=d, dtype=dtype, seed=6)
+    if b.fp8:
+        b.k, b.v = (torch.where(torch.isnan(c.float()), 1.0, c.float()).to(dtype) for c in (b.k, b.v))
+    clean = b.want()
+    seen = torch.zeros(30, dtype=torch.bool)
+    for s, draft in ((0, 3), (1, 7), (1, 15)):
+        odd(b, "k", s, before[s] + draft, 1, 77 % d, value)
+        for i in range(n[s]):
+            seen[int(b.starts[s]) + i] |= bool(b.bits[int(b.starts[s]) + i] >> draft & 1)
+    b.cuda()
+    out = b.call(kv_split_tokens=split).double().cpu()
+    ok = (out - clean[0]).abs() <= clean[1]
+    half = hq // 2
+    assert bool(ok[:, :half].all()) and bool(ok[~seen].all())
+    if value != value:   # (an infinite score of either sign: +inf gives NaN, -inf a weight of 0)
+        assert bool(torch.isnan(out[seen][:, half:]).all())
+
+
+@pytest.mark.parametrize("split", [0, 64, 128])
+@pytest.mark.parametrize("hq,d", [(2, 128), (8, 64)])
+def test_not_finite_v_of_drafts_in_fp32(split, hq, d):
+    n, before = [14, 90], [50, 330]
+    b = Batch(n, before, hq=hq, hkv=2, d=d, dtype=F32, seed=6)
+    seen = torch.zeros(104, dtype=torch.bool)
+    for s, draft in ((0, 3), (1, 37), (1, 88)):
+        odd(b, "v", s, before[s] + draft, 1, 9, float("nan"))
+        odd(b, "v", s, before[s] + draft, 1, 33, float("-inf"))
+        for i in range(n[s]):
+            seen[int(b.starts[s]) + i] |= bool(b.bits[int(b.starts[s]) + i] >> draft & 1)
+    b.cuda()
+    out, want = b.call(kv_split_tokens=split), b.want()
+    bad = ~torch.isfinite(out.cpu())
+    assert torch.equal(bad, ~torch.isfinite(want[0]))
+    assert bool(bad[seen][:, hq // 2:].any(2).all())
+    b.check(out, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("g", [17, 33, 65, 100, 128])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("split", [0, 64])
+def test_many_q_heads_a_kv_head(dtype, g, d, split):
+    """Row tiles of a few tokens, or one."""
+    b = Batch([3, 1, 5, 9], [60, 700, 1, 1400], hq=2 * g, hkv=2, d=d, dtype=dtype, seed=g).cuda()
+    b.check(b.call(kv_split_tokens=split))
