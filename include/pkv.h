@@ -376,7 +376,8 @@ int pkv_copy_blocks(void *const *buffers, const int64_t *page_bytes, int32_t num
  * (pkv_rope_write: their positions come from their depth in the tree, their
  * slots from the pool), attends from all of them at once (pkv_attention_tree)
  * and, once the model's outputs say which path is right, keeps that path's rows
- * (pkv_accept_drafts).
+ * (pkv_accept_drafts).  The pool gets the other drafts' positions back before it
+ * gives the next step its slots (pkv_pool.h: pkv_pool_take_back).
  *
  * The pass between the QKV projection and attention, for any step. */
 typedef struct {

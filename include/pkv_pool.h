@@ -92,6 +92,17 @@ int pkv_pool_allocate_slots_batch(pkv_pool *pool, const int64_t *req_ids,
                                   const int32_t *num_new_tokens, int32_t num_reqs,
                                   int32_t sliding_window, int64_t *slot_mapping,
                                   int32_t *num_done);
+/* Takes back the last positions that pkv_pool_allocate_slots gave each of num_reqs requests:
+ * the drafted tokens of a step that were not accepted (pkv_accept_drafts moves the
+ * accepted ones' rows to the front).  req_ids[i] keeps its first num_computed[i] positions; blocks
+ * that hold none of them are released, last to first, and the next call gives slots from there
+ * on.  PKV_E_SHAPE: num_computed[i] lies before the request's last allocation or behind its
+ * computed count; PKV_E_REQUEST: an unknown request, or a block past num_computed[i] is in
+ * the prefix cache (tokens are appended once they are accepted, so that drafts are not filed).
+ * Stops at the first request that it cannot serve.  A released block may be handed out at
+ * once: what still reads it (pkv_accept_drafts) is enqueued before what then writes it. */
+int pkv_pool_take_back(pkv_pool *pool, const int64_t *req_ids, const int32_t *num_computed,
+                       int32_t num_reqs);
 /* Forks request parent_id into the new request child_id: the same token ids,
  * the same computed count and the same blocks, shared (counted).  Afterwards
  * the two go on apart.  Full blocks stay shared; when pkv_pool_allocate_slots

@@ -222,6 +222,14 @@ class Pool:
                     self._cache_block(r.blocks[i], h)
         return slots
 
+    def take_back(self, req_id, num_computed):
+        """the positions from num_computed on lose their slots again."""
+        r = self.reqs[req_id]
+        keep = -(-num_computed // self.bs)
+        gone, r.blocks = r.blocks[keep:], r.blocks[:keep]
+        self._free_blocks(list(reversed(gone)))
+        r.num_computed = num_computed
+
     def fork_request(self, parent_id, child_id):
         """the child shares everything the parent has; counts go up."""
         p = self.reqs[parent_id]

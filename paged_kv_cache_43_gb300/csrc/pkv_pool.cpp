@@ -49,6 +49,7 @@ struct Request {
   std::vector<uint64_t> hashes;   // chained hashes of the leading full blocks
   int32_t num_computed = 0;
   int32_t num_filed = 0;          // leading full blocks already offered to the cache
+  int32_t last_first = 0;         // the first position that the last allocation gave a slot
 };
 
 }  // namespace
@@ -325,6 +326,7 @@ int pkv_pool_admit(pkv_pool* pool, int64_t req_id, int32_t* num_cached_tokens) {
   for (int32_t b : r.blocks) pool->touch(b);
   r.num_computed = static_cast<int32_t>(r.blocks.size()) * pool->bs;
   r.num_filed = static_cast<int32_t>(r.blocks.size());
+  r.last_first = r.num_computed;
   *num_cached_tokens = r.num_computed;
   return PKV_OK;
 }
@@ -379,6 +381,7 @@ int pkv_pool_allocate_slots(pkv_pool* pool, int64_t req_id, int32_t num_new_toke
     for (int64_t p = first; p < end; ++p)
       slot_mapping[p - first] = static_cast<int64_t>(r.blocks[p / bs]) * bs + p % bs;
   r.num_computed = static_cast<int32_t>(end);
+  r.last_first = static_cast<int32_t>(first);
   // newly full blocks whose tokens are known go into the prefix cache
   if (pool->caching) {
     const int64_t known = end < static_cast<int64_t>(r.tokens.size())
@@ -408,6 +411,26 @@ int pkv_pool_allocate_slots_batch(pkv_pool* pool, const int64_t* req_ids,
     if (st != PKV_OK) return st;
     off += num_new_tokens[i];
     *num_done = i + 1;
+  }
+  return PKV_OK;
+}
+
+int pkv_pool_take_back(pkv_pool* pool, const int64_t* req_ids, const int32_t* num_computed,
+                       int32_t num_reqs) {
+  if (!pool || (num_reqs > 0 && (!req_ids || !num_computed))) return PKV_E_NULL;
+  if (num_reqs < 0) return PKV_E_SHAPE;
+  const int32_t bs = pool->bs;
+  for (int32_t i = 0; i < num_reqs; ++i) {
+    auto it = pool->reqs.find(req_ids[i]);
+    if (it == pool->reqs.end()) return PKV_E_REQUEST;
+    Request& r = it->second;
+    const int32_t n = num_computed[i];
+    if (n < r.last_first || n > r.num_computed) return PKV_E_SHAPE;
+    if (n < static_cast<int64_t>(r.num_filed) * bs) return PKV_E_REQUEST;
+    const size_t keep = (static_cast<size_t>(n) + bs - 1) / bs;
+    for (size_t k = r.blocks.size(); k-- > keep;) pool->release(r.blocks[k]);
+    r.blocks.resize(keep);
+    r.num_computed = n;
   }
   return PKV_OK;
 }

@@ -16,7 +16,7 @@ EXPORTED = ("pkv_pool_create", "pkv_pool_destroy", "pkv_pool_num_free", "pkv_poo
             "pkv_pool_append_token_batch",
             "pkv_pool_admit", "pkv_pool_allocate_slots", "pkv_pool_allocate_slots_batch",
             "pkv_pool_free_request", "pkv_pool_fork_request", "pkv_pool_resize",
-            "pkv_pool_take_copies",
+            "pkv_pool_take_copies", "pkv_pool_take_back",
             "pkv_pool_block_table", "pkv_pool_build_block_tables", "pkv_pool_num_computed",
             "pkv_pool_block_state", "pkv_pool_free_queue")
 
@@ -45,6 +45,7 @@ def _lib():
             "pkv_pool_fork_request": (ctypes.c_int, [vp, i64, i64]),
             "pkv_pool_resize": (ctypes.c_int, [vp, i32]),
             "pkv_pool_take_copies": (ctypes.c_int, [vp, P32, i32, P32]),
+            "pkv_pool_take_back": (ctypes.c_int, [vp, P64, P32, i32]),
             "pkv_pool_block_table": (ctypes.c_int, [vp, i64, P32, i32, P32]),
             "pkv_pool_build_block_tables": (ctypes.c_int, [vp, P64, i32, P32, i32]),
             "pkv_pool_num_computed": (ctypes.c_int, [vp, i64, P32]),
@@ -138,6 +139,16 @@ class BlockPool:
             nn.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)), ids.size, int(window),
             out.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)), ctypes.byref(done)))
         return out[:int(nn[:done.value].sum())], int(done.value)
+
+    def take_back(self, req_ids, num_computed):
+        """Of each request's last allocation only the positions below num_computed
+        are kept (drafted tokens that were not accepted); blocks behind are released."""
+        ids = np.ascontiguousarray(req_ids, dtype=np.int64)
+        n, np_ = _i32(num_computed)
+        if ids.ndim != 1 or ids.shape != n.shape:
+            raise pkv.PkvError("req_ids and num_computed must be lists of the same length")
+        self._check(self._lib.pkv_pool_take_back(
+            self._p, ids.ctypes.data_as(ctypes.POINTER(ctypes.c_int64)), np_, ids.size))
 
     def free_request(self, req_id: int):
         self._check(self._lib.pkv_pool_free_request(self._p, int(req_id)))
