@@ -171,10 +171,9 @@ __global__ void __launch_bounds__(128) pkv_tree_merge_kernel(const TreeArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t t = w / a.num_q_heads;
   if (t >= a.num_tokens) return;
-  const int s = seq_of_row(a.query_start_loc, a.num_seqs, static_cast<int>(t));
-  if (s < 0) return;   // a row of no sequence
-  const TreeSeq q = tree_seq(a, s);
-  if (q.skip || q.err != 0 || t < q.q0 || t >= q.q0 + q.n) return;
+  TreeSeq q;
+  const int s = tree_seq_of_row(a, static_cast<int>(t), q);
+  if (s < 0) return;   // a row of no sequence, or of a bad one
   const int nsplit = tree_splits(a, q.L);
   if (nsplit <= 1) return;
   const int64_t row = w * a.max_splits;

@@ -34,6 +34,27 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeArgs& a, int s) {
   return q;
 }
 
+// The sequence that computes query row t, -1: none; a whole warp together.  query_start_loc ascends
+// unless some sequence's entry is bad, and the search for t may end at such a one: then all
+// sequences are looked at, as those that are right are not to suffer.
+__device__ __forceinline__ int tree_seq_of_row(const TreeArgs& a, int t, TreeSeq& q) {
+  const int lane = threadIdx.x & 31;
+  int s = seq_of_row(a.query_start_loc, a.num_seqs, t);
+  if (s >= 0) {
+    q = tree_seq(a, s);
+    if (!q.skip && q.err == 0) return s;
+  }
+  for (int at = 0; at < a.num_seqs; at += 32) {
+    q = tree_seq(a, min(at + lane, a.num_seqs - 1));
+    const uint32_t has = __ballot_sync(0xffffffffu, !q.skip && q.err == 0 && t >= q.q0 && t < q.q0 + q.n);
+    if (has == 0) continue;
+    s = min(at + __ffs(has) - 1, a.num_seqs - 1);
+    q = tree_seq(a, s);
+    return s;
+  }
+  return -1;
+}
+
 // Bits of the keys [key0, key0 + 64) that the row whose mask words are `mask` sees: every
 // key before the sequence's first draft, and the drafts whose bits are set.
 __device__ __forceinline__ uint64_t tree_bits(const uint64_t* mask, const TreeSeq& q, int key0) {

@@ -670,10 +670,9 @@ __global__ void __launch_bounds__(128) pkv_tree_tc_merge_kernel(const TreeArgs a
   const int in_row = static_cast<int>(w - t * a.num_kv_heads * chunks);
   const int kvh = in_row / chunks, g0 = (in_row - kvh * chunks) * kMergeRows;
   const int rows = min(a.group - g0, kMergeRows);
-  const int s = seq_of_row(a.query_start_loc, a.num_seqs, static_cast<int>(t));
-  if (s < 0) return;   // a row of no sequence
-  const TreeSeq q = tree_seq(a, s);
-  if (q.skip || q.err != 0 || t < q.q0 || t >= q.q0 + q.n) return;
+  TreeSeq q;
+  const int s = tree_seq_of_row(a, static_cast<int>(t), q);
+  if (s < 0) return;   // a row of no sequence, or of a bad one
   const int tile_rows = a.tile_toks * a.group;
   const int r = (static_cast<int>(t) - q.q0) * a.group + g0;   // (a token's rows are in one tile)
   const int tile = r / tile_rows, tg = tile / a.cta_tiles;
