@@ -3,7 +3,7 @@ the rows behind those stay as they were."""
 import pytest
 import torch
 
-from drafts import Batch
+from drafts import Batch, mask_words
 from paged_kv_cache_43_gb300 import build, pkv
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +35,16 @@ def test_rows_behind_the_stated_most_stay(dtype, hq, d):
         # (e4m3: a few of the random K and V are past 448 and NaN; the reference has them)
         same = torch.isnan(got[rows]) & torch.isnan(want[rows])
         assert bool((same | ((got[rows] - want[rows]).abs() <= tol[rows])).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3, F32])
+@pytest.mark.parametrize("hq,d", [(2, 128), (8, 64), (24, 128)])
+@pytest.mark.parametrize("most", [33, 200, 5000])
+@pytest.mark.parametrize("split", [0, 64])
+def test_far_fewer_drafts_than_the_stated_most(dtype, hq, d, most, split):
+    """Masks, tiles and workers are made for `most` rows; the sequences have 1 to 17."""
+    if split and most == 5000:
+        pytest.skip("that many parts of 64 keys for that many rows: a workspace of many GB")
+    b = Batch([1, 17, 0, 4, 2], [1200, 333, 9, 0, 2500], hq=hq, hkv=2, d=d, dtype=dtype, seed=most).cuda()
+    b.g["mask"] = mask_words(b.bits, -(-most // 64)).cuda()
+    b.check(b.call(max_query_len=most, kv_split_tokens=split))
