@@ -8,10 +8,11 @@
 // row in the order of j; a batch of kRowsInFlight rows is loaded before the first of them is
 // stored (a later batch's rows lie behind every place that an earlier one wrote).
 //
-// Bound by latency for few rows (ids, then tables, then rows: 1 sequence in 32 buffers 3.6 us),
-// by HBM for many: 256 sequences of up to 8 accepted drafts in 32 buffers 16.7 us, 5.0 TB/s
-// read and written, 0.73 of the copy rate.  A CTA has 4 buffers, so that the path's lookups are
-// gone once for them.
+// Bound by loads that wait for one another: lengths and path, then the tables' ids, then the rows, 8
+// of them in flight (1 sequence in 32 buffers 3.7 us; 256 sequences of up to 8 accepted drafts in 32
+// buffers 16.7 us, 83 MB read and written at 5.0 TB/s, much of it in L2: from a cold L2 20 us and
+// 45 MB of HBM traffic, 2.2 TB/s, with 36 % of the issue slots used).  A CTA has 4 buffers, so that the
+// path's lookups are gone once for them.
 #include "pkv_common.cuh"
 #include "pkv_internal.h"
 

@@ -1667,9 +1667,14 @@ void make_tree_plan(const pkv_cache_desc* c, const pkv_attn_meta* m, int num_sms
   const int tiles = std::max((m->max_query_len + p->tile_toks - 1) / p->tile_toks, 1);
   // A worker is as many CTAs as there are row tiles: they share the keys' way through L2 (16
   // sequences of 16K to 32K keys with 2 tiles: 356 us, with a CTA a worker 456).  Of more than
-  // 8 tiles it takes 2 to 8 at a time, so that the last group is as full as can be (one
-  // sequence of 16000 keys, 19 tiles, us: 2 or 4 at a time, 20 in all, 155; 3 at a time, 21,
-  // 163; 8 at a time, 24, 179).
+  // 8 tiles it takes 2 to 8 at a time, the most that leave the fewest places of the last group
+  // empty (sequences of 8000 to 16000 keys, us: 9 tiles 3 at a time 89, 4 106; 19 tiles 5 at a time 165, 4 163,
+  // 2 167; 4 sequences of 38 tiles 2 at a time 585, 4 634).  One at a time would lose
+  // where there are few sequences (9 tiles 112, 19 tiles 196) and gain where there are many (16 of 4000
+  // keys, 19 tiles, 636 for 673).
+  // The longest tree makes the worker for all: of sequences with fewer tiles its other CTAs do nothing
+  // (100 sequences of 1 to 8 drafts x 4 heads over 500 to 4000 keys beside one of 8 drafts 154 us, of
+  // 64, two tiles, 231, of 256, eight tiles, 760).
   constexpr int kMaxTiles = 8;
   p->cta_tiles = std::min(tiles, kMaxTiles);
   auto padded = [&](int c) { return (tiles + c - 1) / c * c; };

@@ -20,8 +20,9 @@
 // (e4m3) widen codes.
 //
 // Bound by the keys' bytes (HBM): 64 sequences of 8 to 16 drafts over 128 to 4096 keys, 32 kv heads,
-// 335 us, 6.2 TB/s, 0.92 of the copy rate (query rows on M: 374); e4m3 by its steps' chain (64
-// sequences of 500 to 4000 keys, 8 kv heads, 16 rows 107 us, 2.6 TB/s; query rows on M: 165).
+// 336 us, 6.2 TB/s, 0.92 of the copy rate (query rows on M: 374); e4m3 by its steps' chain (64
+// sequences of 500 to 4000 keys, 8 kv heads, 16 rows 104 us, 2.6 TB/s, the shared-memory pipe 44 % and
+// the issue slots 27 % busy; query rows on M: 165).
 #include "pkv_tree_tc.cuh"
 
 namespace pkv {

@@ -31,8 +31,9 @@
 // the end.
 //
 // Measured (8 kv heads of 128): 8 sequences of 64 drafts over 2K to 8K keys, 32 q heads, 66 us,
-// 3.0 TB/s of keys; 16 of 26 drafts over 16K to 32K keys, 64 q heads, 355 us, 4.5 TB/s; one of 300
-// drafts over 16000 keys, 64 q heads, 155 us, 1.0 PFLOP/s.  A step takes 1.6 us a CTA, of
+// 3.0 TB/s of keys; 16 of 26 drafts over 16K to 32K keys, 64 q heads, 358 us, 4.4 TB/s (at 2070 MHz; 382 us
+// where the load lasts and the power limit brings the clock to 1770 MHz); one of 300
+// drafts over 16000 keys, 64 q heads, 165 us, 0.95 PFLOP/s.  A step takes 1.6 us a CTA, of
 // which the tensor core works 0.34: the way from S over the softmax warps to P bounds it.
 // e4m3, 128 sequences of 1 to 24 drafts over 64 to 8192 keys: 304 us, the same steps with half
 // the bytes.
